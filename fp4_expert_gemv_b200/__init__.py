@@ -31,6 +31,9 @@ FE_DEVICE_LOAD_TIMEOUT = 0x8
 FE_DEVICE_TC_TIMEOUT = 0x10
 
 PATH_AUTO, PATH_GEMV, PATH_TCGEN05, PATH_FUSED_DECODE, PATH_NVFP4 = 0, 1, 2, 3, 4
+DTYPE_BF16, DTYPE_F32 = 0, 1
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL, GATE_SIGMOID = 0, 1, 2, 3, 16
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_SILU, ACT_SWIGLU = 0, 1, 2, 3, 4
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is not built; run `python fp4_expert_gemv_b200/build.py`")
@@ -41,6 +44,15 @@ _P = ctypes.c_void_p
 _i32 = ctypes.c_int
 _i64 = ctypes.c_int64
 _st = ctypes.c_int
+_f32 = ctypes.c_float
+_sz = ctypes.c_size_t
+
+
+class BlockWeights(ctypes.Structure):
+    """fe_moe_block_t of include/fe_moe.h (device addresses)."""
+    _fields_ = [("w_pre", _P), ("w_router", _P), ("shared_gate_up", _P), ("shared_down", _P), ("shared_I", _i32),
+                ("w_post", _P), ("gate", _P), ("gate_kind", _i32), ("scale", _f32), ("w_next_pre", _P), ("eps", _f32)]
+
 
 _SIGS = {
     "fe_moe_create": (_st, [_i32, _i32, _i32, _i32, ctypes.POINTER(_P)]),
@@ -77,6 +89,19 @@ _SIGS = {
     "fe_moe_forward_router": (_st, [_P, _P, _P, _i32, _i32, _P, _P, _P]),
     "fe_moe_load_nvfp4": (_st, [_P, _P, _P, _P, _P, _i32, _P]),
     "fe_moe_nvfp4_quantize_device": (_st, [_P, _i64, _i64, _P, _P, _P, _P]),
+    "fe_moe_block_norm": (_st, [_P, _i32, _P, _P, _P, _i32, _f32, _P, _f32, _i64, _i32, _P, _P, _P]),
+    "fe_moe_block_norm_workspace": (_sz, [_i64, _i32]),
+    "fe_moe_block_norm_backward": (_st, [_P, _P, _P, _i32, _P, _P, _P, _i32, _f32, _P, _f32, _i64, _i32, _P, _P, _P, _P,
+                                         _P, _P, _sz, _P]),
+    "fe_moe_balance_workspace": (_sz, [_i64, _i32]),
+    "fe_moe_balance_loss": (_st, [_P, _P, _P, _i64, _i32, _i32, _f32, _f32, _P, _P, _P, _P, _sz, _P]),
+    "fe_moe_balance_loss_backward": (_st, [_P, _P, _P, _P, _P, _i64, _i32, _i32, _f32, _f32, _P, _i32, _P]),
+    "fe_moe_linear": (_st, [_P, _i64, _P, _P, _P, _i64, _i64, _i32, _i32, _i32, _P, _i64, _P, _P]),
+    "fe_moe_linear_workspace": (_sz, [_i64, _i32, _i32, _i32]),
+    "fe_moe_linear_backward": (_st, [_P, _i64, _P, _i64, _P, _P, _i64, _i32, _i32, _i32, _P, _i64, _P, _P, _P, _sz, _P]),
+    "fe_moe_get_op_status": (_st, [ctypes.POINTER(ctypes.c_uint32)]),
+    "fe_moe_forward_block_workspace": (_sz, [_P, _i32, _i32]),
+    "fe_moe_forward_block": (_st, [_P, ctypes.POINTER(BlockWeights), _P, _i32, _P, _i32, _i32, _P, _P, _P, _P, _sz, _P]),
 }
 
 for _name, (_res, _args) in _SIGS.items():
@@ -215,6 +240,48 @@ class MoELayer:
         check(fe_moe_forward_router(self.h, _dptr(x_bf16), _dptr(w_router_bf16), T, top_k, _dptr(y_bf16),
                                     _dptr(logits), _stream_ptr(stream)), "fe_moe_forward_router")
         return y_bf16, logits
+
+    def forward_block(self, r, top_k: int, w_router, w_pre=None, u_in=None, shared=None, w_post=None, gate=None,
+                      gate_kind=GATE_NONE, scale=1.0, w_next_pre=None, eps=1e-6, r_out=None, u_out=None, logits=None,
+                      stream=None):
+        """One block on the residual stream r [T, H] (bf16 or float32): norm (or u_in, the previous call's
+        u_out), router, routed experts, shared expert (shared = (gate_up [2 I_s, H], down [H, I_s]) or None),
+        norm, gate, residual, and the next block's norm.  Returns (r_out, u_out or None, logits)."""
+        if stream is not None:
+            with _on_stream(stream, r.device):
+                return self.forward_block(r, top_k, w_router, w_pre, u_in, shared, w_post, gate, gate_kind, scale,
+                                          w_next_pre, eps, r_out, u_out, logits)
+        import torch
+        bf, dev = torch.bfloat16, r.device
+        T, H = r.shape
+        dt = _dtype_of(r, "r")
+        _arg(r, "r", r.dtype, (T, self.H), dev)
+        _arg(w_router, "w_router", bf, (self.E, H), dev)
+        for name, t in (("w_pre", w_pre), ("w_post", w_post), ("w_next_pre", w_next_pre)):
+            _arg(t, name, bf, (H,), dev, optional=True)
+        _arg(u_in, "u_in", bf, (T, H), dev, optional=True)
+        _arg_gate(gate, gate_kind, T, H, dev)
+        Is = 0
+        if shared is not None:
+            Is = shared[1].shape[1]
+            _arg(shared[0], "shared gate_up", bf, (2 * Is, H), dev)
+            _arg(shared[1], "shared down", bf, (H, Is), dev)
+        r_out = _out(r_out, "r_out", r.dtype, (T, H), dev)
+        if w_next_pre is not None:
+            u_out = _out(u_out, "u_out", bf, (T, H), dev)
+        elif u_out is not None:
+            raise ValueError("u_out needs w_next_pre")
+        logits = _out(logits, "logits", torch.float32, (T, self.E), dev)
+        nb = fe_moe_forward_block_workspace(self.h, T, Is)
+        b = BlockWeights(_dptr(w_pre), _dptr(w_router), _dptr(shared[0]) if shared else None,
+                         _dptr(shared[1]) if shared else None, Is, _dptr(w_post), _dptr(gate), gate_kind, scale,
+                         _dptr(w_next_pre), eps)
+        with _device(dev):
+            ws = torch.empty(max(nb, 16), dtype=torch.uint8, device=dev)
+            check(fe_moe_forward_block(self.h, ctypes.byref(b), _dptr(r), dt, _dptr(u_in), T, top_k, _dptr(r_out),
+                                       _dptr(u_out), _dptr(logits), _dptr(ws), ws.numel(), _stream_ptr(None)),
+                  "fe_moe_forward_block")
+        return r_out, u_out, logits
 
     def forward_host(self, x_bf16_host, logits_host, top_k: int, y_bf16_host, stream=None):
         """Host (ideally pinned) numpy/torch CPU buffers in and out; synchronous."""
@@ -390,3 +457,262 @@ def pack_device(W, codes=None, scales=None, stream=None):
     check(fe_moe_pack_device(_dptr(W), E, K, N, _dptr(codes), _dptr(scales), _stream_ptr(stream)),
           "fe_moe_pack_device")
     return codes, scales
+
+
+# ---- the operators around the experts ---------------------------------------------------
+# Torch CUDA tensors in and out; outputs that are not given are allocated.  `stream` (a torch
+# stream or an address) makes the call, its allocations included, on that stream; otherwise it
+# runs on the current stream of the tensors' device.
+
+
+class _Nothing:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *_):
+        return False
+
+
+_NOTHING = _Nothing()
+
+
+def _device(dev):
+    import torch
+    return _NOTHING if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _on_stream(stream, dev):
+    """The stream made current, so that what the call allocates belongs to it."""
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev)
+    if stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    return torch.cuda.stream(stream)
+
+
+def _arg(t, name, dtype, shape, dev, optional=False):
+    if t is None:
+        if optional:
+            return
+        raise ValueError(f"{name} is needed")
+    if t.dtype != dtype or tuple(t.shape) != shape or t.device != dev or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} CUDA tensor of shape {shape} on {dev} is needed, "
+                         f"got {t.dtype} {tuple(t.shape)} strides {tuple(t.stride())} on {t.device}")
+
+
+def _arg_rows(t, name, dtype, shape, dev):
+    """A matrix whose rows are contiguous; returns its row stride."""
+    if (t.dtype != dtype or tuple(t.shape) != shape or t.device != dev or not t.is_cuda
+            or (shape[1] > 1 and shape[0] > 0 and t.stride(1) != 1)):
+        raise ValueError(f"{name}: a {dtype} CUDA matrix of shape {shape} on {dev} with contiguous rows is needed, "
+                         f"got {t.dtype} {tuple(t.shape)} strides {tuple(t.stride())} on {t.device}")
+    if shape[0] <= 1:
+        return (shape[1] + 7) // 8 * 8
+    if t.stride(0) < shape[1]:
+        raise ValueError(f"{name}: rows overlap (strides {tuple(t.stride())})")
+    return t.stride(0)
+
+
+def _arg_gate(gate, kind, T, H, dev):
+    import torch
+    k = kind & ~GATE_SIGMOID
+    if k not in (GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL) or (gate is None) != (k == GATE_NONE):
+        raise ValueError("gate and gate_kind do not go together")
+    if gate is not None:
+        _arg(gate, "gate", torch.bfloat16, {GATE_CHANNEL: (H,), GATE_TOKEN: (T,), GATE_FULL: (T, H)}[k], dev)
+
+
+def _out(t, name, dtype, shape, dev):
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _arg(t, name, dtype, shape, dev)
+    return t
+
+
+def _dtype_of(t, name):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return DTYPE_BF16
+    if t.dtype == torch.float32:
+        return DTYPE_F32
+    raise ValueError(f"{name}: bfloat16 or float32 is needed, got {t.dtype}")
+
+
+def block_norm(r, y=None, w_post=None, w_pre=None, gate=None, gate_kind=GATE_NONE, scale=1.0, eps=1e-6, r_out=None,
+               u=None, stream=None):
+    """r' = r + scale * a(gate) * w_post * y / rms(y) and u = w_pre * r' / rms(r') in one pass
+    (fe_moe_block_norm).  r [T, H] bf16 or float32, the rest bf16.  Returns (r', u): None for what
+    was not asked for (r' without y, u without w_pre)."""
+    if stream is not None:
+        with _on_stream(stream, r.device):
+            return block_norm(r, y, w_post, w_pre, gate, gate_kind, scale, eps, r_out, u)
+    import torch
+    bf, dev = torch.bfloat16, r.device
+    T, H = r.shape
+    dt = _dtype_of(r, "r")
+    _arg(r, "r", r.dtype, (T, H), dev)
+    _arg(y, "y", bf, (T, H), dev, optional=True)
+    _arg(w_post, "w_post", bf, (H,), dev, optional=True)
+    _arg(w_pre, "w_pre", bf, (H,), dev, optional=True)
+    _arg_gate(gate, gate_kind, T, H, dev)
+    if y is not None:
+        r_out = _out(r_out, "r_out", r.dtype, (T, H), dev)
+    if w_pre is not None:
+        u = _out(u, "u", bf, (T, H), dev)
+    with _device(dev):
+        check(fe_moe_block_norm(_dptr(r), dt, _dptr(y), _dptr(w_post), _dptr(gate), gate_kind, scale, _dptr(w_pre), eps,
+                                T, H, _dptr(r_out), _dptr(u), _stream_ptr(None)), "fe_moe_block_norm")
+    return r_out, u
+
+
+def block_norm_backward(dr_out, du, r, y=None, w_post=None, w_pre=None, gate=None, gate_kind=GATE_NONE, scale=1.0,
+                        eps=1e-6, weight_grads=True, stream=None):
+    """The gradients of block_norm: (dr, dy, dgate, dw_post, dw_pre), None for an operand that is None.
+    dr_out (like r) or du (bf16) may be None for no gradient.  dgate is float32 for a channel or
+    token gate, bf16 for a full one; dw_post and dw_pre are float32.  weight_grads=False leaves
+    out dw_post, dw_pre and a channel dgate."""
+    if stream is not None:
+        with _on_stream(stream, r.device):
+            return block_norm_backward(dr_out, du, r, y, w_post, w_pre, gate, gate_kind, scale, eps, weight_grads)
+    import torch
+    bf, f32, dev = torch.bfloat16, torch.float32, r.device
+    T, H = r.shape
+    dt = _dtype_of(r, "r")
+    _arg(r, "r", r.dtype, (T, H), dev)
+    _arg(dr_out, "dr_out", r.dtype, (T, H), dev, optional=True)
+    _arg(du, "du", bf, (T, H), dev, optional=True)
+    _arg(y, "y", bf, (T, H), dev, optional=True)
+    _arg(w_post, "w_post", bf, (H,), dev, optional=True)
+    _arg(w_pre, "w_pre", bf, (H,), dev, optional=True)
+    _arg_gate(gate, gate_kind, T, H, dev)
+    kind = gate_kind & ~GATE_SIGMOID
+    dr = torch.empty((T, H), dtype=r.dtype, device=dev)
+    dy = torch.empty((T, H), dtype=bf, device=dev) if y is not None else None
+    dgate = None
+    if kind == GATE_FULL:
+        dgate = torch.empty((T, H), dtype=bf, device=dev)
+    elif kind == GATE_TOKEN or (kind == GATE_CHANNEL and weight_grads):
+        dgate = torch.empty((T,) if kind == GATE_TOKEN else (H,), dtype=f32, device=dev)
+    dw_post = torch.empty((H,), dtype=f32, device=dev) if w_post is not None and weight_grads else None
+    dw_pre = torch.empty((H,), dtype=f32, device=dev) if w_pre is not None and weight_grads else None
+    ws, nb = None, 0
+    if dw_post is not None or dw_pre is not None or (kind == GATE_CHANNEL and dgate is not None):
+        nb = fe_moe_block_norm_workspace(T, H)
+        ws = torch.empty(max(nb, 1), dtype=torch.uint8, device=dev)
+    with _device(dev):
+        check(fe_moe_block_norm_backward(_dptr(dr_out), _dptr(du), _dptr(r), dt, _dptr(y), _dptr(w_post), _dptr(gate),
+                                         gate_kind, scale, _dptr(w_pre), eps, T, H, _dptr(dr), _dptr(dy), _dptr(dgate),
+                                         _dptr(dw_post), _dptr(dw_pre), _dptr(ws), nb, _stream_ptr(None)),
+              "fe_moe_block_norm_backward")
+    return dr, dy, dgate, dw_post, dw_pre
+
+
+def balance_loss(logits, idx, mask=None, balance_coef=1.0, z_coef=0.0, loss=None, counts=None, n_tokens=None,
+                 stream=None):
+    """The router's balance loss: logits float32 [T, E], idx int32 [T, k], mask uint8 [T] (0 = padding).
+    Returns (float32 [3]: loss, balance, z; int32 [E] counts; int32 [1] kept tokens)."""
+    if stream is not None:
+        with _on_stream(stream, logits.device):
+            return balance_loss(logits, idx, mask, balance_coef, z_coef, loss, counts, n_tokens)
+    import torch
+    i32, f32, dev = torch.int32, torch.float32, logits.device
+    T, E = logits.shape
+    k = idx.shape[1]
+    _arg(logits, "logits", f32, (T, E), dev)
+    _arg(idx, "idx", i32, (T, k), dev)
+    _arg(mask, "mask", torch.uint8, (T,), dev, optional=True)
+    loss = _out(loss, "loss", f32, (3,), dev)
+    counts = _out(counts, "counts", i32, (E,), dev)
+    n_tokens = _out(n_tokens, "n_tokens", i32, (1,), dev)
+    nb = fe_moe_balance_workspace(T, E)
+    ws = torch.empty(max(nb, 1), dtype=torch.uint8, device=dev)
+    with _device(dev):
+        check(fe_moe_balance_loss(_dptr(logits), _dptr(idx), _dptr(mask), T, E, k, balance_coef, z_coef, _dptr(loss),
+                                  _dptr(counts), _dptr(n_tokens), _dptr(ws), nb, _stream_ptr(None)),
+              "fe_moe_balance_loss")
+    return loss, counts, n_tokens
+
+
+def balance_loss_backward(logits, counts, n_tokens, top_k: int, mask=None, dloss=None, balance_coef=1.0, z_coef=0.0,
+                          dlogits=None, dtype=None, stream=None):
+    """dloss/dlogits [T, E] of balance_loss (float32, or bf16 with dtype=torch.bfloat16), times dloss
+    (float32 [1] on the device, None = 1); counts and n_tokens as balance_loss returned them."""
+    if stream is not None:
+        with _on_stream(stream, logits.device):
+            return balance_loss_backward(logits, counts, n_tokens, top_k, mask, dloss, balance_coef, z_coef, dlogits, dtype)
+    import torch
+    f32, dev = torch.float32, logits.device
+    T, E = logits.shape
+    _arg(logits, "logits", f32, (T, E), dev)
+    _arg(counts, "counts", torch.int32, (E,), dev)
+    _arg(n_tokens, "n_tokens", torch.int32, (1,), dev)
+    _arg(mask, "mask", torch.uint8, (T,), dev, optional=True)
+    _arg(dloss, "dloss", f32, (1,), dev, optional=True)
+    dlogits = _out(dlogits, "dlogits", dtype or (f32 if dlogits is None else dlogits.dtype), (T, E), dev)
+    dt = _dtype_of(dlogits, "dlogits")
+    with _device(dev):
+        check(fe_moe_balance_loss_backward(_dptr(logits), _dptr(counts), _dptr(n_tokens), _dptr(mask), _dptr(dloss), T, E,
+                                           top_k, balance_coef, z_coef, _dptr(dlogits), dt, _stream_ptr(None)),
+              "fe_moe_balance_loss_backward")
+    return dlogits
+
+
+def linear(x, w, bias=None, act=ACT_NONE, residual=None, y=None, z=None, stream=None):
+    """y = act(x w^T + bias) + residual on bf16 matrices: x [M, K], w [N, K], bias [N]; residual and y
+    [M, N] ([M, N / 2] for ACT_SWIGLU).  The rows of x, residual and y may be strided; y may be the
+    residual.  z [M, N], if given, receives the pre-activation for linear_backward."""
+    if stream is not None:
+        with _on_stream(stream, x.device):
+            return linear(x, w, bias, act, residual, y, z)
+    import torch
+    bf, dev = torch.bfloat16, x.device
+    M, K = x.shape
+    N = w.shape[0]
+    cols = N // 2 if act == ACT_SWIGLU else N
+    ldx = _arg_rows(x, "x", bf, (M, K), dev)
+    _arg(w, "w", bf, (N, K), dev)
+    _arg(bias, "bias", bf, (N,), dev, optional=True)
+    _arg(z, "z", bf, (M, N), dev, optional=True)
+    ldr = 0 if residual is None else _arg_rows(residual, "residual", bf, (M, cols), dev)
+    if y is None:
+        y = torch.empty((M, cols), dtype=bf, device=dev)
+    ldy = _arg_rows(y, "y", bf, (M, cols), dev)
+    with _device(dev):
+        check(fe_moe_linear(_dptr(x), ldx, _dptr(w), _dptr(bias), _dptr(residual), ldr, M, N, K, act, _dptr(y), ldy,
+                            _dptr(z), _stream_ptr(None)), "fe_moe_linear")
+    return y
+
+
+def linear_backward(dy, x, w, z=None, act=ACT_NONE, need_dx=True, need_dw=True, need_db=True, stream=None):
+    """The gradients of linear: (dx bf16 [M, K], dw bf16 [N, K], db float32 [N]), None for what is not
+    needed; z is the pre-activation that linear wrote.  The residual's gradient is dy."""
+    if stream is not None:
+        with _on_stream(stream, x.device):
+            return linear_backward(dy, x, w, z, act, need_dx, need_dw, need_db)
+    import torch
+    bf, dev = torch.bfloat16, x.device
+    M, K = x.shape
+    N = w.shape[0]
+    cols = N // 2 if act == ACT_SWIGLU else N
+    ldx = _arg_rows(x, "x", bf, (M, K), dev)
+    _arg(w, "w", bf, (N, K), dev)
+    _arg(z, "z", bf, (M, N), dev, optional=act == ACT_NONE)
+    lddy = _arg_rows(dy, "dy", bf, (M, cols), dev)
+    dx = torch.empty((M, K), dtype=bf, device=dev) if need_dx else None
+    dw = torch.empty((N, K), dtype=bf, device=dev) if need_dw else None
+    db = torch.empty((N,), dtype=torch.float32, device=dev) if need_db else None
+    nb = fe_moe_linear_workspace(M, N, K, act)
+    ws = torch.empty(max(nb, 16), dtype=torch.uint8, device=dev)
+    with _device(dev):
+        check(fe_moe_linear_backward(_dptr(dy), lddy, _dptr(x), ldx, _dptr(w), _dptr(z), M, N, K, act, _dptr(dx), K,
+                                     _dptr(dw), _dptr(db), _dptr(ws), nb, _stream_ptr(None)), "fe_moe_linear_backward")
+    return dx, dw, db
+
+
+def op_status():
+    """(status, bits) of the operators around the experts on the current device since the last query."""
+    bits = ctypes.c_uint32(0)
+    st = fe_moe_get_op_status(ctypes.byref(bits))
+    return st, bits.value

@@ -24,7 +24,7 @@ LIB_SYNTH = os.path.join(ROOT, "synth", "libfe_synth.so")
 
 
 def _sources_moe():
-    return ([os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith((".cu", ".cpp", ".cuh"))]
+    return ([os.path.join(CSRC, f) for f in sorted(os.listdir(CSRC)) if f.endswith((".cu", ".cpp", ".cuh", ".h"))]
             + [os.path.join(ROOT, "include", "fe_moe.h")])
 
 
@@ -46,7 +46,7 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> None:
     if force or _stale(LIB_MOE, deps):
         tmp = LIB_MOE + f".{os.getpid()}.tmp"
         _run([NVCC, *ARCH, *COMMON, *extra, "-I", os.path.join(ROOT, "include"), "-o", tmp,
-              os.path.join(CSRC, "fe_moe.cu"), os.path.join(CSRC, "pack_host.cpp")])
+              os.path.join(CSRC, "fe_moe.cu"), os.path.join(CSRC, "fe_block.cu"), os.path.join(CSRC, "pack_host.cpp")])
         os.replace(tmp, LIB_MOE)
     src = os.path.join(ROOT, "synth", "synth.cu")
     if force or _stale(LIB_SYNTH, [src]):

@@ -1,0 +1,736 @@
+// Entry points of the operators around the expert layer: the block's norms with gate and residual,
+// the router's balance loss, and the dense product with its epilogue.  They need no handle: the
+// caller passes every buffer, workspace included, and they run on the current device.  The
+// declarations and the contract of every entry point are in include/fe_moe.h.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <type_traits>
+
+#include "../../include/fe_moe.h"
+#include "balance.cuh"
+#include "common.cuh"
+#include "host.h"
+#include "linear.cuh"
+#include "norm.cuh"
+
+using fe_host::record_cuda;
+
+namespace {
+
+#define FE_CUDA_TRY(expr)                                 \
+    do {                                                  \
+        cudaError_t err__ = (expr);                       \
+        if (err__ != cudaSuccess) return record_cuda(err__, #expr); \
+    } while (0)
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// Whether [a, a + na) and [b, b + nb) share a byte; null ranges share none.
+bool overlap(const void* a, size_t na, const void* b, size_t nb)
+{
+    if (!a || !b || na == 0 || nb == 0) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// SMs of the current device (looked up once per device).
+int sm_count()
+{
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        known[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+// The workspace sizes must not depend on the device that is current when they are asked for.
+constexpr int kMaxPartials = 512;
+
+// Every kernel here begins with griddepcontrol.wait, so its launch may overlap the tail of the
+// kernel before it on the stream.
+template <typename... KArgs, typename... Args>
+cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const Args&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// ---- norms ------------------------------------------------------------------------------
+
+// Threads of a row: 8 elements each, as many as cover the row, from one warp to 1024.
+int norm_threads(int H, int chunk)
+{
+    int tpr = 32;
+    while (tpr < 1024 && tpr * 8 * chunk < H) tpr *= 2;
+    return tpr;
+}
+
+size_t dtype_bytes(int dt) { return dt == FE_DTYPE_F32 ? 4 : 2; }
+
+bool gate_ok(int kind)
+{
+    const int k = kind & ~FE_GATE_SIGMOID;
+    return (k == FE_GATE_NONE && kind == FE_GATE_NONE) || k == FE_GATE_CHANNEL || k == FE_GATE_TOKEN || k == FE_GATE_FULL;
+}
+
+size_t gate_elems(int kind, int64_t T, int H)
+{
+    switch (kind & ~FE_GATE_SIGMOID) {
+        case FE_GATE_CHANNEL: return (size_t)H;
+        case FE_GATE_TOKEN: return (size_t)T;
+        case FE_GATE_FULL: return (size_t)T * H;
+    }
+    return 0;
+}
+
+// What both directions need of the forward's operands.
+fe_status check_norm_operands(const void* r, int r_dtype, const void* y, const void* w_post, const void* gate,
+                              int gate_kind, const void* w_pre, float eps, int64_t T, int H)
+{
+    if (T < 0 || H < 1 || (r_dtype != FE_DTYPE_BF16 && r_dtype != FE_DTYPE_F32) || !gate_ok(gate_kind) ||
+        !(eps > 0.0f) || std::isinf(eps))
+        return FE_ERR_INVALID_ARG;
+    if (T > 0 && (gate_kind == FE_GATE_NONE) != (gate == nullptr)) return FE_ERR_INVALID_ARG;
+    if (T > 0 && !y && (w_post || gate)) return FE_ERR_INVALID_ARG;
+    if (!aligned(r, r_dtype == FE_DTYPE_F32 ? 4 : 2) || !aligned(y, 2) || !aligned(w_post, 2) || !aligned(gate, 2) ||
+        !aligned(w_pre, 2))
+        return FE_ERR_INVALID_ARG;
+    if (H > fe::kNormMaxH || T > INT32_MAX) return FE_ERR_UNSUPPORTED;
+    return FE_OK;
+}
+
+fe::NormParams norm_params(const void* r, const void* y, const void* w_post, const void* gate, int gate_kind, float scale,
+                           const void* w_pre, float eps, int64_t T, int H)
+{
+    fe::NormParams p{};
+    p.r = r;
+    p.y = static_cast<const uint16_t*>(y);
+    p.w_post = static_cast<const uint16_t*>(w_post);
+    p.gate = static_cast<const uint16_t*>(gate);
+    p.gate_kind = gate_kind & ~FE_GATE_SIGMOID;
+    p.gate_sigmoid = (gate_kind & FE_GATE_SIGMOID) != 0;
+    p.scale = scale;
+    p.w_pre = static_cast<const uint16_t*>(w_pre);
+    p.eps = eps;
+    p.T = T;
+    p.H = H;
+    return p;
+}
+
+// 16-byte accesses need a row length of whole chunks and every row pointer aligned.
+bool norm_vec(const fe::NormParams& p)
+{
+    return p.H % 8 == 0 && aligned(p.r, 16) && aligned(p.y, 16) && aligned(p.w_post, 16) && aligned(p.w_pre, 16) &&
+           (p.gate_kind == FE_GATE_TOKEN || aligned(p.gate, 16)) && aligned(p.r_out, 16) && aligned(p.u, 16);
+}
+
+template <int C>
+cudaError_t norm_launch(const fe::NormParams& p, bool r32, int tpr, cudaStream_t s)
+{
+    const int threads = std::max(tpr, 128);
+    const dim3 grid((unsigned)((p.T + threads / tpr - 1) / (threads / tpr)));
+    if (norm_vec(p))
+        return r32 ? launch(fe::block_norm_kernel<8, C, true>, grid, threads, 0, s, p, tpr)
+                   : launch(fe::block_norm_kernel<8, C, false>, grid, threads, 0, s, p, tpr);
+    return r32 ? launch(fe::block_norm_kernel<1, C, true>, grid, threads, 0, s, p, tpr)
+               : launch(fe::block_norm_kernel<1, C, false>, grid, threads, 0, s, p, tpr);
+}
+
+// Shape of the backward launch: threads per row, threads per CTA, CTAs.
+struct NormBwdPlan {
+    int tpr, chunk, threads, grid;
+    int64_t rows_per_cta;
+    size_t smem;
+};
+
+NormBwdPlan norm_bwd_plan(int64_t T, int H, int sms)
+{
+    NormBwdPlan b;
+    b.chunk = H <= 8192 ? 1 : 2;
+    b.tpr = norm_threads(H, b.chunk);
+    b.threads = std::max(b.tpr, 512);
+    const int groups = b.threads / b.tpr;
+    const int64_t want = std::min<int64_t>(std::min(kMaxPartials, 2 * sms), (T + groups - 1) / groups);
+    const int64_t per = std::max<int64_t>(1, (T + want - 1) / std::max<int64_t>(want, 1));
+    b.rows_per_cta = (per + groups - 1) / groups * groups;
+    b.grid = (int)((T + b.rows_per_cta - 1) / b.rows_per_cta);
+    b.smem = groups > 1 ? sizeof(float) * 3 * H : 0;
+    return b;
+}
+
+template <int C, int MAXT>
+cudaError_t norm_bwd_launch(const fe::NormBwdParams& q, bool vec, bool r32, const NormBwdPlan& b, cudaStream_t s)
+{
+    if (vec)
+        return r32 ? launch(fe::block_norm_backward_kernel<8, C, true, MAXT>, b.grid, b.threads, b.smem, s, q, b.tpr)
+                   : launch(fe::block_norm_backward_kernel<8, C, false, MAXT>, b.grid, b.threads, b.smem, s, q, b.tpr);
+    return r32 ? launch(fe::block_norm_backward_kernel<1, C, true, MAXT>, b.grid, b.threads, b.smem, s, q, b.tpr)
+               : launch(fe::block_norm_backward_kernel<1, C, false, MAXT>, b.grid, b.threads, b.smem, s, q, b.tpr);
+}
+
+// ---- balance loss -------------------------------------------------------------------------
+
+int balance_ctas(int64_t T) { return (int)std::max<int64_t>(1, std::min<int64_t>(kMaxPartials, (T + fe::kBalWarps - 1) / fe::kBalWarps)); }
+
+fe_status check_balance(const float* logits, const uint8_t*, int64_t T, int E, int top_k)
+{
+    if (T < 0 || E < 1 || top_k < 1 || top_k > E || (T > 0 && !logits) || !aligned(logits, 4)) return FE_ERR_INVALID_ARG;
+    if (E > fe::kBalMaxE || T > INT32_MAX / top_k) return FE_ERR_UNSUPPORTED;
+    return FE_OK;
+}
+
+template <int NPL>
+cudaError_t balance_launch(const fe::BalanceParams& p, bool backward, int grid, bool vec, cudaStream_t s)
+{
+    if constexpr (NPL >= 4) {
+        if (vec)
+            return backward ? launch(fe::balance_backward_kernel<NPL, 4>, grid, fe::kBalThreads, 0, s, p)
+                            : launch(fe::balance_kernel<NPL, 4>, grid, fe::kBalThreads, 0, s, p);
+    }
+    return backward ? launch(fe::balance_backward_kernel<NPL, 1>, grid, fe::kBalThreads, 0, s, p)
+                    : launch(fe::balance_kernel<NPL, 1>, grid, fe::kBalThreads, 0, s, p);
+}
+
+cudaError_t balance_dispatch(const fe::BalanceParams& p, bool backward, int grid, bool vec, cudaStream_t s)
+{
+    if (p.E <= 32) return balance_launch<1>(p, backward, grid, vec, s);
+    if (p.E <= 64) return balance_launch<2>(p, backward, grid, vec, s);
+    if (p.E <= 128) return balance_launch<4>(p, backward, grid, vec, s);
+    if (p.E <= 256) return balance_launch<8>(p, backward, grid, vec, s);
+    if (p.E <= 512) return balance_launch<16>(p, backward, grid, vec, s);
+    return balance_launch<32>(p, backward, grid, vec, s);
+}
+
+// ---- dense product --------------------------------------------------------------------------
+
+constexpr int kLinRowsMax = 8;   // rows that stream the weights without tensor cores
+
+bool act_ok(int act, int N) { return act >= FE_ACT_NONE && act <= FE_ACT_SWIGLU && (act != FE_ACT_SWIGLU || N % 2 == 0); }
+int out_cols(int act, int N) { return act == FE_ACT_SWIGLU ? N / 2 : N; }
+
+// Bytes that M rows of `cols` bf16 with stride ld span.
+size_t span(int64_t M, int64_t ld, int64_t cols) { return M > 0 ? 2 * ((size_t)(M - 1) * ld + cols) : 0; }
+
+fe_status check_linear_shape(int64_t M, int N, int K, int act)
+{
+    if (M < 0 || N < 1 || K < 1 || !act_ok(act, N)) return FE_ERR_INVALID_ARG;
+    // TMA rows are multiples of 16 bytes; tile counts and coordinates are 32-bit
+    if (K % 8 != 0 || M > INT32_MAX - 256 || N > INT32_MAX - 256 || K > INT32_MAX - 256 ||
+        (M / fe::kLinM + 1) * (int64_t)(N / 128 + 1) > INT32_MAX / 2)
+        return FE_ERR_UNSUPPORTED;
+    return FE_OK;
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn()
+{
+    static EncodeFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
+}
+
+// Map over a bf16 matrix [rows][cols] with row stride ld (elements): boxes of 64 x 64, 128-byte
+// swizzle, zeros outside.
+cudaError_t tensor_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld)
+{
+    EncodeFn fn = encode_fn();
+    if (!fn) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)(rows > 1 ? ld : (cols + 7) / 8 * 8) * 2};
+    const cuuint32_t box[2] = {64, 64}, es[2] = {1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+struct Matrix {
+    const void* p;
+    int64_t rows, cols, ld;
+};
+
+// D [M][N] = A B^T.  a_mn: A is stored [K][M]; b_mn: B is stored [K][N].
+cudaError_t lin_problem(fe::LinProblem* p, const Matrix& a, bool a_mn, const Matrix& b, bool b_mn, int M, int N, int K)
+{
+    *p = fe::LinProblem{};
+    p->M = M;
+    p->N = N;
+    p->K = K;
+    p->a_mn = a_mn;
+    p->b_mn = b_mn;
+    p->cols = N;
+    cudaError_t e = tensor_map(&p->ta, a.p, a.rows, a.cols, a.ld);
+    if (e == cudaSuccess) e = tensor_map(&p->tb, b.p, b.rows, b.cols, b.ld);
+    return e;
+}
+
+void lin_tiles(fe::LinProblem* p, int BN)
+{
+    p->tiles_m = (p->M + fe::kLinM - 1) / fe::kLinM;
+    const int w = p->act == FE_ACT_SWIGLU ? BN / 2 : BN;
+    p->tiles_n = (p->cols + w - 1) / w;
+}
+
+template <int BN>
+cudaError_t lin_launch(const fe::LinParams& P, int sms, cudaStream_t s)
+{
+    static std::atomic<bool> ready[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !ready[dev].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(fe::linear_gemm_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)fe::lin_smem_bytes(BN));
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_relaxed);
+    }
+    return launch(fe::linear_gemm_kernel<BN>, std::min(P.tiles, sms), fe::kLinThreads, fe::lin_smem_bytes(BN), s, P);
+}
+
+// The tile width: with 256 columns a k step moves the fewest bytes per product, with 128 there are
+// more tiles to spread; the one whose longest-loaded SM has less to do runs.
+cudaError_t lin_run(fe::LinParams& P, int n, cudaStream_t s)
+{
+    const int sms = sm_count();
+    if (sms < 1) return cudaErrorInvalidDevice;
+    int64_t work[2];
+    for (int w = 0; w < 2; ++w) {
+        int64_t tiles = 0;
+        for (int i = 0; i < n; ++i) {
+            lin_tiles(&P.p[i], w ? 256 : 128);
+            tiles += (int64_t)P.p[i].tiles_m * P.p[i].tiles_n;
+        }
+        work[w] = (tiles + sms - 1) / sms * (w ? 2 : 1);
+    }
+    const int BN = work[1] <= work[0] ? 256 : 128;
+    for (int i = 0; i < n; ++i) lin_tiles(&P.p[i], BN);
+    P.tiles0 = P.p[0].tiles_m * P.p[0].tiles_n;
+    P.tiles = P.tiles0 + (n > 1 ? P.p[1].tiles_m * P.p[1].tiles_n : 0);
+    return BN == 256 ? lin_launch<256>(P, sms, s) : lin_launch<128>(P, sms, s);
+}
+
+template <bool GLU>
+cudaError_t rows_launch(const fe::LinRowsParams& p, cudaStream_t s)
+{
+    const int grid = (p.cols + fe::kLinRowsWarps - 1) / fe::kLinRowsWarps, block = 32 * fe::kLinRowsWarps;
+    if (p.M == 1) return launch(fe::linear_rows_kernel<1, GLU>, grid, block, 0, s, p);
+    if (p.M == 2) return launch(fe::linear_rows_kernel<2, GLU>, grid, block, 0, s, p);
+    if (p.M <= 4) return launch(fe::linear_rows_kernel<4, GLU>, grid, block, 0, s, p);
+    return launch(fe::linear_rows_kernel<8, GLU>, grid, block, 0, s, p);
+}
+
+// Backward workspace: dz [M][roundup8(N)] bf16, then the column partials.
+int dz_chunks(int64_t M) { return (int)std::max<int64_t>(1, std::min<int64_t>(64, (M + 31) / 32)); }
+
+}  // namespace
+
+namespace fe_host {
+
+fe_status check_block_norm(const void* r, int r_dtype, const void* y, const void* w_post, const void* gate,
+                           int gate_kind, const void* w_pre, float eps, int64_t T, int H, const void* r_out,
+                           const void* u)
+{
+    const fe_status st = check_norm_operands(r, r_dtype, y, w_post, gate, gate_kind, w_pre, eps, T, H);
+    if (st != FE_OK) return st;
+    if (T == 0) return FE_OK;
+    if ((u != nullptr) != (w_pre != nullptr) || (r_out && !y) || (!r_out && !u)) return FE_ERR_INVALID_ARG;
+    if (!r || !aligned(r_out, r_dtype == FE_DTYPE_F32 ? 4 : 2) || !aligned(u, 2)) return FE_ERR_INVALID_ARG;
+    // r_out may be r itself; no other output may touch an operand or the other output
+    const size_t nr = (size_t)T * H * dtype_bytes(r_dtype), nb = (size_t)T * H * 2, nw = (size_t)H * 2;
+    const size_t ng = 2 * gate_elems(gate_kind, T, H);
+    const void* outs[2] = {r_out, u};
+    const size_t ns[2] = {nr, nb};
+    for (int i = 0; i < 2; ++i) {
+        if (outs[i] != r && overlap(outs[i], ns[i], r, nr)) return FE_ERR_INVALID_ARG;
+        if (i == 1 && outs[i] && outs[i] == r) return FE_ERR_INVALID_ARG;
+        if (overlap(outs[i], ns[i], y, nb) || overlap(outs[i], ns[i], gate, ng) || overlap(outs[i], ns[i], w_post, nw) ||
+            overlap(outs[i], ns[i], w_pre, nw))
+            return FE_ERR_INVALID_ARG;
+    }
+    if (overlap(r_out, nr, u, nb)) return FE_ERR_INVALID_ARG;
+    return FE_OK;
+}
+
+fe_status check_linear(const void* x, int64_t ldx, const void* w, const void* bias, const void* residual, int64_t ldr,
+                       int64_t M, int N, int K, int act, const void* y, int64_t ldy, const void* z)
+{
+    const fe_status st = check_linear_shape(M, N, K, act);
+    if (st != FE_OK) return st;
+    const int cols = out_cols(act, N);
+    if (M == 0) return FE_OK;
+    if (!x || !w || !y || ldx < K || ldy < cols || (residual && ldr < cols)) return FE_ERR_INVALID_ARG;
+    if (ldx % 8 != 0) return FE_ERR_UNSUPPORTED;
+    if (!aligned(x, 16) || !aligned(w, 16) || !aligned(bias, 2) || !aligned(residual, 2) || !aligned(y, 2) ||
+        !aligned(z, 2))
+        return FE_ERR_INVALID_ARG;
+    const size_t ny = span(M, ldy, cols), nz = 2 * (size_t)M * N, nx = span(M, ldx, K), nw = 2 * (size_t)N * K;
+    const size_t nres = span(M, ldr, cols), nbias = 2 * (size_t)N;
+    if (overlap(y, ny, x, nx) || overlap(y, ny, w, nw) || overlap(y, ny, bias, nbias) || overlap(y, ny, z, nz) ||
+        overlap(z, nz, x, nx) || overlap(z, nz, w, nw) || overlap(z, nz, bias, nbias) || overlap(z, nz, residual, nres))
+        return FE_ERR_INVALID_ARG;
+    // y may be the residual itself (the sum in place), not a shifted view of it
+    if (overlap(y, ny, residual, nres) && (y != residual || ldy != ldr)) return FE_ERR_INVALID_ARG;
+    return FE_OK;
+}
+
+}  // namespace fe_host
+
+extern "C" {
+
+fe_status fe_moe_block_norm(const void* r, int r_dtype, const void* y, const void* w_post, const void* gate,
+                            int gate_kind, float scale, const void* w_pre, float eps, int64_t T, int H, void* r_out,
+                            void* u, fe_stream_t stream)
+{
+    const fe_status st =
+        fe_host::check_block_norm(r, r_dtype, y, w_post, gate, gate_kind, w_pre, eps, T, H, r_out, u);
+    if (st != FE_OK) return st;
+    if (T == 0) return FE_OK;
+    fe::NormParams p = norm_params(r, y, w_post, gate, gate_kind, scale, w_pre, eps, T, H);
+    p.r_out = r_out;
+    p.u = static_cast<uint16_t*>(u);
+    const bool r32 = r_dtype == FE_DTYPE_F32;
+    const cudaStream_t s = (cudaStream_t)stream;
+    FE_CUDA_TRY(H <= 8192 ? norm_launch<1>(p, r32, norm_threads(H, 1), s) : norm_launch<2>(p, r32, norm_threads(H, 2), s));
+    return FE_OK;
+}
+
+size_t fe_moe_block_norm_workspace(int64_t T, int H)
+{
+    if (T < 0 || H < 1 || H > fe::kNormMaxH) return 0;
+    return sizeof(float) * 3 * (size_t)H * (size_t)std::min<int64_t>(kMaxPartials, std::max<int64_t>(T, 1));
+}
+
+fe_status fe_moe_block_norm_backward(const void* dr_out, const void* du, const void* r, int r_dtype, const void* y,
+                                     const void* w_post, const void* gate, int gate_kind, float scale,
+                                     const void* w_pre, float eps, int64_t T, int H, void* dr, void* dy, void* dgate,
+                                     float* dw_post, float* dw_pre, void* workspace, size_t workspace_bytes,
+                                     fe_stream_t stream)
+{
+    fe_status st = check_norm_operands(r, r_dtype, y, w_post, gate, gate_kind, w_pre, eps, T, H);
+    if (st != FE_OK) return st;
+    const int kind = gate_kind & ~FE_GATE_SIGMOID;
+    const int rb = r_dtype == FE_DTYPE_F32 ? 4 : 2;
+    if ((dgate && kind == FE_GATE_NONE) || (dw_post && !w_post) || (dw_pre && !w_pre)) return FE_ERR_INVALID_ARG;
+    if (T > 0 && ((du != nullptr) != (w_pre != nullptr) || (!dr_out && !du) || (dy && !y) ||
+                  (!dr && !dy && !dgate && !dw_post && !dw_pre)))
+        return FE_ERR_INVALID_ARG;
+    if (!aligned(dr_out, rb) || !aligned(du, 2) || !aligned(dr, rb) || !aligned(dy, 2) ||
+        !aligned(dgate, kind == FE_GATE_FULL ? 2 : 4) || !aligned(dw_post, 4) || !aligned(dw_pre, 4) ||
+        !aligned(workspace, 4))
+        return FE_ERR_INVALID_ARG;
+    if (T > 0 && !r) return FE_ERR_INVALID_ARG;
+    const bool sums = dw_post || dw_pre || (dgate && kind == FE_GATE_CHANNEL);
+    const size_t need = sums ? fe_moe_block_norm_workspace(T, H) : 0;
+    if (sums && !workspace) return FE_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return FE_ERR_CAPACITY;
+    const size_t nr = (size_t)T * H * rb, nb = (size_t)T * H * 2, nw = (size_t)H * 2, ng = gate_elems(gate_kind, T, H);
+    const void* ins[7] = {dr_out, du, r, y, w_post, gate, w_pre};
+    const size_t in_n[7] = {nr, nb, nr, nb, nw, 2 * ng, nw};
+    const void* outs[6] = {dr, dy, dgate, dw_post, dw_pre, sums ? workspace : nullptr};
+    const size_t out_n[6] = {nr, nb, (kind == FE_GATE_FULL ? 2 : 4) * ng, 4 * (size_t)H, 4 * (size_t)H, need};
+    for (int i = 0; i < 6; ++i) {
+        for (int j = 0; j < 7; ++j)   // dr may be dr_out itself
+            if (overlap(outs[i], out_n[i], ins[j], in_n[j]) && !(i == 0 && j == 0 && dr == dr_out)) return FE_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i], out_n[i], outs[j], out_n[j])) return FE_ERR_INVALID_ARG;
+    }
+    const cudaStream_t s = (cudaStream_t)stream;
+    if (T == 0) {   // sums over no rows
+        if (dw_post) FE_CUDA_TRY(cudaMemsetAsync(dw_post, 0, 4 * (size_t)H, s));
+        if (dw_pre) FE_CUDA_TRY(cudaMemsetAsync(dw_pre, 0, 4 * (size_t)H, s));
+        if (dgate && kind == FE_GATE_CHANNEL) FE_CUDA_TRY(cudaMemsetAsync(dgate, 0, 4 * (size_t)H, s));
+        return FE_OK;
+    }
+    const int sms = sm_count();
+    if (sms < 1) return record_cuda(cudaErrorInvalidDevice, "device");
+    fe::NormBwdParams q{};
+    q.f = norm_params(r, y, w_post, gate, gate_kind, scale, w_pre, eps, T, H);
+    q.dr_out = dr_out;
+    q.du = static_cast<const uint16_t*>(du);
+    q.dr = dr;
+    q.dy = static_cast<uint16_t*>(dy);
+    q.dgate = kind == FE_GATE_CHANNEL ? nullptr : dgate;
+    q.part = sums ? static_cast<float*>(workspace) : nullptr;
+    const NormBwdPlan b = norm_bwd_plan(T, H, sms);
+    q.rows_per_cta = b.rows_per_cta;
+    const bool vec = norm_vec(q.f) && aligned(dr_out, 16) && aligned(du, 16) && aligned(dr, 16) && aligned(dy, 16) &&
+                     (kind != FE_GATE_FULL || aligned(dgate, 16));
+    const bool r32 = r_dtype == FE_DTYPE_F32;
+    if (b.chunk == 2) FE_CUDA_TRY((norm_bwd_launch<2, 1024>(q, vec, r32, b, s)));
+    else if (b.threads > 512) FE_CUDA_TRY((norm_bwd_launch<1, 1024>(q, vec, r32, b, s)));
+    else FE_CUDA_TRY((norm_bwd_launch<1, 512>(q, vec, r32, b, s)));
+    if (sums)
+        FE_CUDA_TRY(launch(fe::column_sum_kernel, dim3((H + 31) / 32, 3), dim3(1024), 0, s,
+                           static_cast<const float*>(workspace), b.grid, H, 3, dw_post, dw_pre,
+                           kind == FE_GATE_CHANNEL ? static_cast<float*>(dgate) : static_cast<float*>(nullptr)));
+    return FE_OK;
+}
+
+size_t fe_moe_balance_workspace(int64_t T, int E)
+{
+    if (T < 0 || E < 1 || E > fe::kBalMaxE) return 0;
+    return 8 * (size_t)balance_ctas(T) * ((size_t)E + 1);
+}
+
+fe_status fe_moe_balance_loss(const float* logits, const int32_t* idx, const uint8_t* mask, int64_t T, int E, int top_k,
+                              float balance_coef, float z_coef, float* loss, int32_t* counts, int32_t* n_tokens,
+                              void* workspace, size_t workspace_bytes, fe_stream_t stream)
+{
+    const fe_status st = check_balance(logits, mask, T, E, top_k);
+    if (st != FE_OK) return st;
+    if ((T > 0 && !idx) || !loss || !counts || !n_tokens || !workspace || !aligned(idx, 4) || !aligned(loss, 4) ||
+        !aligned(counts, 4) || !aligned(n_tokens, 4) || !aligned(workspace, 4))
+        return FE_ERR_INVALID_ARG;
+    const size_t need = fe_moe_balance_workspace(T, E);
+    if (workspace_bytes < need) return FE_ERR_CAPACITY;
+    const void* ins[3] = {logits, idx, mask};
+    const size_t in_n[3] = {4 * (size_t)T * E, 4 * (size_t)T * top_k, (size_t)T};
+    const void* outs[4] = {loss, counts, n_tokens, workspace};
+    const size_t out_n[4] = {12, 4 * (size_t)E, 4, need};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < 3; ++j)
+            if (overlap(outs[i], out_n[i], ins[j], in_n[j])) return FE_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i], out_n[i], outs[j], out_n[j])) return FE_ERR_INVALID_ARG;
+    }
+    fe::BalanceParams p{};
+    p.logits = logits;
+    p.idx = idx;
+    p.mask = mask;
+    p.T = T;
+    p.E = E;
+    p.k = top_k;
+    p.a = balance_coef;
+    p.b = z_coef;
+    p.loss = loss;
+    p.counts = counts;
+    p.n_tokens = n_tokens;
+    p.G = balance_ctas(T);
+    p.part = static_cast<float*>(workspace);
+    p.ipart = reinterpret_cast<int32_t*>(p.part + (size_t)p.G * (E + 1));
+    const cudaStream_t s = (cudaStream_t)stream;
+    FE_CUDA_TRY(balance_dispatch(p, false, p.G, E % 4 == 0 && aligned(logits, 16), s));
+    FE_CUDA_TRY(launch(fe::balance_final_kernel, dim3(1), dim3(1024), 0, s, p));
+    return FE_OK;
+}
+
+fe_status fe_moe_balance_loss_backward(const float* logits, const int32_t* counts, const int32_t* n_tokens,
+                                       const uint8_t* mask, const float* dloss, int64_t T, int E, int top_k,
+                                       float balance_coef, float z_coef, void* dlogits, int dlogits_dtype,
+                                       fe_stream_t stream)
+{
+    const fe_status st = check_balance(logits, mask, T, E, top_k);
+    if (st != FE_OK) return st;
+    if (dlogits_dtype != FE_DTYPE_F32 && dlogits_dtype != FE_DTYPE_BF16) return FE_ERR_INVALID_ARG;
+    if (T == 0) return FE_OK;
+    const size_t eb = dtype_bytes(dlogits_dtype);
+    if (!counts || !n_tokens || !dlogits || !aligned(counts, 4) || !aligned(n_tokens, 4) || !aligned(dloss, 4) ||
+        !aligned(dlogits, eb))
+        return FE_ERR_INVALID_ARG;
+    const size_t nd = eb * (size_t)T * E, nl = 4 * (size_t)T * E;
+    // dlogits may be the logits themselves (fp32): a row is read before it is written
+    if ((overlap(dlogits, nd, logits, nl) && (dlogits != (const void*)logits || eb != 4)) ||
+        overlap(dlogits, nd, counts, 4 * (size_t)E) || overlap(dlogits, nd, n_tokens, 4) ||
+        overlap(dlogits, nd, mask, (size_t)T) || overlap(dlogits, nd, dloss, 4))
+        return FE_ERR_INVALID_ARG;
+    fe::BalanceParams p{};
+    p.logits = logits;
+    p.mask = mask;
+    p.T = T;
+    p.E = E;
+    p.k = top_k;
+    p.a = balance_coef;
+    p.b = z_coef;
+    p.counts = const_cast<int32_t*>(counts);
+    p.n_tokens = const_cast<int32_t*>(n_tokens);
+    p.dloss = dloss;
+    p.dlogits = dlogits;
+    p.dl_bf16 = dlogits_dtype == FE_DTYPE_BF16;
+    const int sms = sm_count();
+    if (sms < 1) return record_cuda(cudaErrorInvalidDevice, "device");
+    const int grid = (int)std::min<int64_t>((T + fe::kBalWarps - 1) / fe::kBalWarps, 8 * (int64_t)sms);
+    FE_CUDA_TRY(balance_dispatch(p, true, grid, E % 4 == 0 && aligned(logits, 16) && aligned(dlogits, 4 * eb),
+                                 (cudaStream_t)stream));
+    return FE_OK;
+}
+
+fe_status fe_moe_linear(const void* x, int64_t ldx, const void* w, const void* bias, const void* residual, int64_t ldr,
+                        int64_t M, int N, int K, int act, void* y, int64_t ldy, void* z, fe_stream_t stream)
+{
+    const fe_status st = fe_host::check_linear(x, ldx, w, bias, residual, ldr, M, N, K, act, y, ldy, z);
+    if (st != FE_OK) return st;
+    if (M == 0) return FE_OK;
+    const cudaStream_t s = (cudaStream_t)stream;
+    const int cols = out_cols(act, N);
+    if (M <= kLinRowsMax) {
+        fe::LinRowsParams p{};
+        p.x = static_cast<const uint16_t*>(x);
+        p.ldx = ldx;
+        p.w = static_cast<const uint16_t*>(w);
+        p.bias = static_cast<const uint16_t*>(bias);
+        p.res = static_cast<const uint16_t*>(residual);
+        p.ldr = ldr;
+        p.y = static_cast<uint16_t*>(y);
+        p.ldy = ldy;
+        p.z = static_cast<uint16_t*>(z);
+        p.M = (int)M;
+        p.N = N;
+        p.K = K;
+        p.act = act;
+        p.cols = cols;
+        FE_CUDA_TRY(act == FE_ACT_SWIGLU ? rows_launch<true>(p, s) : rows_launch<false>(p, s));
+        return FE_OK;
+    }
+    fe::LinParams P{};
+    FE_CUDA_TRY(lin_problem(&P.p[0], {x, M, K, ldx}, false, {w, N, K, K}, false, (int)M, N, K));
+    fe::LinProblem& p = P.p[0];
+    p.act = act;
+    p.cols = cols;
+    p.bias = static_cast<const uint16_t*>(bias);
+    p.res = static_cast<const uint16_t*>(residual);
+    p.ldr = ldr;
+    p.out = static_cast<uint16_t*>(y);
+    p.ldo = ldy;
+    p.z = static_cast<uint16_t*>(z);
+    p.vec = aligned(y, 16) && ldy % 8 == 0 && (!residual || (aligned(residual, 16) && ldr % 8 == 0)) &&
+            (!z || (aligned(z, 16) && N % 8 == 0 && cols % 8 == 0));
+    FE_CUDA_TRY(lin_run(P, 1, s));
+    return FE_OK;
+}
+
+size_t fe_moe_linear_workspace(int64_t M, int N, int K, int act)
+{
+    if (check_linear_shape(M, N, K, act) != FE_OK) return 0;
+    return align256(2 * (size_t)M * (((size_t)N + 7) / 8 * 8)) + sizeof(float) * (size_t)dz_chunks(M) * N;
+}
+
+fe_status fe_moe_linear_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w, const void* z,
+                                 int64_t M, int N, int K, int act, void* dx, int64_t lddx, void* dw, float* db,
+                                 void* workspace, size_t workspace_bytes, fe_stream_t stream)
+{
+    const fe_status st = check_linear_shape(M, N, K, act);
+    if (st != FE_OK) return st;
+    const int cols = out_cols(act, N);
+    if (!dx && !dw && !db) return FE_ERR_INVALID_ARG;
+    const size_t nx = span(M, ldx, K), ndx = span(M, lddx, K), nw = 2 * (size_t)N * K, nz = 2 * (size_t)M * N;
+    const size_t ndy = span(M, lddy, cols);
+    const size_t need = fe_moe_linear_workspace(M, N, K, act);
+    if (M > 0) {
+        if (!dy || lddy < cols || (act != FE_ACT_NONE && !z) || (dx && (!w || lddx < K)) || (dw && (!x || ldx < K)) ||
+            !workspace || !aligned(workspace, 16))
+            return FE_ERR_INVALID_ARG;
+        if (dw && ldx % 8 != 0) return FE_ERR_UNSUPPORTED;
+        if (!aligned(dy, 2) || !aligned(z, 2) || (dw && !aligned(x, 16)) || (dx && !aligned(w, 16))) return FE_ERR_INVALID_ARG;
+        if (workspace_bytes < need) return FE_ERR_CAPACITY;
+    }
+    if (!aligned(dx, 2) || !aligned(dw, 2) || !aligned(db, 4)) return FE_ERR_INVALID_ARG;
+    const void* ins[4] = {dy, dw ? x : nullptr, dx ? w : nullptr, act != FE_ACT_NONE ? z : nullptr};
+    const size_t in_n[4] = {ndy, nx, nw, nz};
+    const void* outs[4] = {dx, dw, db, M > 0 ? workspace : nullptr};
+    const size_t out_n[4] = {ndx, nw, 4 * (size_t)N, need};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < 4; ++j)
+            if (overlap(outs[i], out_n[i], ins[j], in_n[j])) return FE_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i], out_n[i], outs[j], out_n[j])) return FE_ERR_INVALID_ARG;
+    }
+    const cudaStream_t s = (cudaStream_t)stream;
+    if (M == 0) {   // sums over no rows
+        if (dw) FE_CUDA_TRY(cudaMemsetAsync(dw, 0, nw, s));
+        if (db) FE_CUDA_TRY(cudaMemsetAsync(db, 0, 4 * (size_t)N, s));
+        return FE_OK;
+    }
+    // dZ: dY itself without an activation, when its rows suit TMA
+    const bool direct = act == FE_ACT_NONE && lddy % 8 == 0 && aligned(dy, 16);
+    const int64_t lddz = direct ? lddy : ((int64_t)N + 7) / 8 * 8;
+    uint16_t* dzbuf = static_cast<uint16_t*>(workspace);
+    const void* dz = direct ? dy : dzbuf;
+    float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                           align256(2 * (size_t)M * (((size_t)N + 7) / 8 * 8)));
+    if (!direct || db) {
+        fe::LinDzParams p{};
+        p.dy = static_cast<const uint16_t*>(dy);
+        p.lddy = lddy;
+        p.z = static_cast<const uint16_t*>(z);
+        p.dz = direct || (!dx && !dw) ? nullptr : dzbuf;
+        p.lddz = lddz;
+        p.part = db ? part : nullptr;
+        p.M = M;
+        p.N = N;
+        p.cols = cols;
+        p.act = act;
+        const int chunks = dz_chunks(M);
+        p.rows_per_cta = (M + chunks - 1) / chunks;
+        const int used = (int)((M + p.rows_per_cta - 1) / p.rows_per_cta);
+        const bool vec = cols % 8 == 0 && lddy % 8 == 0 && aligned(dy, 16) && (act == FE_ACT_NONE || aligned(z, 16));
+        const int per = 32 * (vec ? 8 : 1);
+        const dim3 grid((cols + per - 1) / per, used);
+        FE_CUDA_TRY(vec ? launch(fe::linear_dz_kernel<8>, grid, dim3(256), 0, s, p)
+                        : launch(fe::linear_dz_kernel<1>, grid, dim3(256), 0, s, p));
+        if (db)
+            FE_CUDA_TRY(launch(fe::column_sum_kernel, dim3((N + 31) / 32, 1), dim3(1024), 0, s,
+                               static_cast<const float*>(part), used, N, 1, db, static_cast<float*>(nullptr),
+                               static_cast<float*>(nullptr)));
+    }
+    if (!dx && !dw) return FE_OK;
+    // dW [N][K] = dZ^T X (longest tiles first), dX [M][K] = dZ W: one launch
+    fe::LinParams P{};
+    int n = 0;
+    if (dw) {
+        FE_CUDA_TRY(lin_problem(&P.p[n], {dz, M, N, lddz}, true, {x, M, K, ldx}, true, N, K, (int)M));
+        P.p[n].out = static_cast<uint16_t*>(dw);
+        P.p[n].ldo = K;
+        P.p[n].vec = aligned(dw, 16);
+        ++n;
+    }
+    if (dx) {
+        FE_CUDA_TRY(lin_problem(&P.p[n], {dz, M, N, lddz}, false, {w, N, K, K}, true, (int)M, K, N));
+        P.p[n].out = static_cast<uint16_t*>(dx);
+        P.p[n].ldo = lddx;
+        P.p[n].vec = aligned(dx, 16) && lddx % 8 == 0;
+        ++n;
+    }
+    FE_CUDA_TRY(lin_run(P, n, s));
+    return FE_OK;
+}
+
+fe_status fe_moe_get_op_status(uint32_t* bits)
+{
+    uint32_t v = 0;
+    const uint32_t zero = 0;
+    FE_CUDA_TRY(cudaDeviceSynchronize());
+    FE_CUDA_TRY(cudaMemcpyFromSymbol(&v, fe::g_op_status, sizeof(v)));
+    if (v) FE_CUDA_TRY(cudaMemcpyToSymbol(fe::g_op_status, &zero, sizeof(v)));
+    if (bits) *bits = v;
+    return v ? FE_ERR_DEVICE_STATUS : FE_OK;
+}
+
+}  // extern "C"

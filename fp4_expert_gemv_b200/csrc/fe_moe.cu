@@ -16,6 +16,7 @@
 #include "gemv.cuh"
 #include "gemv_canonical.cuh"
 #include "gmma.cuh"
+#include "host.h"
 #include "nvfp4.cuh"
 #include "pack.cuh"
 #include "route.cuh"
@@ -1032,7 +1033,7 @@ fe_status forward_impl(fe_moe_t h, const void* x_bf16, const float* router_logit
 
 // The router GEMM fused with the top-k (router.cuh).
 fe_status router_impl(fe_moe_s* h, const void* x_bf16, const void* w_router_bf16, int T, int top_k, float* logits,
-                      int32_t* idx, float* w, cudaStream_t s)
+                      int32_t* idx, float* w, cudaStream_t s, bool check_only = false)
 {
     if (!h || T < 0 || top_k < 1 || top_k > h->E) return FE_ERR_INVALID_ARG;
     if (T == 0) return FE_OK;
@@ -1042,6 +1043,7 @@ fe_status router_impl(fe_moe_s* h, const void* x_bf16, const void* w_router_bf16
     const int J = h->E <= 32 ? 1 : h->E <= 64 ? 2 : h->E <= 128 ? 4 : h->E <= 256 ? 8 : 16;
     if (h->H % 64 != 0 || h->E > 512 || top_k > fe::kRtMaxK || top_k * J > fe::kRtCand) return FE_ERR_UNSUPPORTED;
     if (!h->rt_part || T > h->max_T) return FE_ERR_CAPACITY;
+    if (check_only) return FE_OK;
     fe::RouterParams rp;
     rp.x = static_cast<const uint16_t*>(x_bf16);
     rp.wr = static_cast<const uint16_t*>(w_router_bf16);
@@ -1063,6 +1065,10 @@ fe_status router_impl(fe_moe_s* h, const void* x_bf16, const void* w_router_bf16
 }
 
 }  // namespace
+
+namespace fe_host {
+fe_status record_cuda(cudaError_t e, const char* where) { return ::record_cuda(e, where); }
+}
 
 extern "C" {
 
@@ -1086,6 +1092,58 @@ fe_status fe_moe_forward_router(fe_moe_t h, const void* x_bf16, const void* w_ro
                                      (cudaStream_t)stream);
     if (st != FE_OK) return st;
     return forward_impl(h, x_bf16, logits, T, top_k, y_bf16, stream);
+}
+
+size_t fe_moe_forward_block_workspace(fe_moe_t h, int T, int shared_I)
+{
+    if (!h || T < 0 || shared_I < 0) return 0;
+    auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+    return 2 * up(2 * (size_t)T * h->H) + up(2 * (size_t)T * shared_I);
+}
+
+fe_status fe_moe_forward_block(fe_moe_t h, const fe_moe_block_t* b, const void* r, int r_dtype, const void* u_in, int T,
+                               int top_k, void* r_out, void* u_out, float* logits, void* workspace,
+                               size_t workspace_bytes, fe_stream_t stream)
+{
+    if (!h || !b || T < 0 || top_k < 1 || top_k > h->E) return FE_ERR_INVALID_ARG;
+    if (T == 0) return FE_OK;
+    if (!h->loaded) return FE_ERR_NOT_LOADED;
+    if (!r || !r_out || !logits || !b->w_router || !workspace || !aligned16(workspace) || (!u_in && !b->w_pre))
+        return FE_ERR_INVALID_ARG;
+    const bool shared = b->shared_gate_up != nullptr;
+    if (shared != (b->shared_down != nullptr) || (shared && b->shared_I < 1)) return FE_ERR_INVALID_ARG;
+    if (workspace_bytes < fe_moe_forward_block_workspace(h, T, shared ? b->shared_I : 0)) return FE_ERR_CAPACITY;
+    const int H = h->H, I = b->shared_I;
+    auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+    char* ws = static_cast<char*>(workspace);
+    void* ub = ws;
+    void* y = ws + up(2 * (size_t)T * H);
+    void* a = ws + 2 * up(2 * (size_t)T * H);
+    const void* u = u_in ? u_in : ub;
+    // every part's arguments, before the first launch
+    fe_status st = FE_OK;
+    if (!u_in) st = fe_host::check_block_norm(r, r_dtype, nullptr, nullptr, nullptr, FE_GATE_NONE, b->w_pre, b->eps, T, H, nullptr, ub);
+    if (st == FE_OK) st = router_impl(h, u, b->w_router, T, top_k, logits, nullptr, nullptr, nullptr, true);
+    if (st == FE_OK && top_k > h->max_k) st = FE_ERR_CAPACITY;
+    if (st == FE_OK && shared)
+        st = fe_host::check_linear(u, H, b->shared_gate_up, nullptr, nullptr, 0, T, 2 * I, H, FE_ACT_SWIGLU, a, I, nullptr);
+    if (st == FE_OK && shared)
+        st = fe_host::check_linear(a, I, b->shared_down, nullptr, y, H, T, H, I, FE_ACT_NONE, y, H, nullptr);
+    if (st == FE_OK)
+        st = fe_host::check_block_norm(r, r_dtype, y, b->w_post, b->gate, b->gate_kind, b->w_next_pre, b->eps, T, H, r_out, u_out);
+    if (st != FE_OK) return st;
+    DeviceGuard g(h->device);
+    if (!g.ok) return FE_ERR_CUDA;
+    if (!u_in)
+        st = fe_moe_block_norm(r, r_dtype, nullptr, nullptr, nullptr, FE_GATE_NONE, 0.0f, b->w_pre, b->eps, T, H, nullptr, ub, stream);
+    if (st == FE_OK) st = fe_moe_forward_router(h, u, b->w_router, T, top_k, y, logits, stream);
+    if (st == FE_OK && shared)
+        st = fe_moe_linear(u, H, b->shared_gate_up, nullptr, nullptr, 0, T, 2 * I, H, FE_ACT_SWIGLU, a, I, nullptr, stream);
+    if (st == FE_OK && shared)
+        st = fe_moe_linear(a, I, b->shared_down, nullptr, y, H, T, H, I, FE_ACT_NONE, y, H, nullptr, stream);
+    if (st == FE_OK)
+        st = fe_moe_block_norm(r, r_dtype, y, b->w_post, b->gate, b->gate_kind, b->scale, b->w_next_pre, b->eps, T, H, r_out, u_out, stream);
+    return st;
 }
 
 fe_status fe_moe_forward(fe_moe_t h, const void* x_bf16, const float* router_logits, int T, int top_k, void* y_bf16,

@@ -1,0 +1,20 @@
+// Host helpers shared by the translation units of the library.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "../../include/fe_moe.h"
+
+namespace fe_host {
+
+// Keeps the text of a CUDA failure for fe_moe_last_error and maps it to a status.
+fe_status record_cuda(cudaError_t e, const char* where);
+
+// fe_moe_block_norm and fe_moe_linear with their arguments checked only (nothing is enqueued).
+fe_status check_block_norm(const void* r, int r_dtype, const void* y, const void* w_post, const void* gate,
+                           int gate_kind, const void* w_pre, float eps, int64_t T, int H, const void* r_out,
+                           const void* u);
+fe_status check_linear(const void* x, int64_t ldx, const void* w, const void* bias, const void* residual, int64_t ldr,
+                       int64_t M, int N, int K, int act, const void* y, int64_t ldy, const void* z);
+
+}  // namespace fe_host

@@ -27,6 +27,7 @@
 
 #include "common.cuh"
 #include "mma.cuh"
+#include "tcgen05_ptx.cuh"
 
 namespace fe {
 
@@ -72,113 +73,6 @@ struct TcParams {
     unsigned long long* trace;   // optional: clock64 stamps of tile (0, 0), [3 per chunk]
     unsigned long long* tile_trace;   // optional: [slot][A tile][4] %globaltimer: start, loop end, end, SM
 };
-
-// ---- PTX wrappers ------------------------------------------------------------------
-
-// Shared-memory matrix descriptor for a K-major operand in the 128-byte swizzle
-// layout: rows of 128 bytes (64 f16), groups of 8 rows 1024 bytes apart.
-FE_DEV uint64_t tc_smem_desc(uint32_t saddr)
-{
-    uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);   // start address, 16-byte units
-    d |= (uint64_t)1u << 16;                            // leading byte offset (not used by this layout)
-    d |= (uint64_t)(1024u >> 4) << 32;                  // stride byte offset: 8-row groups
-    d |= (uint64_t)1u << 46;                            // descriptor version of tcgen05
-    d |= (uint64_t)2u << 61;                            // 128-byte swizzle
-    return d;
-}
-
-// Instruction descriptor of kind::f16: f32 accumulator, f16 A and B, both K-major.
-__host__ __device__ constexpr uint32_t tc_instr_desc(int M, int N)
-{
-    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-FE_DEV void tc_mma_f16(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
-{
-    const uint32_t mask = 0u;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %6, %7, %8}, p;\n\t}"
-        ::"r"(tmem_d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(mask), "r"(mask), "r"(mask),
-        "r"(mask));
-}
-
-FE_DEV void tc_commit(uint32_t mbar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(mbar)
-                 : "memory");
-}
-
-FE_DEV void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-FE_DEV void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-FE_DEV void tc_alloc(uint32_t dst_smem, uint32_t ncols)
-{
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
-                 : "memory");
-}
-
-FE_DEV void tc_relinquish() { asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory"); }
-
-FE_DEV void tc_dealloc(uint32_t taddr, uint32_t ncols)
-{
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-
-// 16 consecutive fp32 columns of this thread's TMEM lane.
-FE_DEV void tc_ld16(uint32_t taddr, uint32_t (&r)[16])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-}
-
-FE_DEV void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-
-FE_DEV void fence_proxy_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-
-// 16-byte cp.async; src_bytes 0 fills the destination with zeros.
-FE_DEV void cp_async16(uint32_t dst, const void* src, uint32_t src_bytes)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
-}
-
-FE_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
-template <int N>
-FE_DEV void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-FE_DEV uint32_t tc_saddr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
-FE_DEV void tc_mbar_init(uint32_t bar, uint32_t count)
-{
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-
-// Bounded wait for the completion of phase `parity` of an mbarrier.  Polls
-// with test_wait (no suspension): a thread suspended in try_wait was seen to
-// sleep for microseconds past the commit of the MMAs it waited for.
-FE_DEV bool tc_mbar_wait(uint32_t bar, uint32_t parity, unsigned long long timeout_ns)
-{
-    unsigned long long t0 = 0;
-    for (int it = 0;; ++it) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
-        if (ok) return true;
-        if (it == 0) t0 = globaltimer_ns();
-        else if ((it & 15) == 0 && globaltimer_ns() - t0 > timeout_ns) return false;
-    }
-}
-
-// Byte offset of 16-byte chunk c of row r in a 128-byte-swizzled K-major tile.
-FE_DEV uint32_t tc_swz(int r, int c) { return (uint32_t)r * 128u + (uint32_t)((c ^ (r & 7)) << 4); }
 
 // ---- the grouped GEMM tile ---------------------------------------------------------
 // grid: (A tiles of one expert, tile slots); block: kTcThreads.  Tile slot y

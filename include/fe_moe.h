@@ -425,6 +425,160 @@ int fe_moe_stack_last_launches(fe_moe_stack_t s);
 /* Free the stack's buffers (not the layers).  Waits for the device first. */
 void fe_moe_stack_destroy(fe_moe_stack_t s);
 
+/* ---- the operators around the experts --------------------------------------------
+ * What stands around the packed layer in a model's block: the norms before and
+ * after it with the gate and the residual ("FastInfer", the fused RMSNorm), the
+ * dense product with its epilogue (a shared expert beside the routed ones; "Packed
+ * Marlin projections": gate and up packed into one matrix), and the router's
+ * balance loss.  No counterpart of their combination on the pages.  These entry
+ * points take no handle: every buffer is the caller's, workspace included, so calls
+ * on several streams or captured graphs share nothing as long as their buffers
+ * differ.  They run on the current device, which the pointers and the stream must
+ * belong to, asynchronously, without allocation or host synchronisation
+ * (capturable).  Arrays are dense and row-major unless a row stride (ld, in
+ * elements) is given; addresses need their type's alignment, 16-byte aligned rows
+ * are faster.  Outputs must not overlap operands, workspace or each other except
+ * where said (FE_ERR_INVALID_ARG).  Sums, statistics and epilogues are fp32, each
+ * output is rounded once, and every result is the same from run to run.  */
+#define FE_DTYPE_BF16 0
+#define FE_DTYPE_F32 1
+
+#define FE_GATE_NONE 0
+#define FE_GATE_CHANNEL 1   /* bf16 [H] */
+#define FE_GATE_TOKEN 2     /* bf16 [T] */
+#define FE_GATE_FULL 3      /* bf16 [T][H] */
+#define FE_GATE_SIGMOID 16  /* added to one of the three: the gate goes through a sigmoid */
+
+/* The boundary of two blocks in one launch, per row of H:
+ *   m  = y / sqrt(mean(y^2) + eps),  v = w_post * m      (v = y if w_post is NULL)
+ *   r' = r + scale * a(gate) * v                         (a: identity or sigmoid)
+ *   u  = w_pre * r' / sqrt(mean(r'^2) + eps)             (from the unrounded r')
+ *   r      [T][H] of r_dtype, the residual stream;
+ *   y      bf16 [T][H], the block's output, or NULL: no block, r' = r (w_post and
+ *          gate NULL, r_out NULL: the norm in front of the first block);
+ *   w_post, w_pre   bf16 [H] or NULL;  gate   bf16, its shape from gate_kind;
+ *   r_out  [T][H] of r_dtype, may be r itself, or NULL to skip;
+ *   u      bf16 [T][H], given exactly when w_pre is.  At least one output.
+ * eps > 0 and finite, 1 <= H <= 16384 (FE_ERR_UNSUPPORTED above), T < 2^31; T = 0 is
+ * a no-op. */
+fe_status fe_moe_block_norm(const void* r, int r_dtype, const void* y, const void* w_post, const void* gate,
+                            int gate_kind, float scale, const void* w_pre, float eps, int64_t T, int H, void* r_out,
+                            void* u, fe_stream_t stream);
+
+/* Bytes of workspace fe_moe_block_norm_backward needs for a weight or channel-gate
+ * gradient (0 for sizes it refuses). */
+size_t fe_moe_block_norm_workspace(int64_t T, int H);
+
+/* Its gradients.  dr_out [T][H] of r_dtype (gradient at r', NULL: zero), du bf16
+ * [T][H] (gradient at u, given exactly when w_pre is), at least one of the two; the
+ * operands are the forward call's (nothing else is saved).  Outputs, each optional
+ * (at least one):
+ *   dr      [T][H] of r_dtype, may be dr_out itself;  dy   bf16 [T][H];
+ *   dgate   per channel float [H], per token float [T], full bf16 [T][H]; with
+ *           FE_GATE_SIGMOID the gradient at the gate before the sigmoid;
+ *   dw_post, dw_pre   float [H].
+ * workspace: needed for dw_post, dw_pre and a channel dgate; too small:
+ * FE_ERR_CAPACITY.  T = 0 writes zeros to the sums over rows. */
+fe_status fe_moe_block_norm_backward(const void* dr_out, const void* du, const void* r, int r_dtype, const void* y,
+                                     const void* w_post, const void* gate, int gate_kind, float scale,
+                                     const void* w_pre, float eps, int64_t T, int H, void* dr, void* dy, void* dgate,
+                                     float* dw_post, float* dw_pre, void* workspace, size_t workspace_bytes,
+                                     fe_stream_t stream);
+
+/* Bytes of workspace fe_moe_balance_loss needs (0 for sizes it refuses). */
+size_t fe_moe_balance_workspace(int64_t T, int E);
+
+/* The router's balance loss and the experts' token counts, over the n tokens that
+ * the mask keeps:
+ *   p_t = softmax(logits_t),  counts[e] = #{(t, j): idx[t][j] = e},
+ *   balance = E * sum_e (counts[e] / (n top_k)) * ((1/n) sum_t p_te),
+ *   z = (1/n) sum_t logsumexp(logits_t)^2,  loss = balance_coef * balance + z_coef * z.
+ *   logits float [T][E] and idx int32 [T][top_k], as fe_moe_router writes them (ids
+ *   outside [0, E) are not counted; an id given twice counts twice);
+ *   mask   uint8 [T], 0 = padding (its rows are not read), or NULL;
+ *   loss   float [3]: loss, balance, z;  counts int32 [E];  n_tokens int32 [1].
+ * -inf logits have p = 0; a row of them alone adds nothing to balance and z; a NaN or
+ * +inf logit makes the loss NaN.  n = 0: all zeros.  1 <= E <= 1024, T * top_k < 2^31
+ * (FE_ERR_UNSUPPORTED above). */
+fe_status fe_moe_balance_loss(const float* logits, const int32_t* idx, const uint8_t* mask, int64_t T, int E, int top_k,
+                              float balance_coef, float z_coef, float* loss, int32_t* counts, int32_t* n_tokens,
+                              void* workspace, size_t workspace_bytes, fe_stream_t stream);
+
+/* Its gradient with respect to the logits, times dloss (device float [1], NULL: 1):
+ * the counts are constants of it, and counts and n_tokens are the loss call's.
+ * dlogits [T][E] of dlogits_dtype (bf16 to go on as fe_moe_linear_backward's dy:
+ * the router's weights and input); rows that the mask drops and rows of -inf alone
+ * are written as zeros; float dlogits may be the logits themselves. */
+fe_status fe_moe_balance_loss_backward(const float* logits, const int32_t* counts, const int32_t* n_tokens,
+                                       const uint8_t* mask, const float* dloss, int64_t T, int E, int top_k,
+                                       float balance_coef, float z_coef, void* dlogits, int dlogits_dtype,
+                                       fe_stream_t stream);
+
+#define FE_ACT_NONE 0
+#define FE_ACT_RELU 1
+#define FE_ACT_GELU 2     /* z * Phi(z), the exact form */
+#define FE_ACT_SILU 3
+#define FE_ACT_SWIGLU 4   /* silu(z[:, :N/2]) * z[:, N/2:]: gate rows of w first, as in the packed layer */
+
+/* z = x w^T + bias,  y = act(z) + residual, on bf16 operands with fp32 sums:
+ *   x        bf16 [M][K], row stride ldx (a multiple of 8, else FE_ERR_UNSUPPORTED),
+ *            16-byte aligned;  w  bf16 [N][K], 16-byte aligned;  bias bf16 [N] or NULL;
+ *   residual bf16 [M][C], row stride ldr, or NULL; C = N (N / 2 for FE_ACT_SWIGLU);
+ *   y        bf16 [M][C], row stride ldy; may be the residual itself (same stride);
+ *   z        bf16 [M][N], the pre-activation for fe_moe_linear_backward, or NULL.
+ * K % 8 == 0 (else FE_ERR_UNSUPPORTED); M = 0 is a no-op. */
+fe_status fe_moe_linear(const void* x, int64_t ldx, const void* w, const void* bias, const void* residual, int64_t ldr,
+                        int64_t M, int N, int K, int act, void* y, int64_t ldy, void* z, fe_stream_t stream);
+
+/* Bytes of workspace fe_moe_linear_backward needs (0 for sizes it refuses). */
+size_t fe_moe_linear_workspace(int64_t M, int N, int K, int act);
+
+/* Its gradients: dz = dy * act'(z) (0 at a relu's zero), dx = dz w, dw = dz^T x, db =
+ * sum over rows of dz; the residual's gradient is dy.  dy bf16 [M][C], row stride
+ * lddy; z as the forward call wrote it (NULL without an activation).  dz is rounded
+ * to bf16 as an operand of the two products; db sums it unrounded.  Outputs, each optional
+ * (at least one): dx bf16 [M][K] (row stride lddx), dw bf16 [N][K], db float [N]; x
+ * is needed for dw, w for dx.  workspace 16-byte aligned.  M = 0 writes zeros to dw
+ * and db. */
+fe_status fe_moe_linear_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w, const void* z,
+                                 int64_t M, int N, int K, int act, void* dx, int64_t lddx, void* dw, float* db,
+                                 void* workspace, size_t workspace_bytes, fe_stream_t stream);
+
+/* Device-side problem bits (FE_DEVICE_TC_TIMEOUT) of the calls above on the current
+ * device since the last query; waits for the device and clears them.  Returns
+ * FE_ERR_DEVICE_STATUS if a bit is set. */
+fe_status fe_moe_get_op_status(uint32_t* bits);
+
+/* One block: norm, router, routed experts, shared expert, norm, gate and residual,
+ * and the norm in front of the next block.  All pointers are device memory. */
+typedef struct {
+    const void* w_pre;           /* bf16 [H]; not read when u_in is given */
+    const void* w_router;        /* bf16 [E][H], as fe_moe_router takes it */
+    const void* shared_gate_up;  /* bf16 [2 shared_I][H], gate rows first; NULL: no shared expert */
+    const void* shared_down;     /* bf16 [H][shared_I] */
+    int shared_I;                /* a multiple of 8 */
+    const void* w_post;          /* bf16 [H] or NULL, as fe_moe_block_norm takes them */
+    const void* gate;
+    int gate_kind;
+    float scale;
+    const void* w_next_pre;      /* bf16 [H], the next block's w_pre, or NULL */
+    float eps;
+} fe_moe_block_t;
+
+/* Bytes of workspace fe_moe_forward_block needs for T tokens (0 for a NULL handle). */
+size_t fe_moe_forward_block_workspace(fe_moe_t h, int T, int shared_I);
+
+/* u = norm(r; w_pre) (or u_in), y = the packed layer on u by fe_moe_forward_router,
+ * plus the shared expert swiglu(u shared_gate_up^T) shared_down^T, then
+ * fe_moe_block_norm: r_out = r + scale a(gate) norm(y; w_post), u_out =
+ * norm(r_out; w_next_pre).  r, r_out [T][H] of r_dtype (r_out may be r); u_in bf16
+ * [T][H] or NULL (pass the previous block's u_out); u_out bf16 [T][H], given exactly
+ * when w_next_pre is; logits float [T][E] (written).  Limits and errors as the calls it is
+ * made of; workspace 16-byte aligned.  Asynchronous, capturable. */
+fe_status fe_moe_forward_block(fe_moe_t h, const fe_moe_block_t* b, const void* r, int r_dtype, const void* u_in, int T,
+                               int top_k, void* r_out, void* u_out, float* logits, void* workspace,
+                               size_t workspace_bytes, fe_stream_t stream);
+
 /* Text of the last CUDA failure behind an FE_ERR_CUDA / FE_ERR_OOM returned to
  * this thread ("" if none); static thread-local storage. */
 const char* fe_moe_last_error(void);

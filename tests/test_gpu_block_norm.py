@@ -1,0 +1,215 @@
+"""The block's norms with gate and residual, forward and backward, against the 64-bit definition."""
+import numpy as np
+import pytest
+import torch
+
+import block_ref as ref
+
+pytestmark = pytest.mark.gpu
+EPS = 1e-6
+
+
+def make(T, H, rt, gate, seed=0, y=True):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    n = lambda *s, std=1.0: torch.randn(*s, generator=g, device="cuda") * std
+    bf = torch.bfloat16
+    shape = dict(none=None, channel=(H,), token=(T,), full=(T, H))[gate]
+    return dict(r=n(T, H, std=2.0).to(rt), y=n(T, H, std=0.3).to(bf) if y else None,
+                w_post=(1 + n(H, std=0.2)).to(bf) if y else None, w_pre=(1 + n(H, std=0.2)).to(bf),
+                g=n(*shape).to(bf) if shape else None, dr_out=n(T, H).to(rt), du=n(T, H).to(bf))
+
+
+def kind_of(fe, gate, sigmoid):
+    k = dict(none=fe.GATE_NONE, channel=fe.GATE_CHANNEL, token=fe.GATE_TOKEN, full=fe.GATE_FULL)[gate]
+    return k | (fe.GATE_SIGMOID if sigmoid and gate != "none" else 0)
+
+
+def check_forward(fe, c, gate, sigmoid, s=0.5, eps=EPS):
+    r2, u = fe.block_norm(c["r"], c["y"], c["w_post"], c["w_pre"], gate=c["g"], gate_kind=kind_of(fe, gate, sigmoid), scale=s, eps=eps)
+    want = ref.norm_forward(c["r"], c["y"], c["w_post"], c["w_pre"], c["g"], gate, sigmoid, s, eps)
+    if r2 is not None:
+        ref.close(r2, want["r_out"][0], ref.FWD * want["r_out"][1], "r_out")
+    if u is not None:
+        ref.close(u, want["u"][0], ref.FWD * want["u"][1], "u")
+
+
+def check_backward(fe, c, gate, sigmoid, s=0.5, eps=EPS):
+    got = fe.block_norm_backward(c["dr_out"], c["du"], c["r"], c["y"], c["w_post"], c["w_pre"], gate=c["g"],
+                                 gate_kind=kind_of(fe, gate, sigmoid), scale=s, eps=eps)
+    want = ref.norm_backward(c["dr_out"], c["du"], c["r"], c["y"], c["w_post"], c["w_pre"], c["g"], gate, sigmoid, s, eps)
+    for name, t in zip(("dr", "dy", "dgate", "dw_post", "dw_pre"), got):
+        assert (t is None) == (name not in want), name
+        if t is not None:
+            ref.close(t, want[name][0], ref.BWD * want[name][1], name)
+    return got
+
+
+SHAPES = [(1, 1), (1, 2048), (2, 8), (3, 64), (5, 7), (7, 1999), (33, 256), (4, 257), (130, 2048), (9, 4096), (3, 8192), (2, 8200), (2, 16384),
+          (300, 40), (1, 16383)]
+
+
+@pytest.mark.parametrize("gate, sigmoid", [("none", False), ("channel", False), ("token", True), ("full", True), ("full", False), ("token", False), ("channel", True)])
+@pytest.mark.parametrize("rt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T, H", SHAPES)
+def test_forward_and_backward(T, H, rt, gate, sigmoid):
+    import fp4_expert_gemv_b200 as fe
+    c = make(T, H, rt, gate, seed=T + H)
+    check_forward(fe, c, gate, sigmoid)
+    check_backward(fe, c, gate, sigmoid)
+
+
+@pytest.mark.parametrize("drop", [("y", "w_post"), ("w_post",), ("w_pre", "du"), ("w_post", "w_pre", "du"), ("dr_out",)])
+@pytest.mark.parametrize("gate", ["none", "token"])
+def test_parts_left_out(drop, gate):
+    import fp4_expert_gemv_b200 as fe
+    if "y" in drop and gate != "none":
+        return
+    c = make(37, 520, torch.bfloat16, gate, seed=3)
+    for name in drop:
+        c[name] = None
+    check_forward(fe, c, gate, True)
+    check_backward(fe, c, gate, True)
+
+
+def test_many_rows_walk_several_times():
+    import fp4_expert_gemv_b200 as fe
+    c = make(5003, 136, torch.bfloat16, "channel", seed=9)
+    check_forward(fe, c, "channel", True)
+    check_backward(fe, c, "channel", True)
+
+
+def test_unaligned_rows():
+    """A width of whole chunks whose rows start 2 bytes off take the narrow accesses."""
+    import fp4_expert_gemv_b200 as fe
+    c = make(11, 512, torch.bfloat16, "none", seed=4)
+    buf = torch.empty(11 * 512 + 1, dtype=torch.bfloat16, device="cuda")
+    odd = buf[1:].view(11, 512)
+    odd.copy_(c["y"])
+    c["y"] = odd
+    check_forward(fe, c, "none", False)
+    check_backward(fe, c, "none", False)
+
+
+def test_extreme_rows():
+    """Zero rows, huge and tiny rows, a NaN row and an infinite row stay in their rows."""
+    import fp4_expert_gemv_b200 as fe
+    for H in (256, 255):
+        c = make(8, H, torch.float32, "token", seed=5)
+        c["r"][0] = 0
+        c["y"][0] = 0
+        c["y"][1] = 0
+        c["r"][2] *= 1e15
+        c["y"][3] *= 1e-15
+        c["y"][4, 3] = float("nan")
+        c["r"][5, 1] = float("inf")
+        r2, u = fe.block_norm(c["r"], c["y"], c["w_post"], c["w_pre"], gate=c["g"], gate_kind=fe.GATE_TOKEN, scale=0.5, eps=EPS)
+        keep = [0, 1, 2, 3, 6, 7]
+        want = ref.norm_forward(c["r"], c["y"], c["w_post"], c["w_pre"], c["g"], "token", False, 0.5, EPS)
+        ref.close(r2[keep], want["r_out"][0][keep], ref.FWD * want["r_out"][1][keep], "r_out")
+        ref.close(u[keep], want["u"][0][keep], ref.FWD * want["u"][1][keep], "u")
+        assert torch.isnan(u[4]).all() and torch.isnan(r2[4]).all()
+        # 1 / rms of the infinite row is 0: 0 where r' is finite, inf * 0 where it is not
+        assert torch.isnan(u[5, 1]) and (u[5, 2:] == 0).all()
+
+
+def test_in_place_and_untouched_rows():
+    import fp4_expert_gemv_b200 as fe
+    c = make(9, 192, torch.bfloat16, "none", seed=6)
+    want, wu = fe.block_norm(c["r"], c["y"], c["w_post"], c["w_pre"], scale=0.5)
+    buf = torch.full((12, 192), 7.0, dtype=torch.bfloat16, device="cuda")
+    buf[:9] = c["r"]
+    r, u = fe.block_norm(buf[:9], c["y"], c["w_post"], c["w_pre"], scale=0.5, r_out=buf[:9])
+    assert torch.equal(r, want) and torch.equal(u, wu) and (buf[9:] == 7).all()
+
+
+def test_no_rows():
+    import fp4_expert_gemv_b200 as fe
+    c = make(0, 64, torch.bfloat16, "channel")
+    r2, u = fe.block_norm(c["r"], c["y"], c["w_post"], c["w_pre"], gate=c["g"], gate_kind=fe.GATE_CHANNEL)
+    assert r2.shape == (0, 64) and u.shape == (0, 64)
+    got = fe.block_norm_backward(c["dr_out"], c["du"], c["r"], c["y"], c["w_post"], c["w_pre"], gate=c["g"], gate_kind=fe.GATE_CHANNEL)
+    assert all((t == 0).all() for t in got[2:])
+
+
+def test_the_same_every_time_and_on_another_stream():
+    import fp4_expert_gemv_b200 as fe
+    c = make(2000, 1024, torch.bfloat16, "channel", seed=8)
+    args = (c["dr_out"], c["du"], c["r"], c["y"], c["w_post"], c["w_pre"])
+    kw = dict(gate=c["g"], gate_kind=fe.GATE_CHANNEL | fe.GATE_SIGMOID, scale=0.7)
+    first = fe.block_norm_backward(*args, **kw)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    two = [fe.block_norm_backward(*args, stream=side, **kw), fe.block_norm_backward(*args, **kw),
+           fe.block_norm_backward(*args, stream=side.cuda_stream, **kw)]
+    torch.cuda.synchronize()
+    for got in two:
+        assert all(torch.equal(a, b) for a, b in zip(first, got))
+
+
+def test_captured_and_replayed_on_new_contents():
+    import fp4_expert_gemv_b200 as fe
+    c = make(64, 768, torch.float32, "full", seed=1)
+    kw = dict(gate=c["g"], gate_kind=fe.GATE_FULL | fe.GATE_SIGMOID, scale=0.5)
+
+    def both():
+        return (*fe.block_norm(c["r"], c["y"], c["w_post"], c["w_pre"], **kw),
+                *fe.block_norm_backward(c["dr_out"], c["du"], c["r"], c["y"], c["w_post"], c["w_pre"], **kw))
+
+    both()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = both()
+        graphs.append((g, out))
+    c2 = make(64, 768, torch.float32, "full", seed=2)
+    for k in ("r", "y", "w_post", "w_pre", "g", "dr_out", "du"):
+        c[k].copy_(c2[k])
+    for g, _ in graphs:
+        g.replay()
+    eager = both()
+    torch.cuda.synchronize()
+    for _, out in graphs:
+        assert all(torch.equal(a, b) for a, b in zip(out, eager))
+
+
+@pytest.mark.parametrize("gate", ["channel", "token", "full"])
+def test_gradient_against_differences(gate):
+    """<gradient, direction> against central differences of the 64-bit definition.  The step error is
+    h^2 / 6 of the third derivative: with h = 1e-4 and terms of order one, below 1e-6 of the sums; the
+    kernel's bf16 outputs dr, dy, dgate are off by 2^-8 per element, which their own magnitude bounds."""
+    import fp4_expert_gemv_b200 as fe
+    c = make(6, 96, torch.float32, gate, seed=12)
+    s = 0.6
+    got = dict(zip(("r", "y", "g", "w_post", "w_pre"),
+                   fe.block_norm_backward(c["dr_out"], c["du"], c["r"], c["y"], c["w_post"], c["w_pre"], gate=c["g"],
+                                          gate_kind=kind_of(fe, gate, True), scale=s)))
+
+    def loss(v):
+        o = ref.norm_forward(v["r"], v["y"], v["w_post"], v["w_pre"], v["g"], gate, True, s, 1e-6)
+        return float((o["r_out"][0] * c["dr_out"].double()).sum() + (o["u"][0] * c["du"].double()).sum())
+
+    base = {k: c[k].double() for k in ("r", "y", "g", "w_post", "w_pre")}
+    gen = torch.Generator(device="cuda").manual_seed(77)
+    for name in base:
+        dirn = torch.randn(base[name].shape, generator=gen, device="cuda", dtype=torch.float64)
+        h = 1e-4
+        num = (loss({**base, name: base[name] + h * dirn}) - loss({**base, name: base[name] - h * dirn})) / (2 * h)
+        grad = got[name].double()
+        tol = 2.0 ** -8 * float((grad * dirn).abs().sum()) + 1e-4
+        assert abs(num - float((grad * dirn).sum())) <= tol, (name, num)
+
+
+def test_refuses_other_layouts():
+    import fp4_expert_gemv_b200 as fe
+    c = make(8, 64, torch.bfloat16, "none")
+    with pytest.raises(ValueError):
+        fe.block_norm(c["r"].t().contiguous().t(), c["y"], c["w_post"], c["w_pre"])
+    with pytest.raises(ValueError):
+        fe.block_norm(c["r"], c["y"][:4], c["w_post"], c["w_pre"])
+    with pytest.raises(ValueError):
+        fe.block_norm(c["r"], c["y"].float(), c["w_post"], c["w_pre"])
+    with pytest.raises(fe.FeMoeError):
+        fe.block_norm(c["r"], c["y"], c["w_post"], c["w_pre"], eps=0.0)
+    with pytest.raises(fe.FeMoeError):
+        fe.block_norm(c["r"], c["y"], c["w_post"], c["w_pre"], u=c["y"])

@@ -1,0 +1,248 @@
+"""The dense product with its epilogue, forward and backward, against the 64-bit definition."""
+import pytest
+import torch
+
+import block_ref as ref
+
+pytestmark = pytest.mark.gpu
+bf = torch.bfloat16
+ACTS = ["none", "relu", "gelu", "silu", "swiglu"]
+
+
+def act_id(fe, act):
+    return dict(none=fe.ACT_NONE, relu=fe.ACT_RELU, gelu=fe.ACT_GELU, silu=fe.ACT_SILU, swiglu=fe.ACT_SWIGLU)[act]
+
+
+def make(M, N, K, act, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    n = lambda *s, std=1.0: (torch.randn(*s, generator=g, device="cuda") * std).to(bf)
+    cols = N // 2 if act == "swiglu" else N
+    return n(M, K), n(N, K, std=K ** -0.5), n(N, std=0.2), n(M, cols), n(M, cols)
+
+
+def check_forward(fe, x, w, bias, act, res, y=None, z=None):
+    out = fe.linear(x, w, bias=bias, act=act_id(fe, act), residual=res.clone() if res is not None else None, y=y, z=z)
+    wy, wz, ey, ez = ref.linear(x, w, bias, act, res)
+    ref.close(out, wy, ey, "y")
+    if z is not None:
+        ref.close(z, wz, ez, "z")
+    assert fe.op_status() == (fe.FE_OK, 0)
+    return out
+
+
+def check_backward(fe, dy, x, w, z, act):
+    dx, dw, db = fe.linear_backward(dy, x, w, z=z, act=act_id(fe, act))
+    dz, mag = ref.linear_dz(dy, z if z is not None else dy, act)
+    # dz enters the products rounded to bf16 (half a step, 2^-8 relative), then fp32 sums as forward
+    edz = 2.0 ** -8 * dz.abs() + ref.FWD * mag
+    X, W = x.double(), w.double()
+    adz = dz.abs() + edz
+    M, N = dz.shape
+    ref.close(dx, dz @ W, edz @ W.abs() + (N / 16 + 4) * 2.0 ** -22 * (adz @ W.abs()), "dx")
+    ref.close(dw, dz.t() @ X, edz.t() @ X.abs() + (M / 16 + 4) * 2.0 ** -22 * (adz.t() @ X.abs()), "dw")
+    # chains of at most M / 512 + 1 rows per thread, then 8, then the chunks in a tree
+    ref.close(db, dz.sum(0), (ref.FWD + (M / 512 + 32) * 2.0 ** -24) * mag.sum(0), "db")
+    assert fe.op_status() == (fe.FE_OK, 0)
+
+
+SHAPES = [(1, 2, 8), (1, 1536, 2048), (2, 30, 264), (3, 64, 72), (5, 130, 520), (8, 66, 1000), (9, 64, 64), (17, 34, 40), (64, 2048, 768),
+          (127, 130, 200), (128, 256, 64), (129, 258, 72), (200, 1536, 2048), (1003, 1002, 1992), (700, 22, 8)]
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M, N, K", SHAPES)
+def test_forward(M, N, K, act):
+    import fp4_expert_gemv_b200 as fe
+    x, w, bias, res, _ = make(M, N, K, act, seed=M + N)
+    z = torch.empty(M, N, dtype=bf, device="cuda")
+    a = check_forward(fe, x, w, bias, act, res, z=z)
+    check_forward(fe, x, w, None, act, None)
+    assert torch.equal(a, check_forward(fe, x, w, bias, act, res))   # with and without z, run to run
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M, N, K", [(1, 2, 8), (3, 16, 64), (9, 34, 40), (64, 256, 128), (130, 258, 200), (1003, 502, 264), (2000, 96, 1032)])
+def test_backward(M, N, K, act):
+    import fp4_expert_gemv_b200 as fe
+    x, w, bias, _, dy = make(M, N, K, act, seed=M * N)
+    z = None
+    if act != "none":
+        z = torch.empty(M, N, dtype=bf, device="cuda")
+        fe.linear(x, w, bias=bias, act=act_id(fe, act), z=z)
+    check_backward(fe, dy, x, w, z, act)
+
+
+@pytest.mark.parametrize("N", [1, 5, 7, 33, 1001])
+@pytest.mark.parametrize("M", [1, 6, 150])
+def test_odd_columns(M, N):
+    import fp4_expert_gemv_b200 as fe
+    x, w, bias, res, dy = make(M, N, 96, "gelu", seed=N)
+    z = torch.empty(M, N, dtype=bf, device="cuda")
+    check_forward(fe, x, w, bias, "gelu", res, z=z)
+    check_backward(fe, dy, x, w, z, "gelu")
+    check_backward(fe, dy, x, w, None, "none")
+
+
+@pytest.mark.parametrize("M, N, K", [(64, 64, 64), (130, 70, 136), (5, 24, 64), (512, 264, 192), (300, 1100, 72)])
+def test_small_integers_come_out_exactly(M, N, K):
+    """Values in {-1, 0, 1} with at most 256 nonzero products per sum: every sum is a whole number below
+    2^8, exact in bf16, so each output equals the exact product and a missing, doubled or
+    misplaced term shows."""
+    import fp4_expert_gemv_b200 as fe
+    g = torch.Generator(device="cuda").manual_seed(M + K)
+    tri = lambda *s: (torch.randint(-1, 2, s, generator=g, device="cuda")).to(bf)
+    x, w, dy = tri(M, K), tri(N, K), tri(M, N)
+    # thin out long sums
+    if M > 256:
+        dy[torch.randperm(M, generator=g, device="cuda")[256:]] = 0
+    if N > 256:
+        dy[:, torch.randperm(N, generator=g, device="cuda")[256:]] = 0
+    assert torch.equal(fe.linear(x, w).double(), x.double() @ w.double().t())
+    dx, dw, db = fe.linear_backward(dy, x, w)
+    assert torch.equal(dx.double(), dy.double() @ w.double())
+    assert torch.equal(dw.double(), dy.double().t() @ x.double())
+    assert torch.equal(db.double(), dy.double().sum(0))
+
+
+@pytest.mark.parametrize("M", [1, 4, 40, 300])
+def test_strided_rows_and_the_sum_in_place(M):
+    import fp4_expert_gemv_b200 as fe
+    x, w, bias, res, dy = make(M, 96, 128, "none", seed=M)
+    wide = torch.zeros(M, 200, dtype=bf, device="cuda")
+    wide[:, 8:136] = x
+    out = torch.full((M, 150), 3.0, dtype=bf, device="cuda")
+    want = check_forward(fe, x, w, bias, "none", res)
+    for at in (0, 8, 5):
+        out.fill_(3.0)
+        fe.linear(wide[:, 8:136], w, bias=bias, residual=res, y=out[:, at:at + 96])
+        assert torch.equal(out[:, at:at + 96], want)
+        assert (out[:, :at] == 3).all() and (out[:, at + 96:] == 3).all()
+        out[:, at:at + 96] = res
+        fe.linear(x, w, bias=bias, residual=out[:, at:at + 96], y=out[:, at:at + 96])
+        assert torch.equal(out[:, at:at + 96], want)
+    wdy = torch.zeros(M, 111, dtype=bf, device="cuda")
+    wdy[:, 3:99] = dy
+    a = fe.linear_backward(dy, x, w)
+    b = fe.linear_backward(wdy[:, 3:99], wide[:, 8:136], w)
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_infinities_and_nan_stay_in_their_rows():
+    import fp4_expert_gemv_b200 as fe
+    for M in (4, 140):
+        x, w, bias, res, _ = make(M, 64, 128, "silu", seed=2)
+        clean = fe.linear(x, w, act=fe.ACT_SILU)
+        x[1, 5] = float("nan")
+        x[2, 7] = float("inf")
+        y = fe.linear(x, w, act=fe.ACT_SILU)
+        assert torch.isnan(y[1]).all()
+        keep = [i for i in range(M) if i not in (1, 2)]
+        assert torch.equal(y[keep], clean[keep])
+        relu = fe.linear(x, w, act=fe.ACT_RELU)
+        assert torch.isnan(relu[1]).all()
+
+
+def test_large_activations_saturate_as_the_formula_does():
+    import fp4_expert_gemv_b200 as fe
+    for M in (2, 64):
+        for act in ("silu", "gelu", "swiglu"):
+            x, w, bias, _, dy = make(M, 64, 64, act, seed=5)
+            x = (x.float() * 100).to(bf)
+            z = torch.empty(M, 64, dtype=bf, device="cuda")
+            y = fe.linear(x, w, act=act_id(fe, act), z=z)
+            assert torch.isfinite(y).all()
+            for t in fe.linear_backward(dy, x, w, z=z, act=act_id(fe, act)):
+                assert torch.isfinite(t).all()
+
+
+def test_no_rows_and_parts_left_out():
+    import fp4_expert_gemv_b200 as fe
+    x, w, bias, res, dy = make(0, 32, 64, "none")
+    assert fe.linear(x, w, bias=bias).shape == (0, 32)
+    dx, dw, db = fe.linear_backward(dy, x, w)
+    assert dx.shape == (0, 64) and (dw == 0).all() and (db == 0).all()
+    x, w, bias, res, dy = make(70, 32, 64, "none")
+    full = fe.linear_backward(dy, x, w)
+    for i in range(3):
+        part = fe.linear_backward(dy, x, w, need_dx=i == 0, need_dw=i == 1, need_db=i == 2)
+        assert [t is None for t in part] == [j != i for j in range(3)]
+        assert torch.equal(part[i], full[i])
+
+
+def test_gradient_against_differences():
+    """<gradient, direction> against central differences of the 64-bit forward at the saved z (the bf16
+    rounding of z moves the point where the slope is taken: |act''| <= 1.1 times 2^-8 |z| per element;
+    dz and the outputs are rounded once each: 2 * 2^-8 of the summed magnitudes)."""
+    import fp4_expert_gemv_b200 as fe
+    x, w, bias, _, dy = make(24, 32, 48, "gelu", seed=8)
+    z = torch.empty(24, 32, dtype=bf, device="cuda")
+    fe.linear(x, w, bias=bias, act=fe.ACT_GELU, z=z)
+    got = dict(zip(("x", "w", "bias"), fe.linear_backward(dy, x, w, z=z, act=fe.ACT_GELU)))
+    base = dict(x=x.double(), w=w.double(), bias=bias.double())
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    for name in base:
+        dirn = torch.randn(base[name].shape, generator=gen, device="cuda", dtype=torch.float64)
+        f = []
+        for s in (1, -1):
+            v = {**base, name: base[name] + s * 1e-4 * dirn}
+            f.append(float((ref.act_parts("gelu", v["x"] @ v["w"].t() + v["bias"])[0] * dy.double()).sum()))
+        # slope of the loss along the direction through each element of z
+        dz_dir = dict(x=lambda: dirn @ base["w"].t(), w=lambda: base["x"] @ dirn.t(), bias=lambda: dirn.expand(24, 32))[name]()
+        tol = 2.0 ** -8 * float((1.1 * z.double().abs() * (dy.double() * dz_dir).abs()).sum())
+        tol += 2.0 ** -8 * float((dy.double().abs() * 1.13 * dz_dir.abs()).sum())
+        tol += 2.0 ** -8 * float((got[name].double() * dirn).abs().sum()) + 1e-5
+        assert abs((f[0] - f[1]) / 2e-4 - float((got[name].double() * dirn).sum())) <= tol, name
+
+
+def test_streams_and_graphs():
+    import fp4_expert_gemv_b200 as fe
+    x, w, bias, res, dy = make(384, 512, 256, "swiglu", seed=3)
+    x1 = x[:2].contiguous()
+
+    def step(stream=None):
+        z = torch.empty(384, 512, dtype=bf, device="cuda")
+        y = fe.linear(x, w, bias=bias, act=fe.ACT_SWIGLU, residual=res, z=z, stream=stream)
+        return (y, z, fe.linear(x1, w, act=fe.ACT_SWIGLU, stream=stream),
+                *fe.linear_backward(dy, x, w, z=z, act=fe.ACT_SWIGLU, stream=stream))
+
+    first = step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(3):   # the two streams' products may share the SMs
+        with torch.cuda.stream(side):
+            got.append(step())
+        got.append(step())
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = step()
+        graphs.append((g, out))
+    for g, out in graphs:
+        g.replay()
+        got.append(out)
+    torch.cuda.synchronize()
+    for out in got:
+        assert all(torch.equal(a, b) for a, b in zip(first, out))
+    assert fe.op_status() == (fe.FE_OK, 0)
+
+
+def test_refusals():
+    import fp4_expert_gemv_b200 as fe
+    x, w, bias, res, dy = make(16, 32, 64, "none")
+    with pytest.raises(ValueError):
+        fe.linear(x.t().contiguous().t(), w)
+    with pytest.raises(ValueError):
+        fe.linear(x.float(), w)
+    with pytest.raises(ValueError):
+        fe.linear(x, w, residual=res[:, :16])
+    with pytest.raises(ValueError):
+        fe.linear(x, w, z=torch.empty(16, 30, dtype=bf, device="cuda"))
+    with pytest.raises(fe.FeMoeError):
+        fe.linear(x[:, :60].contiguous(), w[:, :60].contiguous())
+    with pytest.raises(fe.FeMoeError):
+        fe.linear(x[:, 4:60], w[:, :56].contiguous())      # rows not on 16 bytes
+    with pytest.raises(fe.FeMoeError):
+        fe.linear(x, w, y=x[:, :32])
