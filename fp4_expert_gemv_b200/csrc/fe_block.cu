@@ -235,7 +235,7 @@ fe_status check_linear_shape(int64_t M, int N, int K, int act)
     if (M < 0 || N < 1 || K < 1 || !act_ok(act, N)) return FE_ERR_INVALID_ARG;
     // TMA rows are multiples of 16 bytes; tile counts and coordinates are 32-bit
     if (K % 8 != 0 || M > INT32_MAX - 256 || N > INT32_MAX - 256 || K > INT32_MAX - 256 ||
-        (M / fe::kLinM + 1) * (int64_t)(N / 128 + 1) > INT32_MAX / 2)
+        (M / 128 + 1) * (int64_t)(std::max(N, K) / 64 + 1) > INT32_MAX / 4)
         return FE_ERR_UNSUPPORTED;
     return FE_OK;
 }
@@ -257,17 +257,17 @@ EncodeFn encode_fn()
     return fn;
 }
 
-// Map over a bf16 matrix [rows][cols] with row stride ld (elements): boxes of 64 x 64, 128-byte
-// swizzle, zeros outside.
-cudaError_t tensor_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld)
+// Map over a bf16 matrix [rows][cols] with row stride ld (elements), boxes of bc columns x br rows in
+// the swizzle of their row's bytes; zeros outside, nothing stored there.
+cudaError_t tensor_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int64_t ld, int bc, int br)
 {
     EncodeFn fn = encode_fn();
     if (!fn) return cudaErrorNotSupported;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)(rows > 1 ? ld : (cols + 7) / 8 * 8) * 2};
-    const cuuint32_t box[2] = {64, 64}, es[2] = {1, 1};
+    const cuuint32_t box[2] = {(cuuint32_t)bc, (cuuint32_t)br}, es[2] = {1, 1};
     const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, es,
-                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, bc == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -277,64 +277,213 @@ struct Matrix {
     int64_t rows, cols, ld;
 };
 
-// D [M][N] = A B^T.  a_mn: A is stored [K][M]; b_mn: B is stored [K][N].
-cudaError_t lin_problem(fe::LinProblem* p, const Matrix& a, bool a_mn, const Matrix& b, bool b_mn, int M, int N, int K)
+// D [M][N] = A B^T with its operands as stored: a_mn: A is [K][M]; b_mn: B is [K][N].
+struct Product {
+    Matrix a, b;
+    bool a_mn, b_mn;
+    int M, N, K;
+};
+
+// Rows of 16 bytes: what a TMA box needs of its matrix.
+bool tma_rows(const void* p, int64_t rows, int64_t ld) { return aligned(p, 16) && (rows <= 1 || ld % 8 == 0); }
+
+// CTA pairs that run at once (looked up once per device and kernel).
+template <int BN, bool PLAIN>
+cudaError_t lin_pairs(int* pairs)
 {
-    *p = fe::LinProblem{};
-    p->M = M;
-    p->N = N;
-    p->K = K;
-    p->a_mn = a_mn;
-    p->b_mn = b_mn;
-    p->cols = N;
-    cudaError_t e = tensor_map(&p->ta, a.p, a.rows, a.cols, a.ld);
-    if (e == cudaSuccess) e = tensor_map(&p->tb, b.p, b.rows, b.cols, b.ld);
-    return e;
+    static std::atomic<int> known[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    int n = known[dev].load(std::memory_order_acquire);
+    if (n == 0) {
+        e = cudaFuncSetAttribute(fe::linear_gemm_kernel<BN, PLAIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)fe::kLinSmem);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(fe::kLinThreads);
+        cfg.dynamicSmemBytes = fe::kLinSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&n, fe::linear_gemm_kernel<BN, PLAIN>, &cfg);
+        if (e != cudaSuccess) return e;
+        if (n < 1) return cudaErrorLaunchOutOfResources;
+        n = std::min(n, fe::kLinMaxPairs);
+        known[dev].store(n, std::memory_order_release);
+    }
+    *pairs = n;
+    return cudaSuccess;
 }
 
-void lin_tiles(fe::LinProblem* p, int BN)
+// Shares out two problems' tiles, the first's (fewer and longer) evenly, the second's so that the pairs
+// end together: the smallest finish time, found by bisection, that has room for all of them.
+void lin_share(fe::LinParams& P, int pairs)
 {
-    p->tiles_m = (p->M + fe::kLinM - 1) / fe::kLinM;
-    const int w = p->act == FE_ACT_SWIGLU ? BN / 2 : BN;
-    p->tiles_n = (p->cols + w - 1) / w;
+    const int64_t ca = (P.p[0].K + 63) / 64 + 2, cb = (P.p[1].K + 63) / 64 + 2;   // k steps, and a tile's ends
+    const int na = P.p[0].tiles, nb = P.p[1].tiles;
+    auto load = [&](int c) { return (int64_t)(na / pairs + (c < na % pairs ? 1 : 0)) * ca; };
+    const int64_t la = load(0), lb = load(pairs - 1);
+    const int xa = na % pairs;
+    auto room = [&](int64_t L) {
+        return (L > la ? (L - la) / cb : 0) * xa + (L > lb ? (L - lb) / cb : 0) * (pairs - xa);
+    };
+    int64_t lo = 0, hi = la + cb * ((int64_t)nb + 1);
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) / 2;
+        if (room(mid) >= nb) hi = mid;
+        else lo = mid + 1;
+    }
+    int ta = 0, tb = 0;
+    for (int c = 0; c < pairs; ++c) {
+        P.start[0][c] = ta;
+        P.start[1][c] = tb;
+        ta += na / pairs + (c < xa ? 1 : 0);
+        const int64_t l = load(c);
+        tb += (int)std::min<int64_t>(nb - tb, lo > l ? (lo - l) / cb : 0);
+    }
+    P.start[0][pairs] = na;
+    P.start[1][pairs] = nb;
 }
 
-template <int BN>
-cudaError_t lin_launch(const fe::LinParams& P, int sms, cudaStream_t s)
+int lin_tile_cols(const fe::LinProblem& p, int BN) { return p.act == FE_ACT_SWIGLU ? BN / 2 : BN; }
+
+template <int BN, bool PLAIN>
+cudaError_t lin_launch(fe::LinParams& P, const Product* f, int n, cudaStream_t s)
+{
+    int pairs = 0;
+    cudaError_t e = lin_pairs<BN, PLAIN>(&pairs);
+    P.n = n;
+    int tiles = 0;
+    for (int i = 0; i < n && e == cudaSuccess; ++i) {
+        fe::LinProblem& p = P.p[i];
+        const int w = lin_tile_cols(p, BN);
+        p.tiles_n = (p.cols + w - 1) / w;
+        p.tiles = p.tiles_n * ((p.M + fe::kLinM - 1) / fe::kLinM);
+        tiles += p.tiles;
+        e = tensor_map(&p.ta, f[i].a.p, f[i].a.rows, f[i].a.cols, f[i].a.ld, 64, p.a_mn ? 64 : 128);
+        if (e == cudaSuccess)
+            e = tensor_map(&p.tb, f[i].b.p, f[i].b.rows, f[i].b.cols, f[i].b.ld, 64, p.b_mn ? 64 : BN / 2);
+        if (e == cudaSuccess && p.vec_out) e = tensor_map(&p.to, p.out, p.M, p.cols, p.ldo, 32, 32);
+        if (e == cudaSuccess && p.vec_res) e = tensor_map(&p.tr, p.res, p.M, p.cols, p.ldr, 32, 32);
+        if (e == cudaSuccess && p.vec_z) e = tensor_map(&p.tz, p.z, p.M, p.N, p.N, 32, 32);
+    }
+    if (e != cudaSuccess) return e;
+    pairs = std::min(pairs, tiles);
+    if (n == 2) lin_share(P, pairs);
+    return launch(fe::linear_gemm_kernel<BN, PLAIN>, dim3(2 * pairs), dim3(fe::kLinThreads), fe::kLinSmem, s, P);
+}
+
+// Runs one product, or two in one launch, with the epilogues already in P.p.
+cudaError_t lin_run(fe::LinParams& P, const Product* f, int n, cudaStream_t s)
+{
+    for (int i = 0; i < n; ++i) {
+        fe::LinProblem& p = P.p[i];
+        p.M = f[i].M;
+        p.N = f[i].N;
+        p.K = f[i].K;
+        p.a_mn = f[i].a_mn;
+        p.b_mn = f[i].b_mn;
+        p.vec_out = tma_rows(p.out, p.M, p.ldo);
+        p.vec_res = p.res && tma_rows(p.res, p.M, p.ldr);
+        p.vec_z = p.z && tma_rows(p.z, p.M, p.N) && (p.act != FE_ACT_SWIGLU || p.cols % 8 == 0);
+    }
+    // The tile width whose busiest pair has least to do.  A k step of 256 columns takes 512 cycles of
+    // products; narrower ones less, but a little more per column (A is read as often).
+    int pairs = 0;
+    const cudaError_t e = lin_pairs<256, true>(&pairs);
+    if (e != cudaSuccess) return e;
+    const int widths[3] = {256, 192, 128};
+    const int64_t cost[3] = {512, 392, 272};
+    int best = 0;
+    int64_t least = INT64_MAX;
+    for (int w = 0; w < 3; ++w) {
+        int64_t total = 0, longest = 0;
+        for (int i = 0; i < n; ++i) {
+            const int tc = lin_tile_cols(P.p[i], widths[w]);
+            const int64_t tiles = (int64_t)((P.p[i].cols + tc - 1) / tc) * ((P.p[i].M + fe::kLinM - 1) / fe::kLinM);
+            const int64_t steps = (P.p[i].K + 63) / 64 + 2;
+            if (n == 1) total = (tiles + pairs - 1) / pairs * steps * pairs;
+            else total += tiles * steps;
+            longest = std::max(longest, steps);
+        }
+        const int64_t c = std::max((total + pairs - 1) / pairs, longest) * cost[w];
+        if (c < least) {
+            least = c;
+            best = w;
+        }
+    }
+    bool plain = true;   // nothing but the product: the lean epilogue
+    for (int i = 0; i < n; ++i) plain &= P.p[i].act == FE_ACT_NONE && !P.p[i].bias && !P.p[i].res && !P.p[i].z;
+    if (plain)
+        return best == 0   ? lin_launch<256, true>(P, f, n, s)
+               : best == 1 ? lin_launch<192, true>(P, f, n, s)
+                           : lin_launch<128, true>(P, f, n, s);
+    return best == 0   ? lin_launch<256, false>(P, f, n, s)
+           : best == 1 ? lin_launch<192, false>(P, f, n, s)
+                       : lin_launch<128, false>(P, f, n, s);
+}
+
+// Products of few tiles, the contraction split over clusters.
+cudaError_t split_launch(const fe::LinProblem& q, const Product& f, int splits, cudaStream_t s)
 {
     static std::atomic<bool> ready[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (dev < 0 || dev >= 64 || !ready[dev].load(std::memory_order_relaxed)) {
-        e = cudaFuncSetAttribute(fe::linear_gemm_kernel<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)fe::lin_smem_bytes(BN));
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(fe::linear_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)fe::kSplSmem);
         if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_relaxed);
+        ready[dev].store(true, std::memory_order_release);
     }
-    return launch(fe::linear_gemm_kernel<BN>, std::min(P.tiles, sms), fe::kLinThreads, fe::lin_smem_bytes(BN), s, P);
+    fe::LinSplitParams p{};
+    e = tensor_map(&p.ta, f.a.p, f.a.rows, f.a.cols, f.a.ld, 64, 128);
+    if (e == cudaSuccess) e = tensor_map(&p.tb, f.b.p, f.b.rows, f.b.cols, f.b.ld, 64, 32);
+    if (e != cudaSuccess) return e;
+    p.M = f.M;
+    p.N = f.N;
+    p.K = f.K;
+    p.splits = splits;
+    p.act = q.act;
+    p.cols = q.cols;
+    p.bias = q.bias;
+    p.res = q.res;
+    p.ldr = q.ldr;
+    p.out = q.out;
+    p.ldo = q.ldo;
+    p.z = q.z;
+    const int w = lin_tile_cols(q, fe::kSplN);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((q.cols + w - 1) / w, (f.M + 127) / 128, splits);
+    cfg.blockDim = dim3(fe::kSplThreads);
+    cfg.dynamicSmemBytes = fe::kSplSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = splits;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, fe::linear_split_kernel, p);
 }
 
-// The tile width: with 256 columns a k step moves the fewest bytes per product, with 128 there are
-// more tiles to spread; the one whose longest-loaded SM has less to do runs.
-cudaError_t lin_run(fe::LinParams& P, int n, cudaStream_t s)
+// CTAs that share a tile's contraction: as many (a power of two, to 8) as fill the SMs and leave each at
+// least two k steps; 0 if the tiles alone fill them.
+int split_ways(const fe::LinProblem& q, const Product& f, int sms)
 {
-    const int sms = sm_count();
-    if (sms < 1) return cudaErrorInvalidDevice;
-    int64_t work[2];
-    for (int w = 0; w < 2; ++w) {
-        int64_t tiles = 0;
-        for (int i = 0; i < n; ++i) {
-            lin_tiles(&P.p[i], w ? 256 : 128);
-            tiles += (int64_t)P.p[i].tiles_m * P.p[i].tiles_n;
-        }
-        work[w] = (tiles + sms - 1) / sms * (w ? 2 : 1);
-    }
-    const int BN = work[1] <= work[0] ? 256 : 128;
-    for (int i = 0; i < n; ++i) lin_tiles(&P.p[i], BN);
-    P.tiles0 = P.p[0].tiles_m * P.p[0].tiles_n;
-    P.tiles = P.tiles0 + (n > 1 ? P.p[1].tiles_m * P.p[1].tiles_n : 0);
-    return BN == 256 ? lin_launch<256>(P, sms, s) : lin_launch<128>(P, sms, s);
+    const int w = lin_tile_cols(q, fe::kSplN);
+    const int64_t tiles = (int64_t)((q.cols + w - 1) / w) * ((f.M + 127) / 128);
+    if (tiles > sms) return 0;
+    int n = 1;
+    while (n < 8 && tiles * 2 * n <= sms && (f.K + 63) / 64 >= 4 * n) n *= 2;
+    return n;
 }
 
 template <bool GLU>
@@ -609,8 +758,8 @@ fe_status fe_moe_linear(const void* x, int64_t ldx, const void* w, const void* b
         FE_CUDA_TRY(act == FE_ACT_SWIGLU ? rows_launch<true>(p, s) : rows_launch<false>(p, s));
         return FE_OK;
     }
+    const Product f{{x, M, K, ldx}, {w, N, K, K}, false, false, (int)M, N, K};
     fe::LinParams P{};
-    FE_CUDA_TRY(lin_problem(&P.p[0], {x, M, K, ldx}, false, {w, N, K, K}, false, (int)M, N, K));
     fe::LinProblem& p = P.p[0];
     p.act = act;
     p.cols = cols;
@@ -620,9 +769,11 @@ fe_status fe_moe_linear(const void* x, int64_t ldx, const void* w, const void* b
     p.out = static_cast<uint16_t*>(y);
     p.ldo = ldy;
     p.z = static_cast<uint16_t*>(z);
-    p.vec = aligned(y, 16) && ldy % 8 == 0 && (!residual || (aligned(residual, 16) && ldr % 8 == 0)) &&
-            (!z || (aligned(z, 16) && N % 8 == 0 && cols % 8 == 0));
-    FE_CUDA_TRY(lin_run(P, 1, s));
+    const int sms = sm_count();
+    if (sms < 1) return record_cuda(cudaErrorInvalidDevice, "device");
+    const int ways = split_ways(p, f, sms);
+    if (ways > 0) FE_CUDA_TRY(split_launch(p, f, ways, s));
+    else FE_CUDA_TRY(lin_run(P, &f, 1, s));
     return FE_OK;
 }
 
@@ -703,22 +854,22 @@ fe_status fe_moe_linear_backward(const void* dy, int64_t lddy, const void* x, in
     if (!dx && !dw) return FE_OK;
     // dW [N][K] = dZ^T X (longest tiles first), dX [M][K] = dZ W: one launch
     fe::LinParams P{};
+    Product prod[2];
     int n = 0;
     if (dw) {
-        FE_CUDA_TRY(lin_problem(&P.p[n], {dz, M, N, lddz}, true, {x, M, K, ldx}, true, N, K, (int)M));
+        prod[n] = {{dz, M, N, lddz}, {x, M, K, ldx}, true, true, N, K, (int)M};
         P.p[n].out = static_cast<uint16_t*>(dw);
-        P.p[n].ldo = K;
-        P.p[n].vec = aligned(dw, 16);
+        P.p[n].ldo = P.p[n].cols = K;
         ++n;
     }
     if (dx) {
-        FE_CUDA_TRY(lin_problem(&P.p[n], {dz, M, N, lddz}, false, {w, N, K, K}, true, (int)M, K, N));
+        prod[n] = {{dz, M, N, lddz}, {w, N, K, K}, false, true, (int)M, K, N};
         P.p[n].out = static_cast<uint16_t*>(dx);
         P.p[n].ldo = lddx;
-        P.p[n].vec = aligned(dx, 16) && lddx % 8 == 0;
+        P.p[n].cols = K;
         ++n;
     }
-    FE_CUDA_TRY(lin_run(P, n, s));
+    FE_CUDA_TRY(lin_run(P, prod, n, s));
     return FE_OK;
 }
 

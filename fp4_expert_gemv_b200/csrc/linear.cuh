@@ -51,23 +51,25 @@ FE_DEV float act_bwd(int act, float z)
 
 // ---- tensor-core tiles ---------------------------------------------------------------
 
-constexpr int kLinThreads = 256;   // warp 0: TMA, 1: MMA, 2: TMEM, 4-7: epilogue
-constexpr int kLinM = 128;
-constexpr uint32_t kLinBox = 64 * 128;   // one TMA box: 64 rows of 128 bytes
 constexpr unsigned long long kLinTimeoutNs = 2000ull * 1000 * 1000;
-
-__host__ __device__ constexpr int lin_stages(int BN) { return BN == 256 ? 4 : 6; }
-__host__ __device__ constexpr uint32_t lin_stage_bytes(int BN) { return kLinM * 128 + BN * 128; }
-__host__ __device__ constexpr uint32_t lin_smem_bytes(int BN)
-{
-    return 1024 + lin_stages(BN) * lin_stage_bytes(BN) + 8 * (2 * lin_stages(BN) + 4) + 16;
-}
+constexpr int kLinThreads = 384;         // warp 0: TMA, 1: MMA, 2: TMEM, 4-11: epilogue
+constexpr int kLinM = 256;               // rows of a tile: 128 in each CTA of the pair
+constexpr int kLinStages = 5;
+constexpr uint32_t kLinABytes = 128 * 128;   // one k step of 64: 128 rows of 128 bytes
+constexpr uint32_t kLinBBytes = 128 * 128;   // at most BN / 2 = 128 columns' rows
+constexpr uint32_t kLinStage = kLinABytes + kLinBBytes;
+constexpr int kLinSlots = 4;                 // output staging of a warp: 32 rows x 32 columns of bf16 each
+constexpr uint32_t kLinSlotBytes = 32 * 64;
+constexpr int kLinMaxPairs = 128;
+constexpr int kLinBars = 2 * kLinStages + 4 + 16;
+constexpr uint32_t kLinSmem = 1024 + kLinStages * kLinStage + 8 * kLinSlots * kLinSlotBytes + 8 * kLinBars + 16;
 
 struct LinProblem {
-    CUtensorMap ta, tb;      // boxes of 64 x 64, 128-byte swizzle
+    CUtensorMap ta, tb;      // operand boxes: 64 of k x rows (K-major), 64 x 64 of k (across)
+    CUtensorMap to, tr, tz;  // out, res and z: boxes of 32 columns x 32 rows
     int M, N, K;             // D [M][N] = A [M][K] B [N][K]^T
     int a_mn, b_mn;          // operand stored across the contraction: A as [K][M], B as [K][N]
-    int tiles_m, tiles_n;
+    int tiles_n, tiles;
     int act;
     int cols;                // output columns: N, or N / 2 for swiglu
     const uint16_t* bias;    // [N] or null
@@ -76,12 +78,13 @@ struct LinProblem {
     uint16_t* out;           // [M][ldo]
     int64_t ldo;
     uint16_t* z;             // [M][N] or null
-    int vec;                 // out, res and z rows take 16-byte accesses
+    int vec_out, vec_res, vec_z;   // rows suit TMA (16-byte aligned base and stride)
 };
 
 struct LinParams {
     LinProblem p[2];
-    int tiles0, tiles;       // tiles of p[0], of both
+    int n;                   // problems
+    int start[2][kLinMaxPairs + 1];   // n == 2: pair c takes tiles [start[i][c], start[i][c + 1]) of problem i
 };
 
 FE_DEV void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
@@ -92,16 +95,116 @@ FE_DEV void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint
         : "memory");
 }
 
+// The same, completing on a barrier of either CTA of the pair.
+FE_DEV void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+FE_DEV void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src)
+{
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n\t"
+                 "cp.async.bulk.commit_group;" ::"l"(map), "r"(x), "r"(y), "r"(src)
+                 : "memory");
+}
+
+template <int N>
+FE_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
+
+// Bounded wait for phase `parity` of an mbarrier by a thread that suspends meanwhile: the products run
+// at the power limit, where polling warps cost clocks.
+FE_DEV bool lin_wait(uint32_t bar, uint32_t parity)
+{
+    unsigned long long t0 = 0;
+    for (int it = 0;; ++it) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(20000u)
+            : "memory");
+        if (ok) return true;
+        if (it == 0) t0 = globaltimer_ns();
+        else if (globaltimer_ns() - t0 > kLinTimeoutNs) return false;
+    }
+}
+
+// The same by every lane of a warp, with one answer.
+FE_DEV bool lin_wait_warp(uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, lin_wait(bar, parity)); }
+
+// One lane of a converged warp.  The producer and MMA warps run their loops with every lane and pick
+// the issuing one only around the instruction, so that addresses and descriptors stay warp-uniform: a
+// loop entered by lane 0 alone took 720 cycles per k step whatever the tile's width.
+FE_DEV bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+FE_DEV uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+FE_DEV void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// This CTA's shared address as seen in CTA `rank` of the cluster.
+FE_DEV uint32_t cluster_map(uint32_t saddr, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+    return r;
+}
+
+FE_DEV void expect_tx(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
 // Descriptor of an operand stored across the contraction: boxes of 64 (M or N) x 64 k, one 128-byte
 // row per k, 8-k groups 1024 bytes apart, the next 64 of M or N one box further.
 FE_DEV uint64_t lin_desc_mn(uint32_t saddr)
 {
     uint64_t d = (uint64_t)((saddr >> 4) & 0x3FFFu);
-    d |= (uint64_t)(kLinBox >> 4) << 16;
+    d |= (uint64_t)(8192u >> 4) << 16;
     d |= (uint64_t)(1024u >> 4) << 32;
     d |= (uint64_t)1u << 46;
     d |= (uint64_t)2u << 61;
     return d;
+}
+
+// f32 accumulator, bf16 operands, which of them lie across the contraction, N and M.
+FE_DEV uint32_t lin_idesc(int a_mn, int b_mn, int M, int N)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) | ((uint32_t)(N >> 3) << 17) |
+           ((uint32_t)(M >> 4) << 24);
+}
+
+FE_DEV void tc_mma_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+
+// Arrives on the barrier at this offset in both CTAs once the MMAs so far are done.
+FE_DEV void tc_commit_pair(uint32_t mbar)
+{
+    asm volatile(
+        "{\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\t"
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(mbar)
+        : "memory");
 }
 
 FE_DEV void tc_ld32(uint32_t taddr, uint32_t (&r)[32])
@@ -116,30 +219,14 @@ FE_DEV void tc_ld32(uint32_t taddr, uint32_t (&r)[32])
         : "r"(taddr));
 }
 
-// 32 consecutive columns from c0 of one row: dst[c0 + j] = bf16(v[j]) for c0 + j < cols.
-FE_DEV void lin_store32(uint16_t* dst, int c0, int cols, bool vec, const float (&v)[32])
+// v[j] += bias[c0 + j] for c0 + j < cols; every lane has the same columns.
+FE_DEV void lin_add_bias(const uint16_t* bias, int c0, int cols, float (&v)[32])
 {
-    if (vec && c0 + 32 <= cols) {
-        uint4* d = reinterpret_cast<uint4*>(dst + c0);
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            d[q] = make_uint4(bf16x2_rn(v[8 * q], v[8 * q + 1]), bf16x2_rn(v[8 * q + 2], v[8 * q + 3]),
-                              bf16x2_rn(v[8 * q + 4], v[8 * q + 5]), bf16x2_rn(v[8 * q + 6], v[8 * q + 7]));
-    } else {
-#pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (c0 + j < cols) dst[c0 + j] = (uint16_t)(bf16x2_rn(v[j], 0.0f) & 0xffffu);
-    }
-}
-
-// v[j] += src[c0 + j] (bf16) for c0 + j < cols.
-FE_DEV void lin_add32(const uint16_t* src, int c0, int cols, bool vec, float (&v)[32])
-{
-    if (vec && c0 + 32 <= cols) {
-        const uint4* s = reinterpret_cast<const uint4*>(src + c0);
+    const uint16_t* b = bias + c0;
+    if (c0 + 32 <= cols && (reinterpret_cast<uintptr_t>(b) & 15) == 0) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const uint4 w = s[q];
+            const uint4 w = __ldg(reinterpret_cast<const uint4*>(b) + q);
             const uint32_t a[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -150,28 +237,121 @@ FE_DEV void lin_add32(const uint16_t* src, int c0, int cols, bool vec, float (&v
     } else {
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-            if (c0 + j < cols) v[j] += bf16_bits_to_f32(src[c0 + j]);
+            if (c0 + j < cols) v[j] += bf16_bits_to_f32(b[j]);
     }
 }
 
-template <int BN>
-__global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __grid_constant__ LinParams P)
+// A staging slot holds 32 rows of 32 bf16 (64 bytes) in TMA's 64-byte swizzle: 16-byte chunk c of row
+// r is stored at chunk c ^ (r / 2 % 4), so the eight rows of an access phase use every bank once.
+FE_DEV uint32_t lin_slot_chunk(int r, int c) { return (uint32_t)r * 64u + (uint32_t)((c ^ ((r >> 1) & 3)) << 4); }
+
+// The epilogue's view of one warp's staging: 32 x 32 blocks of bf16 go out (or a residual comes in)
+// through slots, by TMA where the matrix suits it, else row by row with the lanes along a row.
+struct LinStage {
+    uint8_t* base;
+    uint32_t saddr;
+    uint32_t ny;   // slots given out to y
+
+    // A slot may be written again once at most `pending` of the latest stores still read theirs.
+    template <int PENDING>
+    FE_DEV void settle() const
+    {
+        if ((threadIdx.x & 31) == 0) bulk_wait_read<PENDING>();
+        __syncwarp();
+    }
+
+    FE_DEV void put(int slot, int lane, const float (&v)[32]) const
+    {
+        uint8_t* p = base + slot * kLinSlotBytes;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<uint4*>(p + lin_slot_chunk(lane, q)) =
+                make_uint4(bf16x2_rn(v[8 * q], v[8 * q + 1]), bf16x2_rn(v[8 * q + 2], v[8 * q + 3]),
+                           bf16x2_rn(v[8 * q + 4], v[8 * q + 5]), bf16x2_rn(v[8 * q + 6], v[8 * q + 7]));
+    }
+
+    FE_DEV void add(int slot, int lane, float (&v)[32]) const
+    {
+        const uint8_t* p = base + slot * kLinSlotBytes;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const uint4 w = *reinterpret_cast<const uint4*>(p + lin_slot_chunk(lane, q));
+            const uint32_t a[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[8 * q + 2 * j] += __uint_as_float(a[j] << 16);
+                v[8 * q + 2 * j + 1] += __uint_as_float(a[j] & 0xffff0000u);
+            }
+        }
+    }
+
+    FE_DEV uint16_t* at(int slot, int r, int col) const
+    {
+        return reinterpret_cast<uint16_t*>(base + slot * kLinSlotBytes + lin_slot_chunk(r, col >> 3)) + (col & 7);
+    }
+
+    // Block (row0, col0) of a matrix with row stride ld from a slot; columns from `limit` on are not the
+    // block's (the matrix ends there, where TMA stops by itself, or a swiglu z's other half begins).
+    FE_DEV void flush(int slot, int lane, const CUtensorMap* map, bool vec, bool ends, uint16_t* m, int64_t ld, int row0,
+                      int rows, int col0, int limit) const
+    {
+        if (vec && (ends || col0 + 32 <= limit)) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) tma_store_2d(map, col0, row0, saddr + slot * kLinSlotBytes);
+        } else {
+            __syncwarp();
+            if (col0 + lane < limit)
+                for (int r = 0; r < 32 && row0 + r < rows; ++r) m[(size_t)(row0 + r) * ld + col0 + lane] = *at(slot, r, lane);
+            __syncwarp();
+        }
+    }
+
+    FE_DEV void fill(int slot, int lane, const uint16_t* m, int64_t ld, int row0, int rows, int col0, int cols) const
+    {
+        for (int r = 0; r < 32; ++r)
+            *at(slot, r, lane) = row0 + r < rows && col0 + lane < cols ? m[(size_t)(row0 + r) * ld + col0 + lane] : 0;
+        __syncwarp();
+    }
+};
+
+// The tiles of problem i that a CTA pair works on: round robin over a single problem, its share of two.
+struct LinRange {
+    int t, end, step;
+    FE_DEV LinRange(const LinParams& P, int i, int pair, int pairs)
+        : t(P.n == 1 ? pair : P.start[i][pair]), end(P.n == 1 ? P.p[i].tiles : P.start[i][pair + 1]), step(P.n == 1 ? pairs : 1)
+    {
+    }
+};
+
+// 256 x BN output tiles by pairs of CTAs (one MMA over two SMs: each holds 128 rows of A and half of
+// B's columns, so a k step moves 32 KB into each SM for 512 cycles of products; a single CTA's
+// 128 x 256 tile would move 48 KB and measured 20 % slower).
+template <int BN, bool PLAIN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
+    linear_gemm_kernel(const __grid_constant__ LinParams P)
 {
-    constexpr int S = lin_stages(BN);
-    constexpr uint32_t kStage = lin_stage_bytes(BN);
+    constexpr int S = kLinStages;
+    constexpr int kAccStride = 256;
+    constexpr uint32_t kTmemCols = BN > 128 ? 512 : 256;
+    constexpr uint32_t kAccCol = BN > 128 ? kAccStride : 128;
     extern __shared__ uint8_t lin_dyn[];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const uint32_t rank = cluster_rank();
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     const uint32_t base0 = tc_saddr(lin_dyn);
     uint8_t* sm = lin_dyn + ((1024u - (base0 & 1023u)) & 1023u);
     const uint32_t ring = tc_saddr(sm);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S * kStage);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 4);
+    uint8_t* staging = sm + S * kLinStage;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(staging + 8 * kLinSlots * kLinSlotBytes);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kLinBars);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const uint32_t bar0 = tc_saddr(bars);
-    auto full = [&](int s) { return bar0 + 8u * s; };
-    auto empty = [&](int s) { return bar0 + 8u * (S + s); };
-    auto accfull = [&](int s) { return bar0 + 8u * (2 * S + s); };
-    auto accempty = [&](int s) { return bar0 + 8u * (2 * S + 2 + s); };
+    auto full = [&](int s) { return bar0 + 8u * s; };                   // pair's leader: bytes of both CTAs landed
+    auto empty = [&](int s) { return bar0 + 8u * (S + s); };            // both: the stage's MMAs are done
+    auto accfull = [&](int s) { return bar0 + 8u * (2 * S + s); };      // both: a tile's products are done
+    auto accempty = [&](int s) { return bar0 + 8u * (2 * S + 2 + s); }; // leader: both CTAs drained it
+    auto resfull = [&](int w, int s) { return bar0 + 8u * (2 * S + 4 + 2 * w + s); };
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
             tc_mbar_init(full(s), 1);
@@ -179,13 +359,307 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
         }
         for (int s = 0; s < 2; ++s) {
             tc_mbar_init(accfull(s), 1);
-            tc_mbar_init(accempty(s), 4);
+            tc_mbar_init(accempty(s), 16);
         }
+        for (int w = 0; w < 16; ++w) tc_mbar_init(resfull(0, w), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         *abort = 0;
     }
     if (warp == 2) {
-        tc_alloc(tc_saddr(tmem_slot), 2 * BN);
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc_saddr(tmem_slot)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // both CTAs' barriers are ready before either signals the other
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    griddep_wait();
+
+    if (warp == 0) {
+        // ---- producer: this CTA's boxes of A and B into its ring, reported to the leader ------------
+        uint32_t it = 0;
+        for (int i = 0; i < P.n; ++i) {
+            const LinProblem& p = P.p[i];
+            const int nk = (p.K + 63) / 64, tiles_n = p.tiles_n, a_mn = p.a_mn, b_mn = p.b_mn, cols = p.cols;
+            const bool glu = p.act == kActSwiglu;
+            const CUtensorMap *ta = &p.ta, *tb = &p.tb;
+            const uint32_t bytes = 2 * (kLinABytes + (b_mn ? (BN / 2 + 63) / 64 * 8192u : BN / 2 * 128u));
+            for (LinRange g(P, i, pair, pairs); g.t < g.end && !*abort; g.t += g.step) {
+                const int m0 = g.t / tiles_n * kLinM + 128 * rank, tn = g.t % tiles_n;
+                // swiglu: the leader's columns are gate rows of W, the other's the up rows of the same
+                // output columns
+                const int n0 = glu ? tn * (BN / 2) + (rank ? cols : 0) : tn * BN + (BN / 2) * rank;
+                for (int k = 0; k < nk; ++k, ++it) {
+                    const uint32_t s = it % S;
+                    if (it >= S && !lin_wait_warp(empty(s), (it / S - 1) & 1)) {
+                        *abort = 1;
+                        break;
+                    }
+                    if (elect_one()) {
+                        if (rank == 0) expect_tx(full(s), bytes);
+                        const uint32_t bar = cluster_map(full(s), 0);
+                        const uint32_t a = ring + s * kLinStage, b = a + kLinABytes;
+                        if (a_mn) {
+                            tma_load_2d_pair(a, ta, m0, 64 * k, bar);
+                            tma_load_2d_pair(a + 8192, ta, m0 + 64, 64 * k, bar);
+                        } else {
+                            tma_load_2d_pair(a, ta, 64 * k, m0, bar);
+                        }
+                        if (b_mn) {
+#pragma unroll
+                            for (int j = 0; j < (BN / 2 + 63) / 64; ++j)
+                                tma_load_2d_pair(b + j * 8192, tb, n0 + 64 * j, 64 * k, bar);
+                        } else {
+                            tma_load_2d_pair(b, tb, 64 * k, n0, bar);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        // no copy outlives the loop: the leader sees those of both CTAs land
+        if (rank == 0)
+            for (uint32_t j = it > S ? it - S : 0; j < it; ++j) lin_wait_warp(full(j % S), (j / S) & 1);
+    } else if (warp == 1) {
+        if (rank == 0) {
+            // ---- MMA issue, for both CTAs ------------------------------------------------------------
+            uint32_t it = 0, done = 0;
+            for (int i = 0; i < P.n; ++i) {
+                const LinProblem& p = P.p[i];
+                const int nk = (p.K + 63) / 64, a_mn = p.a_mn, b_mn = p.b_mn;
+                const uint32_t idesc = lin_idesc(a_mn, b_mn, kLinM, BN);
+                const uint64_t a0 = a_mn ? lin_desc_mn(ring) : tc_smem_desc(ring);
+                const uint64_t b0 = b_mn ? lin_desc_mn(ring + kLinABytes) : tc_smem_desc(ring + kLinABytes);
+                const uint32_t as = a_mn ? 2048 / 16 : 32 / 16, bs = b_mn ? 2048 / 16 : 32 / 16;   // 16 of k further
+                for (LinRange g(P, i, pair, pairs); g.t < g.end && !*abort; g.t += g.step, ++done) {
+                    const int acc = done & 1;
+                    if (done >= 2 && !lin_wait_warp(accempty(acc), (done / 2 - 1) & 1)) *abort = 1;
+                    tc_fence_after();
+                    for (int k = 0; k < nk && !*abort; ++k, ++it) {
+                        const uint32_t s = it % S;
+                        if (!lin_wait_warp(full(s), (it / S) & 1)) {
+                            *abort = 1;
+                            break;
+                        }
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint64_t a = a0 + s * (kLinStage >> 4), b = b0 + s * (kLinStage >> 4);
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                tc_mma_pair(tmem + kAccCol * acc, a + ks * as, b + ks * bs, idesc, (k > 0 || ks > 0) ? 1u : 0u);
+                            tc_commit_pair(empty(s));
+                        }
+                        __syncwarp();
+                    }
+                    if (elect_one()) tc_commit_pair(accfull(acc));
+                    __syncwarp();
+                }
+            }
+            // never leave with MMAs in flight: they read shared memory and write TMEM
+            for (uint32_t j = done > 2 ? done - 2 : 0; j < done; ++j)
+                if (!lin_wait_warp(accfull(j & 1), (j / 2) & 1)) *abort = 1;
+        }
+    } else if (warp >= 4) {
+        // ---- epilogue: a thread per row, blocks of 32 columns through the staging slots; the two
+        // warps of a TMEM quarter take every other block (with one warp an SM sub-partition had
+        // nothing to run under its latencies: 1300 cycles a block)
+        const int ew = warp - 4, quarter = ew & 3, half = ew >> 2;
+        LinStage st{staging + ew * kLinSlots * kLinSlotBytes, tc_saddr(staging + ew * kLinSlots * kLinSlotBytes), 0};
+        uint32_t done = 0, nres = 0;
+        bool stop = false;
+        for (int i = 0; i < P.n && !stop; ++i) {
+            const LinProblem& p = P.p[i];
+            // operands in registers: the loops' memory clobbers would reload them each time
+            const int act = p.act, M = p.M, N = p.N, cols = p.cols, tiles_n = p.tiles_n;
+            const bool vec_out = p.vec_out, vec_z = p.vec_z, vec_res = p.vec_res;
+            const uint16_t *bias = p.bias, *res = p.res;
+            uint16_t *out = p.out, *zo = p.z;
+            const int64_t ldr = p.ldr, ldo = p.ldo;
+            const CUtensorMap *to = &p.to, *tr = &p.tr, *tz = &p.tz;
+            const bool glu = !PLAIN && act == kActSwiglu;
+            const int tile_cols = glu ? BN / 2 : BN;
+            st.settle<0>();   // the problem before may have used the slots another way
+            for (LinRange g(P, i, pair, pairs); g.t < g.end; g.t += g.step, ++done) {
+                const int acc = done & 1;
+                const int row0 = g.t / tiles_n * kLinM + 128 * rank + 32 * quarter, n0 = g.t % tiles_n * tile_cols;
+                const int chunks = min(tile_cols, cols - n0 + 31) / 32;   // blocks with a column to write
+                const bool live = row0 < M;
+                // a residual block is fetched one block ahead; nres counts the fetches by TMA
+                const bool has_res = !PLAIN && res && live, tma_res = has_res && vec_res;
+                auto fetch = [&](int c) {
+                    const int slot = st.ny++ & 1;
+                    st.settle<0>();
+                    if (tma_res) {
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0) {
+                            expect_tx(resfull(ew, nres & 1), kLinSlotBytes);
+                            tma_load_2d(st.saddr + slot * kLinSlotBytes, tr, n0 + 32 * c, row0, resfull(ew, nres & 1));
+                        }
+                        ++nres;
+                    } else {
+                        st.fill(slot, lane, res, ldr, row0, M, n0 + 32 * c, cols);
+                    }
+                    return slot;
+                };
+                int slot = 0;
+                if (has_res && half < chunks) slot = fetch(half);
+                if (!lin_wait_warp(accfull(acc), (done / 2) & 1)) *abort = 1;
+                stop = __any_sync(0xffffffffu, *abort != 0);
+                tc_fence_after();
+                const uint32_t t0 = tmem + ((uint32_t)(32 * quarter) << 16) + kAccCol * acc;
+#pragma unroll 1
+                for (int c = half; c < chunks; c += 2) {
+                    uint32_t r[32];
+                    float v[32];
+                    tc_ld32(t0 + 32 * c, r);
+                    const int c0 = n0 + 32 * c;
+                    tc_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+                    if (!PLAIN) {
+                        if (glu) {
+                            tc_ld32(t0 + BN / 2 + 32 * c, r);
+                            tc_wait_ld();
+                            float u[32];
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) u[j] = __uint_as_float(r[j]);
+                            if (bias) {
+                                lin_add_bias(bias, c0, cols, v);
+                                lin_add_bias(bias + cols, c0, cols, u);
+                            }
+                            if (zo && live && !stop) {   // slots 2 and 3 are z's
+                                st.settle<0>();
+                                st.put(2, lane, v);
+                                st.flush(2, lane, tz, vec_z, false, zo, N, row0, M, c0, cols);
+                                st.put(3, lane, u);
+                                st.flush(3, lane, tz, vec_z, true, zo, N, row0, M, c0 + cols, N);
+                            }
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = v[j] * sigmoidf(v[j]) * u[j];
+                        } else {
+                            if (bias) lin_add_bias(bias, c0, cols, v);
+                            if (zo && live && !stop) {
+                                st.settle<0>();
+                                st.put(2, lane, v);
+                                st.flush(2, lane, tz, vec_z, true, zo, N, row0, M, c0, cols);
+                            }
+                            if (act != kActNone) {
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) v[j] = act_fwd(act, v[j]);
+                            }
+                        }
+                        if (has_res) {
+                            const uint32_t turn = nres - 1;   // this block's fetch
+                            if (tma_res && !lin_wait_warp(resfull(ew, turn & 1), (turn >> 1) & 1)) *abort = 1;
+                            st.add(slot, lane, v);
+                            // the next block's residual goes to the other slot, whose store has been read by then
+                            if (c + 2 < chunks) {
+                                const int ahead = fetch(c + 2);
+                                if (live && !stop) {
+                                    st.put(slot, lane, v);
+                                    st.flush(slot, lane, to, vec_out, true, out, ldo, row0, M, c0, cols);
+                                }
+                                slot = ahead;
+                                continue;
+                            }
+                        }
+                    }
+                    if (live && !stop) {
+                        if (!has_res) {
+                            // all four slots go round, or two beside z's: three (one) later stores may be reading
+                            if (!PLAIN && zo) {
+                                slot = st.ny++ & 1;
+                                st.settle<0>();
+                            } else {
+                                slot = st.ny++ & 3;
+                                st.settle<3>();
+                            }
+                        }
+                        st.put(slot, lane, v);
+                        st.flush(slot, lane, to, vec_out, true, out, ldo, row0, M, c0, cols);
+                    }
+                }
+                // the accumulator is read: the products after the next may begin
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_map(accempty(acc), 0))
+                                 : "memory");
+                if (stop) break;
+            }
+        }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0 && *abort) atomicOr(&g_op_status, kDevTcTimeout);
+    cluster_sync();   // the pair's shared memory and TMEM are in use until both are here
+    if (warp == 2) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+    }
+}
+
+// ---- few tiles: the contraction split over a cluster --------------------------------------
+
+constexpr int kSplN = 64;                     // columns of a tile (swiglu: 32 gate and their 32 up columns)
+constexpr int kSplStages = 8;
+constexpr int kSplThreads = 256;               // warp 0: TMA, 1: MMA, 2: TMEM; then all finish
+constexpr uint32_t kSplStage = 128 * 128 + kSplN * 128;
+constexpr int kSplLd = kSplN + 4;             // fp32 partial rows in shared memory: 16-byte accesses of 8 rows hit every bank
+constexpr uint32_t kSplSmem = 1024 + kSplStages * kSplStage + 8 * (2 * kSplStages + 1) + 16;
+
+struct LinSplitParams {
+    CUtensorMap ta, tb;      // x: boxes of 64 k x 128 rows; w: 64 k x 32 rows
+    int M, N, K, splits, act, cols;
+    const uint16_t* bias;
+    const uint16_t* res;
+    int64_t ldr;
+    uint16_t* out;
+    int64_t ldo;
+    uint16_t* z;
+};
+
+// One 128 x 64 tile per cluster of `splits` CTAs, each over its share of the k steps; the partial
+// tiles meet through distributed shared memory, every CTA adding (in rank order) and finishing every
+// splits-th row.  For products of so few tiles that whole tiles would leave most SMs idle while the
+// weights stream through the rest.
+__global__ void __launch_bounds__(kSplThreads, 1) linear_split_kernel(const __grid_constant__ LinSplitParams p)
+{
+    constexpr int S = kSplStages;
+    extern __shared__ uint8_t lin_dyn[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int m0 = blockIdx.y * 128, tn = blockIdx.x;
+    const uint32_t rank = blockIdx.z;
+    const int nk = (p.K + 63) / 64;
+    const int k0 = (int)((int64_t)nk * rank / p.splits), k1 = (int)((int64_t)nk * (rank + 1) / p.splits);
+    const bool glu = p.act == kActSwiglu;
+    const uint32_t base0 = tc_saddr(lin_dyn);
+    uint8_t* sm = lin_dyn + ((1024u - (base0 & 1023u)) & 1023u);
+    const uint32_t ring = tc_saddr(sm);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S * kSplStage);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 1);
+    volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const uint32_t bar0 = tc_saddr(bars);
+    auto full = [&](int s) { return bar0 + 8u * s; };
+    auto empty = [&](int s) { return bar0 + 8u * (S + s); };
+    const uint32_t accfull = bar0 + 8u * 2 * S;
+    if (tid == 0) {
+        for (int s = 0; s < S; ++s) {
+            tc_mbar_init(full(s), 1);
+            tc_mbar_init(empty(s), 1);
+        }
+        tc_mbar_init(accfull, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        *abort = 0;
+    }
+    if (warp == 2) {
+        tc_alloc(tc_saddr(tmem_slot), kSplN);
         tc_relinquish();
     }
     tc_fence_before();
@@ -193,160 +667,119 @@ __global__ void __launch_bounds__(kLinThreads, 1) linear_gemm_kernel(const __gri
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     griddep_wait();
-
     if (warp == 0) {
-        if (lane == 0) {
-            // ---- producer: boxes of A and B into the ring ------------------------------------
-            uint32_t it = 0;
-            for (int tile = blockIdx.x; tile < P.tiles && !*abort; tile += gridDim.x) {
-                const LinProblem& p = P.p[tile >= P.tiles0];
-                const int ti = tile >= P.tiles0 ? tile - P.tiles0 : tile;
-                const int m0 = ti / p.tiles_n * kLinM, tn = ti % p.tiles_n;
-                const int nk = (p.K + 63) / 64;
-                for (int k = 0; k < nk; ++k, ++it) {
-                    const int s = it % S;
-                    if (it >= S && !tc_mbar_wait(empty(s), (it / S - 1) & 1, kLinTimeoutNs)) {
-                        *abort = 1;
-                        break;
-                    }
-                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full(s)), "r"(kStage)
-                                 : "memory");
-                    const uint32_t a = ring + s * kStage, b = a + kLinM * 128;
-#pragma unroll
-                    for (int i = 0; i < kLinM / 64; ++i) {
-                        const int m = m0 + 64 * i;
-                        tma_load_2d(a + i * kLinBox, &p.ta, p.a_mn ? m : 64 * k, p.a_mn ? 64 * k : m, full(s));
-                    }
-#pragma unroll
-                    for (int i = 0; i < BN / 64; ++i) {
-                        // swiglu: the first half of the tile's columns are gate rows of W, the
-                        // second the up rows of the same output columns
-                        int n = tn * BN + 64 * i;
-                        if (p.act == kActSwiglu)
-                            n = tn * (BN / 2) + 64 * (i % (BN / 128)) + (i >= BN / 128 ? p.cols : 0);
-                        tma_load_2d(b + i * kLinBox, &p.tb, p.b_mn ? n : 64 * k, p.b_mn ? 64 * k : n, full(s));
-                    }
-                }
+        const int n0 = glu ? tn * 32 : tn * 64, n1 = glu ? n0 + p.cols : n0 + 32;
+        uint32_t i = 0;
+        for (int k = k0; k < k1; ++k, ++i) {
+            const uint32_t s = i % S;
+            if (i >= S && !lin_wait_warp(empty(s), (i / S - 1) & 1)) {
+                *abort = 1;
+                break;
             }
-            // no copy outlives the loop (only short of the consumer's waits after an abort)
-            for (uint32_t j = it > S ? it - S : 0; j < it; ++j)
-                tc_mbar_wait(full(j % S), (j / S) & 1, kLinTimeoutNs);
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        if (lane == 0) {
-            // ---- MMA issue -----------------------------------------------------------------
-            uint32_t it = 0, done = 0;
-            for (int tile = blockIdx.x; tile < P.tiles && !*abort; tile += gridDim.x, ++done) {
-                const LinProblem& p = P.p[tile >= P.tiles0];
-                const int nk = (p.K + 63) / 64;
-                const int acc = done & 1;
-                // f32 accumulator, bf16 operands, transposed operands' bits, N and M
-                const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)p.a_mn << 15) |
-                                       ((uint32_t)p.b_mn << 16) | ((uint32_t)(BN >> 3) << 17) |
-                                       ((uint32_t)(kLinM >> 4) << 24);
-                if (done >= 2 && !tc_mbar_wait(accempty(acc), (done / 2 - 1) & 1, kLinTimeoutNs)) *abort = 1;
-                tc_fence_after();
-                for (int k = 0; k < nk && !*abort; ++k, ++it) {
-                    const int s = it % S;
-                    if (!tc_mbar_wait(full(s), (it / S) & 1, kLinTimeoutNs)) {
-                        *abort = 1;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t a = ring + s * kStage, b = a + kLinM * 128;
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) {
-                        const uint64_t ad = p.a_mn ? lin_desc_mn(a + 2048 * ks) : tc_smem_desc(a + 32 * ks);
-                        const uint64_t bd = p.b_mn ? lin_desc_mn(b + 2048 * ks) : tc_smem_desc(b + 32 * ks);
-                        tc_mma_f16(tmem + BN * acc, ad, bd, idesc, (k > 0 || ks > 0) ? 1u : 0u);
-                    }
-                    tc_commit(empty(s));
-                }
-                tc_commit(accfull(acc));
+            if (elect_one()) {
+                expect_tx(full(s), kSplStage);
+                const uint32_t a = ring + s * kSplStage, b = a + 128 * 128;
+                tma_load_2d(a, &p.ta, 64 * k, m0, full(s));
+                tma_load_2d(b, &p.tb, 64 * k, n0, full(s));
+                tma_load_2d(b + 32 * 128, &p.tb, 64 * k, n1, full(s));
             }
-            // never leave with MMAs in flight: they read shared memory and write TMEM
-            for (uint32_t j = done > 2 ? done - 2 : 0; j < done; ++j)
-                if (!tc_mbar_wait(accfull(j & 1), (j / 2) & 1, kLinTimeoutNs)) *abort = 1;
-        }
-        __syncwarp();
-    } else if (warp >= 4) {
-        // ---- epilogue: a thread per row, 32 columns at a time ----------------------------------
-        uint32_t done = 0;
-        for (int tile = blockIdx.x; tile < P.tiles; tile += gridDim.x, ++done) {
-            const LinProblem& p = P.p[tile >= P.tiles0];
-            const int ti = tile >= P.tiles0 ? tile - P.tiles0 : tile;
-            const int acc = done & 1;
-            const int64_t row = (int64_t)(ti / p.tiles_n) * kLinM + 32 * (warp - 4) + lane;
-            const bool on = row < p.M, vec = p.vec != 0;
-            if (!tc_mbar_wait(accfull(acc), (done / 2) & 1, kLinTimeoutNs)) *abort = 1;
-            if (__any_sync(0xffffffffu, *abort != 0)) break;
-            tc_fence_after();
-            const uint32_t t0 = tmem + ((uint32_t)(32 * (warp - 4)) << 16) + BN * acc;
-            if (p.act == kActSwiglu) {
-                const int n0 = ti % p.tiles_n * (BN / 2);
-#pragma unroll 1
-                for (int c = 0; c < BN / 2; c += 32) {
-                    uint32_t rg[32], ru[32];
-                    tc_ld32(t0 + c, rg);
-                    tc_ld32(t0 + BN / 2 + c, ru);
-                    tc_wait_ld();
-                    float g[32], u[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        g[j] = __uint_as_float(rg[j]);
-                        u[j] = __uint_as_float(ru[j]);
-                    }
-                    const int c0 = n0 + c;
-                    if (p.bias) {
-                        lin_add32(p.bias, c0, p.cols, false, g);
-                        lin_add32(p.bias + p.cols, c0, p.cols, false, u);
-                    }
-                    if (on && p.z) {
-                        lin_store32(p.z + (size_t)row * p.N, c0, p.cols, vec, g);
-                        lin_store32(p.z + (size_t)row * p.N + p.cols, c0, p.cols, vec, u);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) g[j] = g[j] * sigmoidf(g[j]) * u[j];
-                    if (on) {
-                        if (p.res) lin_add32(p.res + (size_t)row * p.ldr, c0, p.cols, vec, g);
-                        lin_store32(p.out + (size_t)row * p.ldo, c0, p.cols, vec, g);
-                    }
-                }
-            } else {
-                const int n0 = ti % p.tiles_n * BN;
-#pragma unroll 1
-                for (int c = 0; c < BN; c += 32) {
-                    uint32_t r[32];
-                    tc_ld32(t0 + c, r);
-                    tc_wait_ld();
-                    float v[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
-                    const int c0 = n0 + c;
-                    if (p.bias) lin_add32(p.bias, c0, p.cols, false, v);
-                    if (on && p.z) lin_store32(p.z + (size_t)row * p.N, c0, p.cols, vec, v);
-                    if (p.act != kActNone)
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = act_fwd(p.act, v[j]);
-                    if (on) {
-                        if (p.res) lin_add32(p.res + (size_t)row * p.ldr, c0, p.cols, vec, v);
-                        lin_store32(p.out + (size_t)row * p.ldo, c0, p.cols, vec, v);
-                    }
-                }
-            }
-            tc_fence_before();
             __syncwarp();
-            if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(accempty(acc)) : "memory");
+        }
+        for (uint32_t j = i > S ? i - S : 0; j < i; ++j) lin_wait_warp(full(j % S), (j / S) & 1);
+    } else if (warp == 1) {
+        const uint32_t idesc = lin_idesc(0, 0, 128, kSplN);
+        const uint64_t a0 = tc_smem_desc(ring), b0 = tc_smem_desc(ring + 128 * 128);
+        uint32_t i = 0;
+        for (int k = k0; k < k1; ++k, ++i) {
+            const uint32_t s = i % S;
+            if (!lin_wait_warp(full(s), (i / S) & 1)) {
+                *abort = 1;
+                break;
+            }
+            tc_fence_after();
+            if (elect_one()) {
+                const uint64_t a = a0 + s * (kSplStage >> 4), b = b0 + s * (kSplStage >> 4);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    tc_mma_f16(tmem, a + 2 * ks, b + 2 * ks, idesc, (i > 0 || ks > 0) ? 1u : 0u);
+                tc_commit(empty(s));
+            }
+            __syncwarp();
+        }
+        if (elect_one()) tc_commit(accfull);
+        __syncwarp();
+        if (!lin_wait_warp(accfull, 0)) *abort = 1;
+    }
+    __syncthreads();   // the products are done and every copy has landed: the ring is free
+    tc_fence_after();
+    float* part = reinterpret_cast<float*>(sm);   // [128][kSplLd]
+    const int rows = min(128, p.M - m0);
+    {
+        const int row = 32 * (warp & 3) + lane, c = 32 * (warp >> 2);
+        uint32_t r[32];
+        tc_ld32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + c, r);
+        tc_wait_ld();
+        if (row < rows) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                *reinterpret_cast<uint4*>(part + row * kSplLd + c + 4 * q) = make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
         }
     }
     tc_fence_before();
-    __syncthreads();
-    if (tid == 0 && *abort) atomicOr(&g_op_status, kDevTcTimeout);
+    cluster_sync();
     if (warp == 2) {
         tc_fence_after();
-        tc_dealloc(tmem, 2 * BN);
+        tc_dealloc(tmem, kSplN);
     }
+    // four columns per thread; rows rank, rank + splits, ...
+    const int tpr = glu ? 8 : 16, cc = 4 * (tid % tpr);
+    const int col0 = tn * (glu ? 32 : 64) + cc;
+    for (int row = (tid / tpr) * p.splits + rank; row < rows; row += kSplThreads / tpr * p.splits) {
+        float v[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0};
+        const uint32_t at = tc_saddr(part + row * kSplLd + cc);
+        for (int s = 0; s < p.splits; ++s) {
+            const uint32_t from = cluster_map(at, s);
+            float4 q;
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w)
+                         : "r"(from)
+                         : "memory");
+            v[0] += q.x; v[1] += q.y; v[2] += q.z; v[3] += q.w;
+            if (glu) {
+                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w)
+                             : "r"(from + 32 * 4)
+                             : "memory");
+                u[0] += q.x; u[1] += q.y; u[2] += q.z; u[3] += q.w;
+            }
+        }
+        const size_t grow = (size_t)(m0 + row);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = col0 + j;
+            if (c >= p.cols) break;
+            if (p.bias) {
+                v[j] += bf16_bits_to_f32(p.bias[c]);
+                if (glu) u[j] += bf16_bits_to_f32(p.bias[c + p.cols]);
+            }
+            if (p.z) {
+                p.z[grow * p.N + c] = (uint16_t)(bf16x2_rn(v[j], 0.0f) & 0xffffu);
+                if (glu) p.z[grow * p.N + c + p.cols] = (uint16_t)(bf16x2_rn(u[j], 0.0f) & 0xffffu);
+            }
+            v[j] = glu ? v[j] * sigmoidf(v[j]) * u[j] : act_fwd(p.act, v[j]);
+            if (p.res) v[j] += bf16_bits_to_f32(p.res[grow * p.ldr + c]);
+        }
+        uint16_t* o = p.out + grow * p.ldo + col0;
+        if (col0 + 4 <= p.cols && (reinterpret_cast<uintptr_t>(o) & 7) == 0) {
+            *reinterpret_cast<uint2*>(o) = make_uint2(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (col0 + j < p.cols) o[j] = (uint16_t)(bf16x2_rn(v[j], 0.0f) & 0xffffu);
+        }
+    }
+    if (tid == 0 && *abort) atomicOr(&g_op_status, kDevTcTimeout);
+    cluster_sync();   // no CTA leaves while another still reads its partial tile
 }
 
 // ---- a few rows ------------------------------------------------------------------------
