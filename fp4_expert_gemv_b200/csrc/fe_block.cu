@@ -189,7 +189,19 @@ cudaError_t norm_bwd_launch(const fe::NormBwdParams& q, bool vec, bool r32, cons
 
 // ---- balance loss -------------------------------------------------------------------------
 
-int balance_ctas(int64_t T) { return (int)std::max<int64_t>(1, std::min<int64_t>(kMaxPartials, (T + fe::kBalWarps - 1) / fe::kBalWarps)); }
+// Values per lane of a row of E logits.
+int balance_npl(int E) { return E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : E <= 256 ? 8 : E <= 512 ? 16 : 32; }
+
+// CTAs of the forward pass, one row per warp up to kMaxBalanceCtas of them.
+constexpr int kMaxBalanceCtas = 296;
+int balance_ctas(int64_t T, int E)
+{
+    const int w = fe::bal_warps(balance_npl(E));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(kMaxBalanceCtas, (T + w - 1) / w));
+}
+
+// Rows per warp up to which one cluster takes the whole loss.
+constexpr int kBalanceFusedRows = 4;
 
 fe_status check_balance(const float* logits, const uint8_t*, int64_t T, int E, int top_k)
 {
@@ -198,25 +210,45 @@ fe_status check_balance(const float* logits, const uint8_t*, int64_t T, int E, i
     return FE_OK;
 }
 
+template <int NPL, int VEC>
+cudaError_t balance_forward(const fe::BalanceParams& p, int grid, cudaStream_t s)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(32 * fe::bal_warps(NPL));
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.G > 0 ? 1 : grid;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, fe::balance_kernel<NPL, VEC>, p);
+}
+
 template <int NPL>
 cudaError_t balance_launch(const fe::BalanceParams& p, bool backward, int grid, bool vec, cudaStream_t s)
 {
     if constexpr (NPL >= 4) {
         if (vec)
             return backward ? launch(fe::balance_backward_kernel<NPL, 4>, grid, fe::kBalThreads, 0, s, p)
-                            : launch(fe::balance_kernel<NPL, 4>, grid, fe::kBalThreads, 0, s, p);
+                            : balance_forward<NPL, 4>(p, grid, s);
     }
     return backward ? launch(fe::balance_backward_kernel<NPL, 1>, grid, fe::kBalThreads, 0, s, p)
-                    : launch(fe::balance_kernel<NPL, 1>, grid, fe::kBalThreads, 0, s, p);
+                    : balance_forward<NPL, 1>(p, grid, s);
 }
 
 cudaError_t balance_dispatch(const fe::BalanceParams& p, bool backward, int grid, bool vec, cudaStream_t s)
 {
-    if (p.E <= 32) return balance_launch<1>(p, backward, grid, vec, s);
-    if (p.E <= 64) return balance_launch<2>(p, backward, grid, vec, s);
-    if (p.E <= 128) return balance_launch<4>(p, backward, grid, vec, s);
-    if (p.E <= 256) return balance_launch<8>(p, backward, grid, vec, s);
-    if (p.E <= 512) return balance_launch<16>(p, backward, grid, vec, s);
+    switch (balance_npl(p.E)) {
+        case 1: return balance_launch<1>(p, backward, grid, vec, s);
+        case 2: return balance_launch<2>(p, backward, grid, vec, s);
+        case 4: return balance_launch<4>(p, backward, grid, vec, s);
+        case 8: return balance_launch<8>(p, backward, grid, vec, s);
+        case 16: return balance_launch<16>(p, backward, grid, vec, s);
+    }
     return balance_launch<32>(p, backward, grid, vec, s);
 }
 
@@ -497,7 +529,7 @@ cudaError_t rows_launch(const fe::LinRowsParams& p, cudaStream_t s)
 }
 
 // Backward workspace: dz [M][roundup8(N)] bf16, then the column partials.
-int dz_chunks(int64_t M) { return (int)std::max<int64_t>(1, std::min<int64_t>(64, (M + 31) / 32)); }
+int dz_chunks(int64_t M) { return (int)std::max<int64_t>(1, std::min<int64_t>(256, (M + 31) / 32)); }
 
 }  // namespace
 
@@ -646,7 +678,7 @@ fe_status fe_moe_block_norm_backward(const void* dr_out, const void* du, const v
 size_t fe_moe_balance_workspace(int64_t T, int E)
 {
     if (T < 0 || E < 1 || E > fe::kBalMaxE) return 0;
-    return 8 * (size_t)balance_ctas(T) * ((size_t)E + 1);
+    return 8 * (size_t)balance_ctas(T, E) * ((size_t)E + 1);
 }
 
 fe_status fe_moe_balance_loss(const float* logits, const int32_t* idx, const uint8_t* mask, int64_t T, int E, int top_k,
@@ -682,12 +714,21 @@ fe_status fe_moe_balance_loss(const float* logits, const int32_t* idx, const uin
     p.loss = loss;
     p.counts = counts;
     p.n_tokens = n_tokens;
-    p.G = balance_ctas(T);
+    const int ctas = balance_ctas(T, E);
+    const bool vec = E % 4 == 0 && aligned(logits, 16);
+    const cudaStream_t s = (cudaStream_t)stream;
+    if (T <= (int64_t)kBalanceFusedRows * fe::kBalCluster * fe::bal_warps(balance_npl(E))) {
+        int n = 1;   // CTAs of the cluster: a row per warp, to eight
+        while (n < fe::kBalCluster && n < ctas) n *= 2;
+        p.G = 0;
+        FE_CUDA_TRY(balance_dispatch(p, false, n, vec, s));
+        return FE_OK;
+    }
+    p.G = ctas;
     p.part = static_cast<float*>(workspace);
     p.ipart = reinterpret_cast<int32_t*>(p.part + (size_t)p.G * (E + 1));
-    const cudaStream_t s = (cudaStream_t)stream;
-    FE_CUDA_TRY(balance_dispatch(p, false, p.G, E % 4 == 0 && aligned(logits, 16), s));
-    FE_CUDA_TRY(launch(fe::balance_final_kernel, dim3(1), dim3(1024), 0, s, p));
+    FE_CUDA_TRY(balance_dispatch(p, false, p.G, vec, s));
+    FE_CUDA_TRY(launch(fe::balance_final_kernel, dim3(fe::kBalCluster), dim3(1024), 0, s, p));
     return FE_OK;
 }
 

@@ -16,6 +16,7 @@
 
 #include <cuda.h>
 
+#include "cluster.cuh"
 #include "common.cuh"
 #include "norm.cuh"
 #include "tcgen05_ptx.cuh"
@@ -27,12 +28,30 @@ enum { kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3, kActSwiglu = 4 };
 // Device-side problems of the entry points without a handle (kDevTcTimeout).
 __device__ uint32_t g_op_status;
 
-FE_DEV float phi_cdf(float z) { return 0.5f * (1.0f + erff(z * 0.70710678118654752f)); }
+// Phi(z) and exp(-z^2 / 2).  The tail Q(|z|) = erfc(|z| / sqrt 2) / 2 by Abramowitz and Stegun, formula
+// 7.1.26 (a polynomial in t = 1 / (1 + p x) times exp(-x^2), |error of erf| <= 1.5e-7), which keeps the
+// small tail relatively exact: one exponential, shared with the density, and one division.  erff took
+// three times the instructions, as much as a whole product's tile at K = 2048.
+FE_DEV float phi_cdf(float z, float& e)
+{
+    const float x = fabsf(z) * 0.70710678118654752f;
+    const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+    e = __expf(-x * x);
+    float q = fmaf(1.061405429f, t, -1.453152027f);
+    q = fmaf(q, t, 1.421413741f);
+    q = fmaf(q, t, -0.284496736f);
+    q = fmaf(q, t, 0.254829592f);
+    q *= 0.5f * t * e;
+    return z < 0.0f ? q : 1.0f - q;
+}
 
 FE_DEV float act_fwd(int act, float z)
 {
     if (act == kActRelu) return z > 0.0f ? z : (z == z ? 0.0f : z);
-    if (act == kActGelu) return z * phi_cdf(z);
+    if (act == kActGelu) {
+        float e;
+        return z * phi_cdf(z, e);
+    }
     if (act == kActSilu) return z * sigmoidf(z);
     return z;
 }
@@ -41,7 +60,11 @@ FE_DEV float act_fwd(int act, float z)
 FE_DEV float act_bwd(int act, float z)
 {
     if (act == kActRelu) return z > 0.0f ? 1.0f : 0.0f;
-    if (act == kActGelu) return phi_cdf(z) + z * __expf(-0.5f * z * z) * 0.39894228040143268f;
+    if (act == kActGelu) {
+        float e;
+        const float c = phi_cdf(z, e);
+        return c + z * e * 0.39894228040143268f;
+    }
     if (act == kActSilu) {
         const float q = sigmoidf(z);
         return q * (1.0f + z * (1.0f - q));
@@ -112,6 +135,8 @@ FE_DEV void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src)
                  : "memory");
 }
 
+FE_DEV void prefetch_tensormap(const CUtensorMap* map) { asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory"); }
+
 template <int N>
 FE_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory"); }
 
@@ -144,26 +169,6 @@ FE_DEV bool elect_one()
     uint32_t p;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0;
-}
-
-FE_DEV uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-FE_DEV void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// This CTA's shared address as seen in CTA `rank` of the cluster.
-FE_DEV uint32_t cluster_map(uint32_t saddr, uint32_t rank)
-{
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-    return r;
 }
 
 FE_DEV void expect_tx(uint32_t bar, uint32_t bytes)
@@ -352,19 +357,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     auto accfull = [&](int s) { return bar0 + 8u * (2 * S + s); };      // both: a tile's products are done
     auto accempty = [&](int s) { return bar0 + 8u * (2 * S + 2 + s); }; // leader: both CTAs drained it
     auto resfull = [&](int w, int s) { return bar0 + 8u * (2 * S + 4 + 2 * w + s); };
-    if (tid == 0) {
-        for (int s = 0; s < S; ++s) {
-            tc_mbar_init(full(s), 1);
-            tc_mbar_init(empty(s), 1);
-        }
-        for (int s = 0; s < 2; ++s) {
-            tc_mbar_init(accfull(s), 1);
-            tc_mbar_init(accempty(s), 16);
-        }
-        for (int w = 0; w < 16; ++w) tc_mbar_init(resfull(0, w), 1);
+    if (tid < kLinBars) {
+        tc_mbar_init(bar0 + 8u * tid, tid == 2 * S + 2 || tid == 2 * S + 3 ? 16 : 1);   // accempty: both CTAs' 8 warps
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        *abort = 0;
     }
+    if (tid == 64) *abort = 0;
+    if (tid >= 96 && tid < 96 + 2 * P.n) prefetch_tensormap(tid & 1 ? &P.p[(tid - 96) >> 1].tb : &P.p[(tid - 96) >> 1].ta);
     if (warp == 2) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(tc_saddr(tmem_slot)),
                      "r"(kTmemCols)
@@ -625,6 +623,44 @@ struct LinSplitParams {
     uint16_t* z;
 };
 
+// N consecutive values at `at` in every CTA of the cluster, added in rank order.
+template <int N>
+FE_DEV void spl_gather(uint32_t at, int splits, float (&v)[N])
+{
+    float q[8][N];
+#pragma unroll
+    for (int s = 0; s < 8; ++s) {
+        if (s >= splits) break;
+        const uint32_t from = cluster_map(at, s);
+#pragma unroll
+        for (int j = 0; j < N; j += 4)
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(q[s][j]), "=f"(q[s][j + 1]), "=f"(q[s][j + 2]), "=f"(q[s][j + 3])
+                         : "r"(from + 4 * j));
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = q[0][j];
+#pragma unroll
+    for (int s = 1; s < 8; ++s) {
+        if (s >= splits) break;
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] += q[s][j];
+    }
+}
+
+// Up to 8 consecutive bf16 (left: how many belong to the matrix).
+FE_DEV void spl_store8(uint16_t* o, int left, const float (&v)[8])
+{
+    if (left >= 8 && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
+        *reinterpret_cast<uint4*>(o) =
+            make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]), bf16x2_rn(v[4], v[5]), bf16x2_rn(v[6], v[7]));
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < left) o[j] = (uint16_t)(bf16x2_rn(v[j], 0.0f) & 0xffffu);
+    }
+}
+
 // One 128 x 64 tile per cluster of `splits` CTAs, each over its share of the k steps; the partial
 // tiles meet through distributed shared memory, every CTA adding (in rank order) and finishing every
 // splits-th row.  For products of so few tiles that whole tiles would leave most SMs idle while the
@@ -649,15 +685,12 @@ __global__ void __launch_bounds__(kSplThreads, 1) linear_split_kernel(const __gr
     auto full = [&](int s) { return bar0 + 8u * s; };
     auto empty = [&](int s) { return bar0 + 8u * (S + s); };
     const uint32_t accfull = bar0 + 8u * 2 * S;
-    if (tid == 0) {
-        for (int s = 0; s < S; ++s) {
-            tc_mbar_init(full(s), 1);
-            tc_mbar_init(empty(s), 1);
-        }
-        tc_mbar_init(accfull, 1);
+    if (tid <= 2 * S) {
+        tc_mbar_init(bar0 + 8u * tid, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        *abort = 0;
     }
+    if (tid == 32) *abort = 0;
+    if (tid >= 96 && tid < 98) prefetch_tensormap(tid == 96 ? &p.ta : &p.tb);
     if (warp == 2) {
         tc_alloc(tc_saddr(tmem_slot), kSplN);
         tc_relinquish();
@@ -731,52 +764,34 @@ __global__ void __launch_bounds__(kSplThreads, 1) linear_split_kernel(const __gr
         tc_fence_after();
         tc_dealloc(tmem, kSplN);
     }
-    // four columns per thread; rows rank, rank + splits, ...
-    const int tpr = glu ? 8 : 16, cc = 4 * (tid % tpr);
+    // eight columns per thread; rows rank, rank + splits, ...  The partials of a row are all fetched
+    // before the first is added.
+    const int tpr = glu ? 4 : 8, cc = 8 * (tid % tpr);
     const int col0 = tn * (glu ? 32 : 64) + cc;
-    for (int row = (tid / tpr) * p.splits + rank; row < rows; row += kSplThreads / tpr * p.splits) {
-        float v[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0};
+    for (int row = (tid / tpr) * p.splits + rank; row < rows && col0 < p.cols; row += kSplThreads / tpr * p.splits) {
         const uint32_t at = tc_saddr(part + row * kSplLd + cc);
-        for (int s = 0; s < p.splits; ++s) {
-            const uint32_t from = cluster_map(at, s);
-            float4 q;
-            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w)
-                         : "r"(from)
-                         : "memory");
-            v[0] += q.x; v[1] += q.y; v[2] += q.z; v[3] += q.w;
-            if (glu) {
-                asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                             : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w)
-                             : "r"(from + 32 * 4)
-                             : "memory");
-                u[0] += q.x; u[1] += q.y; u[2] += q.z; u[3] += q.w;
-            }
-        }
         const size_t grow = (size_t)(m0 + row);
+        float v[8], u[8], add[8];
+        const uint16_t* rp = p.res ? p.res + grow * p.ldr + col0 : nullptr;
+        spl_gather<8>(at, p.splits, v);
+        if (glu) spl_gather<8>(at + 32 * 4, p.splits, u);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int c = col0 + j;
-            if (c >= p.cols) break;
-            if (p.bias) {
-                v[j] += bf16_bits_to_f32(p.bias[c]);
-                if (glu) u[j] += bf16_bits_to_f32(p.bias[c + p.cols]);
-            }
-            if (p.z) {
-                p.z[grow * p.N + c] = (uint16_t)(bf16x2_rn(v[j], 0.0f) & 0xffffu);
-                if (glu) p.z[grow * p.N + c + p.cols] = (uint16_t)(bf16x2_rn(u[j], 0.0f) & 0xffffu);
-            }
-            v[j] = glu ? v[j] * sigmoidf(v[j]) * u[j] : act_fwd(p.act, v[j]);
-            if (p.res) v[j] += bf16_bits_to_f32(p.res[grow * p.ldr + c]);
-        }
-        uint16_t* o = p.out + grow * p.ldo + col0;
-        if (col0 + 4 <= p.cols && (reinterpret_cast<uintptr_t>(o) & 7) == 0) {
-            *reinterpret_cast<uint2*>(o) = make_uint2(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]));
-        } else {
+        for (int j = 0; j < 8; ++j) add[j] = rp && col0 + j < p.cols ? bf16_bits_to_f32(rp[j]) : 0.0f;
+        if (p.bias) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (col0 + j < p.cols) o[j] = (uint16_t)(bf16x2_rn(v[j], 0.0f) & 0xffffu);
+            for (int j = 0; j < 8; ++j) {
+                if (col0 + j >= p.cols) break;
+                v[j] += bf16_bits_to_f32(p.bias[col0 + j]);
+                if (glu) u[j] += bf16_bits_to_f32(p.bias[col0 + j + p.cols]);
+            }
         }
+        if (p.z) {
+            spl_store8(p.z + grow * p.N + col0, p.cols - col0, v);
+            if (glu) spl_store8(p.z + grow * p.N + col0 + p.cols, p.cols - col0, u);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = (glu ? v[j] * sigmoidf(v[j]) * u[j] : act_fwd(p.act, v[j])) + add[j];
+        spl_store8(p.out + grow * p.ldo + col0, p.cols - col0, v);
     }
     if (tid == 0 && *abort) atomicOr(&g_op_status, kDevTcTimeout);
     cluster_sync();   // no CTA leaves while another still reads its partial tile
@@ -867,36 +882,48 @@ struct LinDzParams {
     int N, cols, act;
 };
 
-// VEC consecutive bf16 values (16-byte aligned when VEC is 8).
 template <int VEC>
-FE_DEV void dz_load(const uint16_t* p, float (&v)[VEC])
+struct DzWord {
+    using T = uint16_t;
+};
+template <>
+struct DzWord<8> {
+    using T = uint4;
+};
+
+template <int VEC>
+FE_DEV void dz_unpack(const typename DzWord<VEC>::T& q, float (&v)[VEC])
 {
-    if (VEC == 8) {
-        const uint4 q = *reinterpret_cast<const uint4*>(p);
+    if constexpr (VEC == 8) {
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
         for (int j = 0; j < VEC; ++j) v[j] = __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
     } else {
-        v[0] = bf16_bits_to_f32(*p);
+        v[0] = bf16_bits_to_f32(q);
     }
 }
 
 template <int VEC>
 FE_DEV void dz_store(uint16_t* p, const float (&v)[VEC])
 {
-    if (VEC == 8)
-        *reinterpret_cast<uint4*>(p) = make_uint4(bf16x2_rn(v[0], v[1 % VEC]), bf16x2_rn(v[2 % VEC], v[3 % VEC]),
-                                                  bf16x2_rn(v[4 % VEC], v[5 % VEC]), bf16x2_rn(v[6 % VEC], v[7 % VEC]));
+    if constexpr (VEC == 8)
+        *reinterpret_cast<uint4*>(p) =
+            make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]), bf16x2_rn(v[4], v[5]), bf16x2_rn(v[6], v[7]));
     else
         *p = (uint16_t)(bf16x2_rn(v[0], 0.0f) & 0xffffu);
 }
 
-// Block 32 x 8: a thread owns VEC columns, 8 threads share the rows of a chunk.
+constexpr int kDzRows = 4;   // rows a thread has in flight
+
+// Block 32 x 8: a thread owns VEC columns, 8 threads share the rows of a chunk.  Bound by memory: dY and
+// Z are read once, dZ written once, so a thread keeps four rows' loads in flight.
 template <int VEC>
 __global__ void __launch_bounds__(256) linear_dz_kernel(LinDzParams p)
 {
+    using W = typename DzWord<VEC>::T;
     __shared__ float red[8][2 * VEC][33];
     griddep_wait();
+    griddep_launch();
     const int x = threadIdx.x & 31, yy = threadIdx.x >> 5;
     const int c = (blockIdx.x * 32 + x) * VEC;
     const int64_t r0 = (int64_t)blockIdx.y * p.rows_per_cta, r1 = min(p.M, r0 + p.rows_per_cta);
@@ -905,29 +932,43 @@ __global__ void __launch_bounds__(256) linear_dz_kernel(LinDzParams p)
 #pragma unroll
     for (int j = 0; j < VEC; ++j) s0[j] = s1[j] = 0.0f;
     if (c < p.cols) {
-        for (int64_t r = r0 + yy; r < r1; r += 8) {
-            float g[VEC], z0[VEC], z1[VEC];
-            dz_load<VEC>(p.dy + r * p.lddy + c, g);
-            if (p.act != kActNone) dz_load<VEC>(p.z + r * p.N + c, z0);
-            if (glu) dz_load<VEC>(p.z + r * p.N + p.cols + c, z1);
+        for (int64_t r = r0 + yy; r < r1; r += 8 * kDzRows) {
+            W wg[kDzRows], w0[kDzRows], w1[kDzRows];
 #pragma unroll
-            for (int j = 0; j < VEC; ++j) {
-                float d0, d1 = 0.0f;
-                if (glu) {
-                    const float q = sigmoidf(z0[j]);
-                    d1 = g[j] * z0[j] * q;
-                    d0 = g[j] * z1[j] * q * (1.0f + z0[j] * (1.0f - q));
-                } else {
-                    d0 = p.act == kActNone ? g[j] : g[j] * act_bwd(p.act, z0[j]);
-                }
-                s0[j] += d0;
-                s1[j] += d1;
-                z0[j] = d0;
-                z1[j] = d1;
+            for (int i = 0; i < kDzRows; ++i) {
+                const int64_t q = r + 8 * i;
+                if (q >= r1) break;
+                wg[i] = *reinterpret_cast<const W*>(p.dy + q * p.lddy + c);
+                if (p.act != kActNone) w0[i] = *reinterpret_cast<const W*>(p.z + q * p.N + c);
+                if (glu) w1[i] = *reinterpret_cast<const W*>(p.z + q * p.N + p.cols + c);
             }
-            if (p.dz) {
-                dz_store<VEC>(p.dz + r * p.lddz + c, z0);
-                if (glu) dz_store<VEC>(p.dz + r * p.lddz + p.cols + c, z1);
+#pragma unroll
+            for (int i = 0; i < kDzRows; ++i) {
+                const int64_t q = r + 8 * i;
+                if (q >= r1) break;
+                float g[VEC], z0[VEC], z1[VEC];
+                dz_unpack<VEC>(wg[i], g);
+                if (p.act != kActNone) dz_unpack<VEC>(w0[i], z0);
+                if (glu) dz_unpack<VEC>(w1[i], z1);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) {
+                    float d0, d1 = 0.0f;
+                    if (glu) {
+                        const float sg = sigmoidf(z0[j]);
+                        d1 = g[j] * z0[j] * sg;
+                        d0 = g[j] * z1[j] * sg * (1.0f + z0[j] * (1.0f - sg));
+                    } else {
+                        d0 = p.act == kActNone ? g[j] : g[j] * act_bwd(p.act, z0[j]);
+                    }
+                    s0[j] += d0;
+                    s1[j] += d1;
+                    z0[j] = d0;
+                    z1[j] = d1;
+                }
+                if (p.dz) {
+                    dz_store<VEC>(p.dz + q * p.lddz + c, z0);
+                    if (glu) dz_store<VEC>(p.dz + q * p.lddz + p.cols + c, z1);
+                }
             }
         }
     }

@@ -11,6 +11,7 @@
 // the unrounded r'.
 #pragma once
 
+#include "cluster.cuh"
 #include "common.cuh"
 
 namespace fe {
@@ -43,9 +44,6 @@ struct NormBwdParams {
     float* part;              // [grid][3][H] column sums (dw_post, dw_pre, dgate per channel), or null
     int64_t rows_per_cta;
 };
-
-FE_DEV void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-FE_DEV void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;"); }
 
 FE_DEV float sigmoidf(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
 

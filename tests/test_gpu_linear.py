@@ -40,7 +40,7 @@ def check_backward(fe, dy, x, w, z, act):
     M, N = dz.shape
     ref.close(dx, dz @ W, edz @ W.abs() + (N / 16 + 4) * 2.0 ** -22 * (adz @ W.abs()), "dx")
     ref.close(dw, dz.t() @ X, edz.t() @ X.abs() + (M / 16 + 4) * 2.0 ** -22 * (adz.t() @ X.abs()), "dw")
-    # chains of at most M / 512 + 1 rows per thread, then 8, then the chunks in a tree
+    # chains of at most M / 2048 + 4 rows per thread, then 8, then the chunks in a tree
     ref.close(db, dz.sum(0), (ref.FWD + (M / 512 + 32) * 2.0 ** -24) * mag.sum(0), "db")
     assert fe.op_status() == (fe.FE_OK, 0)
 
