@@ -279,7 +279,7 @@ class MoELayer:
         with _device(dev):
             ws = torch.empty(max(nb, 16), dtype=torch.uint8, device=dev)
             check(fe_moe_forward_block(self.h, ctypes.byref(b), _dptr(r), dt, _dptr(u_in), T, top_k, _dptr(r_out),
-                                       _dptr(u_out), _dptr(logits), _dptr(ws), ws.numel(), _stream_ptr(None)),
+                                       _dptr(u_out), _dptr(logits), _dptr(ws), ws.numel(), _current_stream(dev)),
                   "fe_moe_forward_block")
         return r_out, u_out, logits
 
@@ -481,6 +481,13 @@ def _device(dev):
     return _NOTHING if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
+def _current_stream(dev):
+    """The current stream of a device, as an address (without the Stream object where torch offers that)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev.index) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
 def _on_stream(stream, dev):
     """The stream made current, so that what the call allocates belongs to it."""
     import torch
@@ -492,26 +499,29 @@ def _on_stream(stream, dev):
 
 
 def _arg(t, name, dtype, shape, dev, optional=False):
+    """The address of a contiguous CUDA tensor of this type and shape on dev (None for None, where allowed)."""
     if t is None:
         if optional:
-            return
+            return None
         raise ValueError(f"{name} is needed")
-    if t.dtype != dtype or tuple(t.shape) != shape or t.device != dev or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous {dtype} CUDA tensor of shape {shape} on {dev} is needed, "
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} CUDA tensor of shape {tuple(shape)} on {dev} is needed, "
                          f"got {t.dtype} {tuple(t.shape)} strides {tuple(t.stride())} on {t.device}")
+    return t.data_ptr()
 
 
 def _arg_rows(t, name, dtype, shape, dev):
-    """A matrix whose rows are contiguous; returns its row stride."""
-    if (t.dtype != dtype or tuple(t.shape) != shape or t.device != dev or not t.is_cuda
+    """The address and row stride of a CUDA matrix whose rows are contiguous."""
+    if (t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_cuda
             or (shape[1] > 1 and shape[0] > 0 and t.stride(1) != 1)):
-        raise ValueError(f"{name}: a {dtype} CUDA matrix of shape {shape} on {dev} with contiguous rows is needed, "
+        raise ValueError(f"{name}: a {dtype} CUDA matrix of shape {tuple(shape)} on {dev} with contiguous rows is needed, "
                          f"got {t.dtype} {tuple(t.shape)} strides {tuple(t.stride())} on {t.device}")
     if shape[0] <= 1:
-        return (shape[1] + 7) // 8 * 8
-    if t.stride(0) < shape[1]:
+        return t.data_ptr(), (shape[1] + 7) // 8 * 8
+    ld = t.stride(0)
+    if ld < shape[1]:
         raise ValueError(f"{name}: rows overlap (strides {tuple(t.stride())})")
-    return t.stride(0)
+    return t.data_ptr(), ld
 
 
 def _arg_gate(gate, kind, T, H, dev):
@@ -519,8 +529,9 @@ def _arg_gate(gate, kind, T, H, dev):
     k = kind & ~GATE_SIGMOID
     if k not in (GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL) or (gate is None) != (k == GATE_NONE):
         raise ValueError("gate and gate_kind do not go together")
-    if gate is not None:
-        _arg(gate, "gate", torch.bfloat16, {GATE_CHANNEL: (H,), GATE_TOKEN: (T,), GATE_FULL: (T, H)}[k], dev)
+    if gate is None:
+        return None
+    return _arg(gate, "gate", torch.bfloat16, (H,) if k == GATE_CHANNEL else (T,) if k == GATE_TOKEN else (T, H), dev)
 
 
 def _out(t, name, dtype, shape, dev):
@@ -549,21 +560,21 @@ def block_norm(r, y=None, w_post=None, w_pre=None, gate=None, gate_kind=GATE_NON
         with _on_stream(stream, r.device):
             return block_norm(r, y, w_post, w_pre, gate, gate_kind, scale, eps, r_out, u)
     import torch
-    bf, dev = torch.bfloat16, r.device
-    T, H = r.shape
+    bf, dev, shape = torch.bfloat16, r.device, r.shape
+    T, H = shape
     dt = _dtype_of(r, "r")
-    _arg(r, "r", r.dtype, (T, H), dev)
-    _arg(y, "y", bf, (T, H), dev, optional=True)
-    _arg(w_post, "w_post", bf, (H,), dev, optional=True)
-    _arg(w_pre, "w_pre", bf, (H,), dev, optional=True)
-    _arg_gate(gate, gate_kind, T, H, dev)
+    rp = _arg(r, "r", r.dtype, shape, dev)
+    yp = _arg(y, "y", bf, shape, dev, True)
+    postp = _arg(w_post, "w_post", bf, (H,), dev, True)
+    prep = _arg(w_pre, "w_pre", bf, (H,), dev, True)
+    gp = _arg_gate(gate, gate_kind, T, H, dev)
     if y is not None:
-        r_out = _out(r_out, "r_out", r.dtype, (T, H), dev)
+        r_out = _out(r_out, "r_out", r.dtype, shape, dev)
     if w_pre is not None:
-        u = _out(u, "u", bf, (T, H), dev)
+        u = _out(u, "u", bf, shape, dev)
     with _device(dev):
-        check(fe_moe_block_norm(_dptr(r), dt, _dptr(y), _dptr(w_post), _dptr(gate), gate_kind, scale, _dptr(w_pre), eps,
-                                T, H, _dptr(r_out), _dptr(u), _stream_ptr(None)), "fe_moe_block_norm")
+        check(fe_moe_block_norm(rp, dt, yp, postp, gp, gate_kind, scale, prep, eps, T, H, _dptr(r_out), _dptr(u),
+                                _current_stream(dev)), "fe_moe_block_norm")
     return r_out, u
 
 
@@ -577,35 +588,38 @@ def block_norm_backward(dr_out, du, r, y=None, w_post=None, w_pre=None, gate=Non
         with _on_stream(stream, r.device):
             return block_norm_backward(dr_out, du, r, y, w_post, w_pre, gate, gate_kind, scale, eps, weight_grads)
     import torch
-    bf, f32, dev = torch.bfloat16, torch.float32, r.device
-    T, H = r.shape
+    bf, f32, dev, shape = torch.bfloat16, torch.float32, r.device, r.shape
+    T, H = shape
     dt = _dtype_of(r, "r")
-    _arg(r, "r", r.dtype, (T, H), dev)
-    _arg(dr_out, "dr_out", r.dtype, (T, H), dev, optional=True)
-    _arg(du, "du", bf, (T, H), dev, optional=True)
-    _arg(y, "y", bf, (T, H), dev, optional=True)
-    _arg(w_post, "w_post", bf, (H,), dev, optional=True)
-    _arg(w_pre, "w_pre", bf, (H,), dev, optional=True)
-    _arg_gate(gate, gate_kind, T, H, dev)
+    rp = _arg(r, "r", r.dtype, shape, dev)
+    drop = _arg(dr_out, "dr_out", r.dtype, shape, dev, True)
+    dup = _arg(du, "du", bf, shape, dev, True)
+    yp = _arg(y, "y", bf, shape, dev, True)
+    postp = _arg(w_post, "w_post", bf, (H,), dev, True)
+    prep = _arg(w_pre, "w_pre", bf, (H,), dev, True)
+    gp = _arg_gate(gate, gate_kind, T, H, dev)
     kind = gate_kind & ~GATE_SIGMOID
-    dr = torch.empty((T, H), dtype=r.dtype, device=dev)
-    dy = torch.empty((T, H), dtype=bf, device=dev) if y is not None else None
-    dgate = None
-    if kind == GATE_FULL:
-        dgate = torch.empty((T, H), dtype=bf, device=dev)
-    elif kind == GATE_TOKEN or (kind == GATE_CHANNEL and weight_grads):
-        dgate = torch.empty((T,) if kind == GATE_TOKEN else (H,), dtype=f32, device=dev)
-    dw_post = torch.empty((H,), dtype=f32, device=dev) if w_post is not None and weight_grads else None
-    dw_pre = torch.empty((H,), dtype=f32, device=dev) if w_pre is not None and weight_grads else None
-    ws, nb = None, 0
-    if dw_post is not None or dw_pre is not None or (kind == GATE_CHANNEL and dgate is not None):
+    dr = torch.empty(shape, dtype=r.dtype, device=dev)
+    dy = torch.empty(shape, dtype=bf, device=dev) if y is not None else None
+    # the float32 sums over rows and the workspace behind them share one allocation
+    sums = [] if not weight_grads else [n for n, on in (("post", w_post is not None), ("pre", w_pre is not None),
+                                                        ("gate", kind == GATE_CHANNEL)) if on]
+    col, ws, nb = {}, None, 0
+    if sums:
         nb = fe_moe_block_norm_workspace(T, H)
-        ws = torch.empty(max(nb, 1), dtype=torch.uint8, device=dev)
+        buf = torch.empty(len(sums) * H + (nb + 3) // 4, dtype=f32, device=dev)
+        col = {n: buf[i * H:(i + 1) * H] for i, n in enumerate(sums)}
+        ws = buf.data_ptr() + 4 * len(sums) * H
+    dgate = col.get("gate")
+    if kind == GATE_FULL:
+        dgate = torch.empty(shape, dtype=bf, device=dev)
+    elif kind == GATE_TOKEN:
+        dgate = torch.empty(T, dtype=f32, device=dev)
+    dw_post, dw_pre = col.get("post"), col.get("pre")
     with _device(dev):
-        check(fe_moe_block_norm_backward(_dptr(dr_out), _dptr(du), _dptr(r), dt, _dptr(y), _dptr(w_post), _dptr(gate),
-                                         gate_kind, scale, _dptr(w_pre), eps, T, H, _dptr(dr), _dptr(dy), _dptr(dgate),
-                                         _dptr(dw_post), _dptr(dw_pre), _dptr(ws), nb, _stream_ptr(None)),
-              "fe_moe_block_norm_backward")
+        check(fe_moe_block_norm_backward(drop, dup, rp, dt, yp, postp, gp, gate_kind, scale, prep, eps, T, H, _dptr(dr),
+                                         _dptr(dy), _dptr(dgate), _dptr(dw_post), _dptr(dw_pre), ws, nb,
+                                         _current_stream(dev)), "fe_moe_block_norm_backward")
     return dr, dy, dgate, dw_post, dw_pre
 
 
@@ -620,18 +634,17 @@ def balance_loss(logits, idx, mask=None, balance_coef=1.0, z_coef=0.0, loss=None
     i32, f32, dev = torch.int32, torch.float32, logits.device
     T, E = logits.shape
     k = idx.shape[1]
-    _arg(logits, "logits", f32, (T, E), dev)
-    _arg(idx, "idx", i32, (T, k), dev)
-    _arg(mask, "mask", torch.uint8, (T,), dev, optional=True)
+    lp = _arg(logits, "logits", f32, (T, E), dev)
+    ip = _arg(idx, "idx", i32, (T, k), dev)
+    mp = _arg(mask, "mask", torch.uint8, (T,), dev, True)
     loss = _out(loss, "loss", f32, (3,), dev)
     counts = _out(counts, "counts", i32, (E,), dev)
     n_tokens = _out(n_tokens, "n_tokens", i32, (1,), dev)
     nb = fe_moe_balance_workspace(T, E)
     ws = torch.empty(max(nb, 1), dtype=torch.uint8, device=dev)
     with _device(dev):
-        check(fe_moe_balance_loss(_dptr(logits), _dptr(idx), _dptr(mask), T, E, k, balance_coef, z_coef, _dptr(loss),
-                                  _dptr(counts), _dptr(n_tokens), _dptr(ws), nb, _stream_ptr(None)),
-              "fe_moe_balance_loss")
+        check(fe_moe_balance_loss(lp, ip, mp, T, E, k, balance_coef, z_coef, loss.data_ptr(), counts.data_ptr(),
+                                  n_tokens.data_ptr(), ws.data_ptr(), nb, _current_stream(dev)), "fe_moe_balance_loss")
     return loss, counts, n_tokens
 
 
@@ -643,19 +656,18 @@ def balance_loss_backward(logits, counts, n_tokens, top_k: int, mask=None, dloss
         with _on_stream(stream, logits.device):
             return balance_loss_backward(logits, counts, n_tokens, top_k, mask, dloss, balance_coef, z_coef, dlogits, dtype)
     import torch
-    f32, dev = torch.float32, logits.device
+    f32, i32, dev = torch.float32, torch.int32, logits.device
     T, E = logits.shape
-    _arg(logits, "logits", f32, (T, E), dev)
-    _arg(counts, "counts", torch.int32, (E,), dev)
-    _arg(n_tokens, "n_tokens", torch.int32, (1,), dev)
-    _arg(mask, "mask", torch.uint8, (T,), dev, optional=True)
-    _arg(dloss, "dloss", f32, (1,), dev, optional=True)
+    lp = _arg(logits, "logits", f32, (T, E), dev)
+    cp = _arg(counts, "counts", i32, (E,), dev)
+    np_ = _arg(n_tokens, "n_tokens", i32, (1,), dev)
+    mp = _arg(mask, "mask", torch.uint8, (T,), dev, True)
+    dp = _arg(dloss, "dloss", f32, (1,), dev, True)
     dlogits = _out(dlogits, "dlogits", dtype or (f32 if dlogits is None else dlogits.dtype), (T, E), dev)
     dt = _dtype_of(dlogits, "dlogits")
     with _device(dev):
-        check(fe_moe_balance_loss_backward(_dptr(logits), _dptr(counts), _dptr(n_tokens), _dptr(mask), _dptr(dloss), T, E,
-                                           top_k, balance_coef, z_coef, _dptr(dlogits), dt, _stream_ptr(None)),
-              "fe_moe_balance_loss_backward")
+        check(fe_moe_balance_loss_backward(lp, cp, np_, mp, dp, T, E, top_k, balance_coef, z_coef, dlogits.data_ptr(), dt,
+                                           _current_stream(dev)), "fe_moe_balance_loss_backward")
     return dlogits
 
 
@@ -670,18 +682,17 @@ def linear(x, w, bias=None, act=ACT_NONE, residual=None, y=None, z=None, stream=
     bf, dev = torch.bfloat16, x.device
     M, K = x.shape
     N = w.shape[0]
-    cols = N // 2 if act == ACT_SWIGLU else N
-    ldx = _arg_rows(x, "x", bf, (M, K), dev)
-    _arg(w, "w", bf, (N, K), dev)
-    _arg(bias, "bias", bf, (N,), dev, optional=True)
-    _arg(z, "z", bf, (M, N), dev, optional=True)
-    ldr = 0 if residual is None else _arg_rows(residual, "residual", bf, (M, cols), dev)
+    out = (M, N // 2 if act == ACT_SWIGLU else N)
+    xp, ldx = _arg_rows(x, "x", bf, (M, K), dev)
+    wp = _arg(w, "w", bf, (N, K), dev)
+    bp = _arg(bias, "bias", bf, (N,), dev, True)
+    zp = _arg(z, "z", bf, (M, N), dev, True)
+    resp, ldr = (None, 0) if residual is None else _arg_rows(residual, "residual", bf, out, dev)
     if y is None:
-        y = torch.empty((M, cols), dtype=bf, device=dev)
-    ldy = _arg_rows(y, "y", bf, (M, cols), dev)
+        y = torch.empty(out, dtype=bf, device=dev)
+    yp, ldy = _arg_rows(y, "y", bf, out, dev)
     with _device(dev):
-        check(fe_moe_linear(_dptr(x), ldx, _dptr(w), _dptr(bias), _dptr(residual), ldr, M, N, K, act, _dptr(y), ldy,
-                            _dptr(z), _stream_ptr(None)), "fe_moe_linear")
+        check(fe_moe_linear(xp, ldx, wp, bp, resp, ldr, M, N, K, act, yp, ldy, zp, _current_stream(dev)), "fe_moe_linear")
     return y
 
 
@@ -695,19 +706,18 @@ def linear_backward(dy, x, w, z=None, act=ACT_NONE, need_dx=True, need_dw=True, 
     bf, dev = torch.bfloat16, x.device
     M, K = x.shape
     N = w.shape[0]
-    cols = N // 2 if act == ACT_SWIGLU else N
-    ldx = _arg_rows(x, "x", bf, (M, K), dev)
-    _arg(w, "w", bf, (N, K), dev)
-    _arg(z, "z", bf, (M, N), dev, optional=act == ACT_NONE)
-    lddy = _arg_rows(dy, "dy", bf, (M, cols), dev)
+    xp, ldx = _arg_rows(x, "x", bf, (M, K), dev)
+    wp = _arg(w, "w", bf, (N, K), dev)
+    zp = _arg(z, "z", bf, (M, N), dev, act == ACT_NONE)
+    dyp, lddy = _arg_rows(dy, "dy", bf, (M, N // 2 if act == ACT_SWIGLU else N), dev)
     dx = torch.empty((M, K), dtype=bf, device=dev) if need_dx else None
     dw = torch.empty((N, K), dtype=bf, device=dev) if need_dw else None
     db = torch.empty((N,), dtype=torch.float32, device=dev) if need_db else None
     nb = fe_moe_linear_workspace(M, N, K, act)
     ws = torch.empty(max(nb, 16), dtype=torch.uint8, device=dev)
     with _device(dev):
-        check(fe_moe_linear_backward(_dptr(dy), lddy, _dptr(x), ldx, _dptr(w), _dptr(z), M, N, K, act, _dptr(dx), K,
-                                     _dptr(dw), _dptr(db), _dptr(ws), nb, _stream_ptr(None)), "fe_moe_linear_backward")
+        check(fe_moe_linear_backward(dyp, lddy, xp, ldx, wp, zp, M, N, K, act, _dptr(dx), K, _dptr(dw), _dptr(db),
+                                     ws.data_ptr(), nb, _current_stream(dev)), "fe_moe_linear_backward")
     return dx, dw, db
 
 

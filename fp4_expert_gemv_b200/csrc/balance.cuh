@@ -15,11 +15,12 @@
 namespace fe {
 
 constexpr int kBalMaxE = 1024;
-constexpr int kBalThreads = 256, kBalWarps = kBalThreads / 32;   // backward
-constexpr int kBalCluster = 8;                                   // CTAs that join partial sums
-// Warps of a forward CTA by values per lane: their sums of p share 32 KB.
-__host__ __device__ constexpr int bal_warps(int npl) { return npl <= 8 ? 32 : 256 / npl; }
+constexpr int kBalThreads = 256, kBalWarps = kBalThreads / 32;
+constexpr int kBalCluster = 8;   // CTAs that join partial sums
 
+// A row is held by L lanes (a power of two) with N values each: 16 values (E up to 512) keep four 16-byte
+// loads per lane in flight whatever E is, and a warp takes 32 / L rows at once with log2 L shuffles
+// per sum; rows of more than 512 have 32 values.
 struct BalanceParams {
     const float* logits;      // [T][E]
     const int32_t* idx;       // [T][k]; ids outside [0, E) are not counted
@@ -39,51 +40,55 @@ struct BalanceParams {
     int dl_bf16;
 };
 
-// Lane's values of a row: element (i * 32 + lane) * VEC + j for i < NPL / VEC.
-template <int NPL, int VEC>
-FE_DEV int bal_elem(int i, int lane) { return ((i / VEC) * 32 + lane) * VEC + i % VEC; }
+// Value i of lane r of a row's L lanes: consecutive VEC values per lane, L lanes side by side.
+template <int L, int VEC>
+FE_DEV int bal_elem(int i, int r) { return ((i / VEC) * L + r) * VEC + i % VEC; }
 
-template <int NPL, int VEC>
-FE_DEV void bal_load(const float* row, int E, int lane, float (&l)[NPL])
+template <int L, int N, int VEC>
+FE_DEV void bal_load(const float* row, int E, int r, bool on, float (&l)[N])
 {
-    if (VEC == 4) {
 #pragma unroll
-        for (int i = 0; i < NPL; i += VEC) {
-            const int e = bal_elem<NPL, VEC>(i, lane);
+    for (int i = 0; i < N; i += VEC) {
+        const int e = bal_elem<L, VEC>(i, r);
+        if constexpr (VEC == 4) {
             float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-            if (e < E) v = __ldg(reinterpret_cast<const float4*>(row + e));
+            if (on && e < E) v = *reinterpret_cast<const float4*>(row + e);
             l[i] = v.x;
-            l[(i + 1) % NPL] = v.y;
-            l[(i + 2) % NPL] = v.z;
-            l[(i + 3) % NPL] = v.w;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) {
-            const int e = bal_elem<NPL, VEC>(i, lane);
-            l[i] = e < E ? __ldg(row + e) : -INFINITY;
+            l[i + 1] = v.y;
+            l[i + 2] = v.z;
+            l[i + 3] = v.w;
+        } else {
+            l[i] = on && e < E ? row[e] : -INFINITY;
         }
     }
 }
 
+template <int L>
+FE_DEV float bal_row_sum(float v)
+{
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
 // l -> softmax numerators exp(l - max), returns 1 / sum and the logsumexp; 0 and 0 for a row of
 // -inf.  NaN or +inf anywhere makes both NaN, as the formula does.
-template <int NPL>
-FE_DEV void bal_softmax(float (&l)[NPL], float& inv, float& lse)
+template <int L, int N>
+FE_DEV void bal_softmax(float (&l)[N], float& inv, float& lse)
 {
     float m = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) m = fmaxf(m, l[i]);
+    for (int i = 0; i < N; ++i) m = fmaxf(m, l[i]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float mm = m == -INFINITY ? 0.0f : m;
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
+    for (int i = 0; i < N; ++i) {
         l[i] = __expf(l[i] - mm);
         s += l[i];
     }
-    s = warp_sum(s);
+    s = bal_row_sum<L>(s);
     inv = s == 0.0f ? 0.0f : 1.0f / s;
     lse = s == 0.0f ? 0.0f : mm + logf(s);
 }
@@ -127,59 +132,66 @@ FE_DEV float bal_block_sum(float v, float* scratch)
     return s;
 }
 
-// A warp takes every so many-th row, with the next one's loads under way; per lane the sums of its
-// experts' p.  For a batch of a few rows per warp of one cluster (p.G = 0) the CTAs join their sums
-// through distributed shared memory and the loss is one launch (T = 64, E = 128: 8.1 us as two
-// launches); beyond, each CTA leaves a partial for balance_final_kernel.
-template <int NPL, int VEC>
-__global__ void __launch_bounds__(32 * bal_warps(NPL)) balance_kernel(BalanceParams p)
+// A warp takes every so many-th group of 32 / L rows, with the next group's loads under way; per lane the
+// sums of its experts' p.  For a batch of a few groups per warp of one cluster (p.G = 0) the CTAs
+// join their sums through distributed shared memory and the loss is one launch (T = 64, E = 128:
+// 8.1 us as two launches); beyond, each CTA leaves a partial for balance_final_kernel.
+template <int L, int N, int VEC>
+__global__ void __launch_bounds__(kBalThreads, N == 16 ? 3 : 1) balance_kernel(BalanceParams p)
 {
-    constexpr int W = bal_warps(NPL);
-    __shared__ float ps[W][32 * NPL];
-    __shared__ int cnt[kBalMaxE];
+    constexpr int W = kBalWarps, R = 32 / L;
+    __shared__ float ps[W][L * N];
+    __shared__ int cnt[L * N];
     __shared__ float scratch[32];
     __shared__ float sums[2];
     __shared__ int ns[32], n_all;
     griddep_wait();
     griddep_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r = lane % L, sub = lane / L;
     for (int e = threadIdx.x; e < p.E; e += 32 * W) cnt[e] = 0;
     __syncthreads();
-    float acc[NPL], next[NPL];
+    float acc[N], next[N];
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) acc[i] = 0.0f;
+    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
     float z = 0.0f;
     int n = 0;
-    const int64_t step = (int64_t)gridDim.x * W;
-    auto kept = [&](int64_t t) { return !p.mask || p.mask[t] != 0; };
-    int64_t t = (int64_t)blockIdx.x * W + warp;
-    while (t < p.T && !kept(t)) t += step;   // the warp's lanes agree
-    if (t < p.T) bal_load<NPL, VEC>(p.logits + (size_t)t * p.E, p.E, lane, next);
-    while (t < p.T) {
-        float l[NPL], inv, lse;
+    const int64_t step = (int64_t)gridDim.x * W * R;
+    int64_t t0 = ((int64_t)blockIdx.x * W + warp) * R;   // the warp's group of rows
+    bool on = t0 + sub < p.T && (!p.mask || p.mask[t0 + sub] != 0);
+    bal_load<L, N, VEC>(p.logits + (size_t)(on ? t0 + sub : 0) * p.E, p.E, r, on, next);
+    for (; t0 < p.T; t0 += step) {
+        float l[N], inv, lse;
+        const bool now = on;
+        const int64_t t = t0 + sub, tn = t + step;
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) l[i] = next[i];
-        int e0 = -1;
-        if (lane < p.k) e0 = p.idx[(size_t)t * p.k + lane];
-        int64_t tn = t + step;
-        while (tn < p.T && !kept(tn)) tn += step;
-        if (tn < p.T) bal_load<NPL, VEC>(p.logits + (size_t)tn * p.E, p.E, lane, next);
-        bal_softmax<NPL>(l, inv, lse);
+        for (int i = 0; i < N; ++i) l[i] = next[i];
+        on = tn < p.T && (!p.mask || p.mask[tn] != 0);
+        bal_load<L, N, VEC>(p.logits + (size_t)(on ? tn : 0) * p.E, p.E, r, on, next);
+        if (now)
+            for (int j = r; j < p.k; j += L) {
+                const int e = p.idx[(size_t)t * p.k + j];
+                if ((unsigned)e < (unsigned)p.E) atomicAdd(&cnt[e], 1);   // integers: any order, one result
+            }
+        __syncwarp();
+        bal_softmax<L, N>(l, inv, lse);   // a row that is off is all -inf: zeros
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) acc[i] += l[i] * inv;
-        z += lse * lse;
-        ++n;
-        if ((unsigned)e0 < (unsigned)p.E) atomicAdd(&cnt[e0], 1);   // integers: any order, one result
-        for (int j = lane + 32; j < p.k; j += 32) {
-            const int e = p.idx[(size_t)t * p.k + j];
-            if ((unsigned)e < (unsigned)p.E) atomicAdd(&cnt[e], 1);
+        for (int i = 0; i < N; ++i) acc[i] += l[i] * inv;
+        if (r == 0) {
+            z += lse * lse;
+            n += now;
         }
-        t = tn;
     }
+    // the warp's row groups join
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) ps[warp][bal_elem<NPL, VEC>(i, lane)] = acc[i];
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+        for (int o = L; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+        if (sub == 0) ps[warp][bal_elem<L, VEC>(i, r)] = acc[i];
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
     if (lane == 0) ns[warp] = n;
-    const float zz = bal_block_sum(lane == 0 ? z : 0.0f, scratch);   // and every warp's sums are in place
+    const float zz = bal_block_sum(z, scratch);   // and every warp's sums are in place
     int nn = 0;
     if (threadIdx.x == 0)
         for (int w = 0; w < W; ++w) nn += ns[w];
@@ -226,38 +238,50 @@ __global__ void __launch_bounds__(32 * bal_warps(NPL)) balance_kernel(BalancePar
     bal_finish(p, sums, &n_all, rank, ranks);
 }
 
-// Joins the CTAs' partials in a fixed order and writes the loss and the counts: one cluster, each CTA
-// 32 experts at a time with 32 threads down the partials of a column.
+// Joins the CTAs' partials in a fixed order and writes the loss and the counts: one cluster, each CTA an
+// eighth of the experts, 32 threads down the partials of a column.
 __global__ void __cluster_dims__(kBalCluster, 1, 1) __launch_bounds__(1024) balance_final_kernel(BalanceParams p)
 {
-    __shared__ float sf[32][33];
-    __shared__ int si[32][33];
+    constexpr int B = kBalMaxE / 32 / kBalCluster;   // blocks of 32 experts per CTA, at most
+    __shared__ float sf[B][32][33];
+    __shared__ int si[B][32][33];
     __shared__ float scratch[32];
     __shared__ float sums[2];
     __shared__ int n_all;
     griddep_wait();
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
     const uint32_t rank = cluster_rank();
-    float fp = 0.0f;   // lane 0 of warp y: sum of counts * P over its experts
-    for (int e0 = 32 * rank; e0 < p.E; e0 += 32 * kBalCluster) {
-        const int e = e0 + x;
-        float v = 0.0f;
-        int c = 0;
-        if (e < p.E) {
+    float v[B];
+    int c[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+        v[b] = 0.0f;
+        c[b] = 0;
+    }
 #pragma unroll 4
-            for (int g = y; g < p.G; g += 32) {
-                v += p.part[(size_t)g * p.E + e];
-                c += p.ipart[(size_t)g * p.E + e];
+    for (int g = y; g < p.G; g += 32)
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const int e = 32 * (rank + kBalCluster * b) + x;
+            if (e < p.E) {
+                v[b] += p.part[(size_t)g * p.E + e];
+                c[b] += p.ipart[(size_t)g * p.E + e];
             }
         }
-        __syncthreads();
-        sf[y][x] = v;
-        si[y][x] = c;
-        __syncthreads();
-        const float P = warp_sum(sf[x][y]);
-        const int cs = __reduce_add_sync(0xffffffffu, si[x][y]);
-        if (x == 0 && e0 + y < p.E) {
-            p.counts[e0 + y] = cs;
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+        sf[b][y][x] = v[b];
+        si[b][y][x] = c[b];
+    }
+    __syncthreads();
+    float fp = 0.0f;   // lane 0 of warp y: sum of counts * P over its experts
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+        const int e = 32 * (rank + kBalCluster * b) + y;
+        const float P = warp_sum(sf[b][x][y]);
+        const int cs = __reduce_add_sync(0xffffffffu, si[b][x][y]);
+        if (x == 0 && e < p.E) {
+            p.counts[e] = cs;
             fp += (float)cs * P;
         }
     }
@@ -280,62 +304,54 @@ __global__ void __cluster_dims__(kBalCluster, 1, 1) __launch_bounds__(1024) bala
     bal_finish(p, sums, &n_all, rank, kBalCluster);
 }
 
-template <int NPL, int VEC>
+template <int L, int N, int VEC>
 __global__ void __launch_bounds__(kBalThreads) balance_backward_kernel(BalanceParams p)
 {
+    constexpr int W = kBalWarps, R = 32 / L;
     griddep_wait();
+    griddep_launch();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r = lane % L, sub = lane / L;
     const int n = *p.n_tokens;
     const float up = (p.dloss ? *p.dloss : 1.0f) / (float)max(n, 1);
     const float fscale = 1.0f / ((float)max(n, 1) * (float)p.k);
-    float f[NPL];
+    float f[N];
 #pragma unroll
-    for (int i = 0; i < NPL; ++i) {
-        const int e = bal_elem<NPL, VEC>(i, lane);
+    for (int i = 0; i < N; ++i) {
+        const int e = bal_elem<L, VEC>(i, r);
         f[i] = e < p.E ? (float)p.counts[e] * fscale : 0.0f;
     }
     const float ca = up * p.a * (float)p.E, cb = 2.0f * up * p.b;
-    for (int64_t t = (int64_t)blockIdx.x * kBalWarps + warp; t < p.T; t += (int64_t)gridDim.x * kBalWarps) {
-        const bool keep = !p.mask || p.mask[t] != 0;
-        float l[NPL];
-        if (keep) {
-            float inv, lse, d = 0.0f;
-            bal_load<NPL, VEC>(p.logits + (size_t)t * p.E, p.E, lane, l);
-            bal_softmax<NPL>(l, inv, lse);
+    for (int64_t t0 = ((int64_t)blockIdx.x * W + warp) * R; t0 < p.T; t0 += (int64_t)gridDim.x * W * R) {
+        const int64_t t = t0 + sub;
+        const bool on = t < p.T && (!p.mask || p.mask[t] != 0);
+        float l[N], inv, lse, d = 0.0f;
+        bal_load<L, N, VEC>(p.logits + (size_t)(on ? t : 0) * p.E, p.E, r, on, l);
+        bal_softmax<L, N>(l, inv, lse);   // a row that is off is all -inf: zeros
 #pragma unroll
-            for (int i = 0; i < NPL; ++i) {
-                l[i] *= inv;
-                d += l[i] * f[i];
-            }
-            d = warp_sum(d);
-#pragma unroll
-            for (int i = 0; i < NPL; ++i) l[i] *= ca * (f[i] - d) + cb * lse;
-        } else {
-#pragma unroll
-            for (int i = 0; i < NPL; ++i) l[i] = 0.0f;
+        for (int i = 0; i < N; ++i) {
+            l[i] *= inv;
+            d += l[i] * f[i];
         }
-        if (VEC == 4) {
+        d = bal_row_sum<L>(d);
 #pragma unroll
-            for (int i = 0; i < NPL; i += VEC) {
-                const int e = bal_elem<NPL, VEC>(i, lane);
-                if (e >= p.E) continue;
-                const float a = l[i], b = l[(i + 1) % NPL], c = l[(i + 2) % NPL], d = l[(i + 3) % NPL];
-                if (p.dl_bf16)
-                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.dlogits) + (size_t)t * p.E + e) =
-                        make_uint2(bf16x2_rn(a, b), bf16x2_rn(c, d));
-                else
-                    *reinterpret_cast<float4*>(static_cast<float*>(p.dlogits) + (size_t)t * p.E + e) =
-                        make_float4(a, b, c, d);
-            }
-        } else {
+        for (int i = 0; i < N; ++i) l[i] = on ? l[i] * (ca * (f[i] - d) + cb * lse) : 0.0f;
+        if (t >= p.T) continue;
 #pragma unroll
-            for (int i = 0; i < NPL; ++i) {
-                const int e = bal_elem<NPL, VEC>(i, lane);
-                if (e >= p.E) continue;
+        for (int i = 0; i < N; i += VEC) {
+            const int e = bal_elem<L, VEC>(i, r);
+            if (e >= p.E) continue;
+            const size_t at = (size_t)t * p.E + e;
+            if constexpr (VEC == 4) {
                 if (p.dl_bf16)
-                    static_cast<uint16_t*>(p.dlogits)[(size_t)t * p.E + e] = (uint16_t)(bf16x2_rn(l[i], 0.0f) & 0xffffu);
+                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.dlogits) + at) =
+                        make_uint2(bf16x2_rn(l[i], l[i + 1]), bf16x2_rn(l[i + 2], l[i + 3]));
                 else
-                    static_cast<float*>(p.dlogits)[(size_t)t * p.E + e] = l[i];
+                    *reinterpret_cast<float4*>(static_cast<float*>(p.dlogits) + at) =
+                        make_float4(l[i], l[i + 1], l[i + 2], l[i + 3]);
+            } else {
+                if (p.dl_bf16) static_cast<uint16_t*>(p.dlogits)[at] = (uint16_t)(bf16x2_rn(l[i], 0.0f) & 0xffffu);
+                else static_cast<float*>(p.dlogits)[at] = l[i];
             }
         }
     }

@@ -189,19 +189,24 @@ cudaError_t norm_bwd_launch(const fe::NormBwdParams& q, bool vec, bool r32, cons
 
 // ---- balance loss -------------------------------------------------------------------------
 
-// Values per lane of a row of E logits.
-int balance_npl(int E) { return E <= 32 ? 1 : E <= 64 ? 2 : E <= 128 ? 4 : E <= 256 ? 8 : E <= 512 ? 16 : 32; }
-
-// CTAs of the forward pass, one row per warp up to kMaxBalanceCtas of them.
-constexpr int kMaxBalanceCtas = 296;
-int balance_ctas(int64_t T, int E)
+// Lanes that hold a row of E logits, 16 values each (32 beyond 512).
+int balance_lanes(int E)
 {
-    const int w = fe::bal_warps(balance_npl(E));
-    return (int)std::max<int64_t>(1, std::min<int64_t>(kMaxBalanceCtas, (T + w - 1) / w));
+    int l = 1;
+    while (l < 32 && 16 * l < E) l *= 2;
+    return l;
 }
 
-// Rows per warp up to which one cluster takes the whole loss.
-constexpr int kBalanceFusedRows = 4;
+// CTAs of the forward pass: a group of rows per warp, up to kMaxBalanceCtas of them.
+constexpr int kMaxBalanceCtas = 444;
+int balance_ctas(int64_t T, int E)
+{
+    const int rows = fe::kBalWarps * (32 / balance_lanes(E));
+    return (int)std::max<int64_t>(1, std::min<int64_t>(kMaxBalanceCtas, (T + rows - 1) / rows));
+}
+
+// Groups of rows per warp up to which one cluster takes the whole loss.
+constexpr int kBalanceFusedGroups = 4;
 
 fe_status check_balance(const float* logits, const uint8_t*, int64_t T, int E, int top_k)
 {
@@ -210,12 +215,13 @@ fe_status check_balance(const float* logits, const uint8_t*, int64_t T, int E, i
     return FE_OK;
 }
 
-template <int NPL, int VEC>
-cudaError_t balance_forward(const fe::BalanceParams& p, int grid, cudaStream_t s)
+template <int L, int N, int VEC>
+cudaError_t balance_run(const fe::BalanceParams& p, bool backward, int grid, cudaStream_t s)
 {
+    if (backward) return launch(fe::balance_backward_kernel<L, N, VEC>, grid, fe::kBalThreads, 0, s, p);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(32 * fe::bal_warps(NPL));
+    cfg.blockDim = dim3(fe::kBalThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -225,36 +231,30 @@ cudaError_t balance_forward(const fe::BalanceParams& p, int grid, cudaStream_t s
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, fe::balance_kernel<NPL, VEC>, p);
+    return cudaLaunchKernelEx(&cfg, fe::balance_kernel<L, N, VEC>, p);
 }
 
-template <int NPL>
-cudaError_t balance_launch(const fe::BalanceParams& p, bool backward, int grid, bool vec, cudaStream_t s)
+template <int L, int N>
+cudaError_t balance_vec(const fe::BalanceParams& p, bool backward, int grid, bool vec, cudaStream_t s)
 {
-    if constexpr (NPL >= 4) {
-        if (vec)
-            return backward ? launch(fe::balance_backward_kernel<NPL, 4>, grid, fe::kBalThreads, 0, s, p)
-                            : balance_forward<NPL, 4>(p, grid, s);
-    }
-    return backward ? launch(fe::balance_backward_kernel<NPL, 1>, grid, fe::kBalThreads, 0, s, p)
-                    : balance_forward<NPL, 1>(p, grid, s);
+    return vec ? balance_run<L, N, 4>(p, backward, grid, s) : balance_run<L, N, 1>(p, backward, grid, s);
 }
 
 cudaError_t balance_dispatch(const fe::BalanceParams& p, bool backward, int grid, bool vec, cudaStream_t s)
 {
-    switch (balance_npl(p.E)) {
-        case 1: return balance_launch<1>(p, backward, grid, vec, s);
-        case 2: return balance_launch<2>(p, backward, grid, vec, s);
-        case 4: return balance_launch<4>(p, backward, grid, vec, s);
-        case 8: return balance_launch<8>(p, backward, grid, vec, s);
-        case 16: return balance_launch<16>(p, backward, grid, vec, s);
+    if (p.E > 512) return balance_vec<32, 32>(p, backward, grid, vec, s);
+    switch (balance_lanes(p.E)) {
+        case 1: return balance_vec<1, 16>(p, backward, grid, vec, s);
+        case 2: return balance_vec<2, 16>(p, backward, grid, vec, s);
+        case 4: return balance_vec<4, 16>(p, backward, grid, vec, s);
+        case 8: return balance_vec<8, 16>(p, backward, grid, vec, s);
+        case 16: return balance_vec<16, 16>(p, backward, grid, vec, s);
     }
-    return balance_launch<32>(p, backward, grid, vec, s);
+    return balance_vec<32, 16>(p, backward, grid, vec, s);
 }
 
 // ---- dense product --------------------------------------------------------------------------
 
-constexpr int kLinRowsMax = 8;   // rows that stream the weights without tensor cores
 
 bool act_ok(int act, int N) { return act >= FE_ACT_NONE && act <= FE_ACT_SWIGLU && (act != FE_ACT_SWIGLU || N % 2 == 0); }
 int out_cols(int act, int N) { return act == FE_ACT_SWIGLU ? N / 2 : N; }
@@ -461,6 +461,7 @@ cudaError_t lin_run(fe::LinParams& P, const Product* f, int n, cudaStream_t s)
 }
 
 // Products of few tiles, the contraction split over clusters.
+template <bool GLU>
 cudaError_t split_launch(const fe::LinProblem& q, const Product& f, int splits, cudaStream_t s)
 {
     static std::atomic<bool> ready[64];
@@ -469,7 +470,8 @@ cudaError_t split_launch(const fe::LinProblem& q, const Product& f, int splits, 
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!ready[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(fe::linear_split_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)fe::kSplSmem);
+        e = cudaFuncSetAttribute(fe::linear_split_kernel<GLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)fe::spl_smem(fe::kSplStages));
         if (e != cudaSuccess) return e;
         ready[dev].store(true, std::memory_order_release);
     }
@@ -481,6 +483,8 @@ cudaError_t split_launch(const fe::LinProblem& q, const Product& f, int splits, 
     p.N = f.N;
     p.K = f.K;
     p.splits = splits;
+    const int steps = (f.K + 63) / 64;
+    p.stages = std::min(fe::kSplStages, (steps + splits - 1) / splits);
     p.act = q.act;
     p.cols = q.cols;
     p.bias = q.bias;
@@ -493,7 +497,7 @@ cudaError_t split_launch(const fe::LinProblem& q, const Product& f, int splits, 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((q.cols + w - 1) / w, (f.M + 127) / 128, splits);
     cfg.blockDim = dim3(fe::kSplThreads);
-    cfg.dynamicSmemBytes = fe::kSplSmem;
+    cfg.dynamicSmemBytes = fe::spl_smem(p.stages);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -503,7 +507,7 @@ cudaError_t split_launch(const fe::LinProblem& q, const Product& f, int splits, 
     attr[1].val.clusterDim.z = splits;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, fe::linear_split_kernel, p);
+    return cudaLaunchKernelEx(&cfg, fe::linear_split_kernel<GLU>, p);
 }
 
 // CTAs that share a tile's contraction: as many (a power of two, to 8) as fill the SMs and leave each at
@@ -521,11 +525,13 @@ int split_ways(const fe::LinProblem& q, const Product& f, int sms)
 template <bool GLU>
 cudaError_t rows_launch(const fe::LinRowsParams& p, cudaStream_t s)
 {
-    const int grid = (p.cols + fe::kLinRowsWarps - 1) / fe::kLinRowsWarps, block = 32 * fe::kLinRowsWarps;
-    if (p.M == 1) return launch(fe::linear_rows_kernel<1, GLU>, grid, block, 0, s, p);
-    if (p.M == 2) return launch(fe::linear_rows_kernel<2, GLU>, grid, block, 0, s, p);
-    if (p.M <= 4) return launch(fe::linear_rows_kernel<4, GLU>, grid, block, 0, s, p);
-    return launch(fe::linear_rows_kernel<8, GLU>, grid, block, 0, s, p);
+    if (p.M == 1) {
+        const int grid = (p.cols + fe::kLinRowsWarps - 1) / fe::kLinRowsWarps;
+        return launch(fe::linear_rows_kernel<1, GLU>, grid, 32 * fe::kLinRowsWarps, 0, s, p);
+    }
+    const int grid = (p.cols + (GLU ? 7 : 15)) / (GLU ? 8 : 16);
+    if (p.M <= 8) return launch(fe::linear_skinny_kernel<1, GLU>, grid, 256, 0, s, p);
+    return launch(fe::linear_skinny_kernel<2, GLU>, grid, 256, 0, s, p);
 }
 
 // Backward workspace: dz [M][roundup8(N)] bf16, then the column partials.
@@ -717,8 +723,8 @@ fe_status fe_moe_balance_loss(const float* logits, const int32_t* idx, const uin
     const int ctas = balance_ctas(T, E);
     const bool vec = E % 4 == 0 && aligned(logits, 16);
     const cudaStream_t s = (cudaStream_t)stream;
-    if (T <= (int64_t)kBalanceFusedRows * fe::kBalCluster * fe::bal_warps(balance_npl(E))) {
-        int n = 1;   // CTAs of the cluster: a row per warp, to eight
+    if (T <= (int64_t)kBalanceFusedGroups * fe::kBalCluster * fe::kBalWarps * (32 / balance_lanes(E))) {
+        int n = 1;   // CTAs of the cluster: a group per warp, to eight
         while (n < fe::kBalCluster && n < ctas) n *= 2;
         p.G = 0;
         FE_CUDA_TRY(balance_dispatch(p, false, n, vec, s));
@@ -766,7 +772,8 @@ fe_status fe_moe_balance_loss_backward(const float* logits, const int32_t* count
     p.dl_bf16 = dlogits_dtype == FE_DTYPE_BF16;
     const int sms = sm_count();
     if (sms < 1) return record_cuda(cudaErrorInvalidDevice, "device");
-    const int grid = (int)std::min<int64_t>((T + fe::kBalWarps - 1) / fe::kBalWarps, 8 * (int64_t)sms);
+    const int rows = fe::kBalWarps * (32 / balance_lanes(E));
+    const int grid = (int)std::min<int64_t>((T + rows - 1) / rows, 8 * (int64_t)sms);
     FE_CUDA_TRY(balance_dispatch(p, true, grid, E % 4 == 0 && aligned(logits, 16) && aligned(dlogits, 4 * eb),
                                  (cudaStream_t)stream));
     return FE_OK;
@@ -780,7 +787,7 @@ fe_status fe_moe_linear(const void* x, int64_t ldx, const void* w, const void* b
     if (M == 0) return FE_OK;
     const cudaStream_t s = (cudaStream_t)stream;
     const int cols = out_cols(act, N);
-    if (M <= kLinRowsMax) {
+    if (M <= fe::kSkinnyMaxM) {
         fe::LinRowsParams p{};
         p.x = static_cast<const uint16_t*>(x);
         p.ldx = ldx;
@@ -813,7 +820,7 @@ fe_status fe_moe_linear(const void* x, int64_t ldx, const void* w, const void* b
     const int sms = sm_count();
     if (sms < 1) return record_cuda(cudaErrorInvalidDevice, "device");
     const int ways = split_ways(p, f, sms);
-    if (ways > 0) FE_CUDA_TRY(split_launch(p, f, ways, s));
+    if (ways > 0) FE_CUDA_TRY(act == FE_ACT_SWIGLU ? split_launch<true>(p, f, ways, s) : split_launch<false>(p, f, ways, s));
     else FE_CUDA_TRY(lin_run(P, &f, 1, s));
     return FE_OK;
 }

@@ -72,6 +72,23 @@ FE_DEV float act_bwd(int act, float z)
     return 1.0f;
 }
 
+// act over an array, the choice made once.
+template <int N>
+FE_DEV void act_all(int act, float (&v)[N])
+{
+    if (act == kActNone) return;
+    if (act == kActRelu) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = act_fwd(kActRelu, v[j]);
+    } else if (act == kActGelu) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = act_fwd(kActGelu, v[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = act_fwd(kActSilu, v[j]);
+    }
+}
+
 // ---- tensor-core tiles ---------------------------------------------------------------
 
 constexpr unsigned long long kLinTimeoutNs = 2000ull * 1000 * 1000;
@@ -545,10 +562,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                                 st.put(2, lane, v);
                                 st.flush(2, lane, tz, vec_z, true, zo, N, row0, M, c0, cols);
                             }
-                            if (act != kActNone) {
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) v[j] = act_fwd(act, v[j]);
-                            }
+                            act_all<32>(act, v);
                         }
                         if (has_res) {
                             const uint32_t turn = nres - 1;   // this block's fetch
@@ -606,15 +620,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
 // ---- few tiles: the contraction split over a cluster --------------------------------------
 
 constexpr int kSplN = 64;                     // columns of a tile (swiglu: 32 gate and their 32 up columns)
-constexpr int kSplStages = 8;
-constexpr int kSplThreads = 256;               // warp 0: TMA, 1: MMA, 2: TMEM; then all finish
+constexpr int kSplStages = 7;
+constexpr int kSplThreads = 256;              // warp 0: TMA, 1: MMA, 2: TMEM; then all finish
 constexpr uint32_t kSplStage = 128 * 128 + kSplN * 128;
-constexpr int kSplLd = kSplN + 4;             // fp32 partial rows in shared memory: 16-byte accesses of 8 rows hit every bank
-constexpr uint32_t kSplSmem = 1024 + kSplStages * kSplStage + 8 * (2 * kSplStages + 1) + 16;
+constexpr int kSplLd = kSplN + 4;             // fp32 rows in shared memory: 16-byte accesses of 8 rows hit every bank
+constexpr uint32_t kSplPart = 128 * kSplLd * 4;   // [splits][128 / splits][kSplLd] partial rows this CTA finishes
+// Shared memory for `stages` stages: short contractions take few, so that CTAs of consecutive launches fit
+// an SM together.
+__host__ __device__ constexpr uint32_t spl_smem(int stages)
+{
+    return 1024 + stages * kSplStage + kSplPart + 8 * (2 * stages + 1) + 16;
+}
 
 struct LinSplitParams {
     CUtensorMap ta, tb;      // x: boxes of 64 k x 128 rows; w: 64 k x 32 rows
-    int M, N, K, splits, act, cols;
+    int M, N, K, splits, stages, act, cols;
     const uint16_t* bias;
     const uint16_t* res;
     int64_t ldr;
@@ -623,69 +643,66 @@ struct LinSplitParams {
     uint16_t* z;
 };
 
-// N consecutive values at `at` in every CTA of the cluster, added in rank order.
-template <int N>
-FE_DEV void spl_gather(uint32_t at, int splits, float (&v)[N])
+// Up to 4 consecutive bf16 (left: how many belong to the matrix).
+FE_DEV void spl_store4(uint16_t* o, int left, const float (&v)[4])
 {
-    float q[8][N];
-#pragma unroll
-    for (int s = 0; s < 8; ++s) {
-        if (s >= splits) break;
-        const uint32_t from = cluster_map(at, s);
-#pragma unroll
-        for (int j = 0; j < N; j += 4)
-            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(q[s][j]), "=f"(q[s][j + 1]), "=f"(q[s][j + 2]), "=f"(q[s][j + 3])
-                         : "r"(from + 4 * j));
-    }
-#pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = q[0][j];
-#pragma unroll
-    for (int s = 1; s < 8; ++s) {
-        if (s >= splits) break;
-#pragma unroll
-        for (int j = 0; j < N; ++j) v[j] += q[s][j];
-    }
-}
-
-// Up to 8 consecutive bf16 (left: how many belong to the matrix).
-FE_DEV void spl_store8(uint16_t* o, int left, const float (&v)[8])
-{
-    if (left >= 8 && (reinterpret_cast<uintptr_t>(o) & 15) == 0) {
-        *reinterpret_cast<uint4*>(o) =
-            make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]), bf16x2_rn(v[4], v[5]), bf16x2_rn(v[6], v[7]));
+    const uint32_t a = bf16x2_rn(v[0], v[1]), b = bf16x2_rn(v[2], v[3]);
+    if (left >= 4 && (reinterpret_cast<uintptr_t>(o) & 7) == 0) {
+        *reinterpret_cast<uint2*>(o) = make_uint2(a, b);
     } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < left) o[j] = (uint16_t)(bf16x2_rn(v[j], 0.0f) & 0xffffu);
+        o[0] = (uint16_t)a;
+        if (left > 1) o[1] = (uint16_t)(a >> 16);
+        if (left > 2) o[2] = (uint16_t)b;
+        if (left > 3) o[3] = (uint16_t)(b >> 16);
     }
 }
 
-// One 128 x 64 tile per cluster of `splits` CTAs, each over its share of the k steps; the partial
-// tiles meet through distributed shared memory, every CTA adding (in rank order) and finishing every
-// splits-th row.  For products of so few tiles that whole tiles would leave most SMs idle while the
-// weights stream through the rest.
-__global__ void __launch_bounds__(kSplThreads, 1) linear_split_kernel(const __grid_constant__ LinSplitParams p)
+// v += up to 4 consecutive bf16.
+FE_DEV void spl_add4(const uint16_t* s, int left, float (&v)[4])
 {
-    constexpr int S = kSplStages;
+    if (left >= 4 && (reinterpret_cast<uintptr_t>(s) & 7) == 0) {
+        const uint2 q = *reinterpret_cast<const uint2*>(s);
+        v[0] += __uint_as_float(q.x << 16);
+        v[1] += __uint_as_float(q.x & 0xffff0000u);
+        v[2] += __uint_as_float(q.y << 16);
+        v[3] += __uint_as_float(q.y & 0xffff0000u);
+    } else {
+        v[0] += bf16_bits_to_f32(s[0]);
+        if (left > 1) v[1] += bf16_bits_to_f32(s[1]);
+        if (left > 2) v[2] += bf16_bits_to_f32(s[2]);
+        if (left > 3) v[3] += bf16_bits_to_f32(s[3]);
+    }
+}
+
+// One 128 x 64 tile per cluster of `splits` CTAs (a power of two), each over its share of the k steps.
+// Row i of a CTA's partial tile goes through distributed shared memory to CTA i % splits, which adds
+// that row's partials in rank order and finishes it.  For products of so few tiles that whole tiles
+// would leave most SMs idle while the weights stream through the rest.  Rows are sent, not fetched: a
+// store needs no answer, and nothing is read across CTAs after the one barrier (fetching cost 3 us a
+// launch).  The finish is a short loop: code that runs once is bound by fetching its instructions.
+template <bool GLU>
+__global__ void __launch_bounds__(kSplThreads) linear_split_kernel(const __grid_constant__ LinSplitParams p)
+{
+    const uint32_t S = p.stages;
     extern __shared__ uint8_t lin_dyn[];
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int m0 = blockIdx.y * 128, tn = blockIdx.x;
     const uint32_t rank = blockIdx.z;
     const int nk = (p.K + 63) / 64;
     const int k0 = (int)((int64_t)nk * rank / p.splits), k1 = (int)((int64_t)nk * (rank + 1) / p.splits);
-    const bool glu = p.act == kActSwiglu;
     const uint32_t base0 = tc_saddr(lin_dyn);
     uint8_t* sm = lin_dyn + ((1024u - (base0 & 1023u)) & 1023u);
     const uint32_t ring = tc_saddr(sm);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S * kSplStage);
+    float* part = reinterpret_cast<float*>(sm + S * kSplStage);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S * kSplStage + kSplPart);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 1);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const uint32_t bar0 = tc_saddr(bars);
-    auto full = [&](int s) { return bar0 + 8u * s; };
-    auto empty = [&](int s) { return bar0 + 8u * (S + s); };
+    auto full = [&](uint32_t s) { return bar0 + 8u * s; };
+    auto empty = [&](uint32_t s) { return bar0 + 8u * (S + s); };
     const uint32_t accfull = bar0 + 8u * 2 * S;
-    if (tid <= 2 * S) {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // this CTA runs: its memory may be written
+    if (tid <= 2 * (int)S) {
         tc_mbar_init(bar0 + 8u * tid, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -700,8 +717,9 @@ __global__ void __launch_bounds__(kSplThreads, 1) linear_split_kernel(const __gr
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     griddep_wait();
+    griddep_launch();
     if (warp == 0) {
-        const int n0 = glu ? tn * 32 : tn * 64, n1 = glu ? n0 + p.cols : n0 + 32;
+        const int n0 = GLU ? tn * 32 : tn * 64, n1 = GLU ? n0 + p.cols : n0 + 32;
         uint32_t i = 0;
         for (int k = k0; k < k1; ++k, ++i) {
             const uint32_t s = i % S;
@@ -743,19 +761,22 @@ __global__ void __launch_bounds__(kSplThreads, 1) linear_split_kernel(const __gr
         __syncwarp();
         if (!lin_wait_warp(accfull, 0)) *abort = 1;
     }
-    __syncthreads();   // the products are done and every copy has landed: the ring is free
+    __syncthreads();   // the products are done
     tc_fence_after();
-    float* part = reinterpret_cast<float*>(sm);   // [128][kSplLd]
-    const int rows = min(128, p.M - m0);
+    const int rows = min(128, p.M - m0), lg = 31 - __clz(p.splits), per = 128 >> lg;
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // every CTA of the cluster runs
     {
         const int row = 32 * (warp & 3) + lane, c = 32 * (warp >> 2);
         uint32_t r[32];
         tc_ld32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + c, r);
         tc_wait_ld();
         if (row < rows) {
+            const uint32_t to = cluster_map(tc_saddr(part + (rank * per + (row >> lg)) * kSplLd + c), row & (p.splits - 1));
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-                *reinterpret_cast<uint4*>(part + row * kSplLd + c + 4 * q) = make_uint4(r[4 * q], r[4 * q + 1], r[4 * q + 2], r[4 * q + 3]);
+                asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + 16 * q), "r"(r[4 * q]),
+                             "r"(r[4 * q + 1]), "r"(r[4 * q + 2]), "r"(r[4 * q + 3])
+                             : "memory");
         }
     }
     tc_fence_before();
@@ -764,37 +785,44 @@ __global__ void __launch_bounds__(kSplThreads, 1) linear_split_kernel(const __gr
         tc_fence_after();
         tc_dealloc(tmem, kSplN);
     }
-    // eight columns per thread; rows rank, rank + splits, ...  The partials of a row are all fetched
-    // before the first is added.
-    const int tpr = glu ? 4 : 8, cc = 8 * (tid % tpr);
-    const int col0 = tn * (glu ? 32 : 64) + cc;
-    for (int row = (tid / tpr) * p.splits + rank; row < rows && col0 < p.cols; row += kSplThreads / tpr * p.splits) {
-        const uint32_t at = tc_saddr(part + row * kSplLd + cc);
-        const size_t grow = (size_t)(m0 + row);
-        float v[8], u[8], add[8];
-        const uint16_t* rp = p.res ? p.res + grow * p.ldr + col0 : nullptr;
-        spl_gather<8>(at, p.splits, v);
-        if (glu) spl_gather<8>(at + 32 * 4, p.splits, u);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) add[j] = rp && col0 + j < p.cols ? bf16_bits_to_f32(rp[j]) : 0.0f;
-        if (p.bias) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (col0 + j >= p.cols) break;
-                v[j] += bf16_bits_to_f32(p.bias[col0 + j]);
-                if (glu) u[j] += bf16_bits_to_f32(p.bias[col0 + j + p.cols]);
+    constexpr int TPR = GLU ? 8 : 16;   // threads per row, four columns each
+    const int cc = 4 * (tid % TPR), col0 = tn * (GLU ? 32 : 64) + cc, left = p.cols - col0;
+    if (left > 0) {
+#pragma unroll 1
+        for (int i = tid / TPR; i < per; i += kSplThreads / TPR) {
+            const int row = (i << lg) + rank;
+            if (row >= rows) break;
+            float v[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0};
+            const float* from = part + i * kSplLd + cc;
+#pragma unroll 2
+            for (int s = 0; s < p.splits; ++s, from += per * kSplLd) {
+                const float4 q = *reinterpret_cast<const float4*>(from);
+                v[0] += q.x; v[1] += q.y; v[2] += q.z; v[3] += q.w;
+                if (GLU) {
+                    const float4 w = *reinterpret_cast<const float4*>(from + 32);
+                    u[0] += w.x; u[1] += w.y; u[2] += w.z; u[3] += w.w;
+                }
             }
-        }
-        if (p.z) {
-            spl_store8(p.z + grow * p.N + col0, p.cols - col0, v);
-            if (glu) spl_store8(p.z + grow * p.N + col0 + p.cols, p.cols - col0, u);
-        }
+            const size_t grow = (size_t)(m0 + row);
+            if (p.bias) {
+                spl_add4(p.bias + col0, left, v);
+                if (GLU) spl_add4(p.bias + p.cols + col0, left, u);
+            }
+            if (p.z) {
+                spl_store4(p.z + grow * p.N + col0, left, v);
+                if (GLU) spl_store4(p.z + grow * p.N + p.cols + col0, left, u);
+            }
+            if (GLU) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = (glu ? v[j] * sigmoidf(v[j]) * u[j] : act_fwd(p.act, v[j])) + add[j];
-        spl_store8(p.out + grow * p.ldo + col0, p.cols - col0, v);
+                for (int j = 0; j < 4; ++j) v[j] *= sigmoidf(v[j]) * u[j];
+            } else {
+                act_all<4>(p.act, v);
+            }
+            if (p.res) spl_add4(p.res + grow * p.ldr + col0, left, v);
+            spl_store4(p.out + grow * p.ldo + col0, left, v);
+        }
     }
     if (tid == 0 && *abort) atomicOr(&g_op_status, kDevTcTimeout);
-    cluster_sync();   // no CTA leaves while another still reads its partial tile
 }
 
 // ---- a few rows ------------------------------------------------------------------------
@@ -869,6 +897,94 @@ __global__ void __launch_bounds__(32 * kLinRowsWarps) linear_rows_kernel(LinRows
     }
 }
 
+// ---- a small batch ---------------------------------------------------------------------
+
+constexpr int kSkinnyMaxM = 16;   // N = 1536, K = 2048: 3.9 us at 16 rows (tiles 5.3), 8.8 at 32 (tiles 5.4): every CTA reads all of x
+
+FE_DEV void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A CTA per 16 rows of W (swiglu: 8 gate rows and their up rows) against up to 8 NT rows of x: W's rows
+// are the M side of m16n8k16, x's the N side.  The warps share the contraction, 64 of k at a time, and
+// add their sums through shared memory in warp order.  A lane feeds both operands from 16-byte runs of
+// a row, so the MMAs see k in another order, the same for both.  What bounds it is the latency of one
+// pass over the weights: everything a warp needs of its share is in flight at once, and no tile, TMA or
+// cluster set-up stands before it.
+template <int NT, bool GLU>
+__global__ void __launch_bounds__(256) linear_skinny_kernel(LinRowsParams p)
+{
+    constexpr int LD = 8 * NT + 1, C = GLU ? 8 : 16;
+    __shared__ float red[8][16][LD];
+    griddep_wait();
+    griddep_launch();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int c0 = blockIdx.x * C;
+    const bool lo_on = c0 + g < p.cols, hi_on = GLU ? lo_on : c0 + 8 + g < p.cols;
+    const uint16_t* wlo = p.w + (size_t)(lo_on ? c0 + g : 0) * p.K;
+    const uint16_t* whi = p.w + (size_t)(hi_on ? (GLU ? p.cols + c0 + g : c0 + 8 + g) : 0) * p.K;
+    float acc[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll(NT <= 2 ? 4 : 2)
+    for (int kb = 64 * warp; kb < p.K; kb += 512) {
+        uint4 lo[2], hi[2], x[2][NT];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int k = kb + 32 * h + 8 * t;
+            const bool in = k < p.K;   // K is a multiple of 8
+            lo[h] = in && lo_on ? ldg_stream(wlo + k) : zero;
+            hi[h] = in && hi_on ? ldg_stream(whi + k) : zero;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int m = 8 * n + g;
+                x[h][n] = in && m < p.M ? __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)m * p.ldx + k)) : zero;
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                mma_bf16(acc[n], lo[h].x, hi[h].x, lo[h].y, hi[h].y, x[h][n].x, x[h][n].y);
+                mma_bf16(acc[n], lo[h].z, hi[h].z, lo[h].w, hi[h].w, x[h][n].z, x[h][n].w);
+            }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        float* r = &red[warp][g][8 * n + 2 * t];
+        r[0] = acc[n][0];
+        r[1] = acc[n][1];
+        r[8 * LD] = acc[n][2];
+        r[8 * LD + 1] = acc[n][3];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < C * p.M; i += 256) {
+        const int c = i % C, m = i / C, col = c0 + c;
+        if (col >= p.cols) continue;
+        float z0 = 0.0f, z1 = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            z0 += red[w][c][m];
+            if (GLU) z1 += red[w][c + 8][m];
+        }
+        if (p.bias) {
+            z0 += bf16_bits_to_f32(p.bias[col]);
+            if (GLU) z1 += bf16_bits_to_f32(p.bias[col + p.cols]);
+        }
+        if (p.z) {
+            p.z[(size_t)m * p.N + col] = (uint16_t)(bf16x2_rn(z0, 0.0f) & 0xffffu);
+            if (GLU) p.z[(size_t)m * p.N + col + p.cols] = (uint16_t)(bf16x2_rn(z1, 0.0f) & 0xffffu);
+        }
+        float v = GLU ? z0 * sigmoidf(z0) * z1 : act_fwd(p.act, z0);
+        if (p.res) v += bf16_bits_to_f32(p.res[(size_t)m * p.ldr + col]);
+        p.y[(size_t)m * p.ldy + col] = (uint16_t)(bf16x2_rn(v, 0.0f) & 0xffffu);
+    }
+}
+
 // ---- dZ and its column sums ----------------------------------------------------------------
 
 struct LinDzParams {
@@ -913,12 +1029,12 @@ FE_DEV void dz_store(uint16_t* p, const float (&v)[VEC])
         *p = (uint16_t)(bf16x2_rn(v[0], 0.0f) & 0xffffu);
 }
 
-constexpr int kDzRows = 4;   // rows a thread has in flight
+constexpr int kDzRows = 2;   // rows a thread has in flight
 
 // Block 32 x 8: a thread owns VEC columns, 8 threads share the rows of a chunk.  Bound by memory: dY and
-// Z are read once, dZ written once, so a thread keeps four rows' loads in flight.
+// Z are read once, dZ written once, so a thread keeps two rows' loads in flight and an SM 16 warps.
 template <int VEC>
-__global__ void __launch_bounds__(256) linear_dz_kernel(LinDzParams p)
+__global__ void __launch_bounds__(256, 2) linear_dz_kernel(LinDzParams p)
 {
     using W = typename DzWord<VEC>::T;
     __shared__ float red[8][2 * VEC][33];
