@@ -8,6 +8,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <cstdlib>
 #include <type_traits>
 
 #include "../../include/fe_moe.h"
@@ -155,36 +156,102 @@ cudaError_t norm_launch(const fe::NormParams& p, bool r32, int tpr, cudaStream_t
                : launch(fe::block_norm_kernel<1, C, false>, grid, threads, 0, s, p, tpr);
 }
 
-// Shape of the backward launch: threads per row, threads per CTA, CTAs.
-struct NormBwdPlan {
-    int tpr, chunk, threads, grid;
-    int64_t rows_per_cta;
+// The streamed kernels' launch: groups of tpr threads with 16 columns each, a CTA of 512 threads per SM, as
+// many stages (to four) as fit.
+struct NormRingPlan {
+    int tpr, threads, stages, grid;
     size_t smem;
 };
 
-NormBwdPlan norm_bwd_plan(int64_t T, int H, int sms)
+constexpr size_t kNormRingSmem = 220 * 1024;
+
+bool norm_ring_plan(int64_t T, int H, uint32_t stage, int sms, NormRingPlan* b)
 {
-    NormBwdPlan b;
-    b.chunk = H <= 8192 ? 1 : 2;
-    b.tpr = norm_threads(H, b.chunk);
-    b.threads = std::max(b.tpr, 512);
-    const int groups = b.threads / b.tpr;
-    const int64_t want = std::min<int64_t>(std::min(kMaxPartials, 2 * sms), (T + groups - 1) / groups);
-    const int64_t per = std::max<int64_t>(1, (T + want - 1) / std::max<int64_t>(want, 1));
-    b.rows_per_cta = (per + groups - 1) / groups * groups;
-    b.grid = (int)((T + b.rows_per_cta - 1) / b.rows_per_cta);
-    b.smem = groups > 1 ? sizeof(float) * 3 * H : 0;
-    return b;
+    b->tpr = norm_threads(H, fe::kRingC);
+    if (b->tpr > 512) return false;
+    b->threads = 512;
+    const int groups = b->threads / b->tpr;
+    for (b->stages = 4; b->stages >= 2; --b->stages) {
+        b->smem = (size_t)groups * (b->stages * stage + fe::norm_group_extra(b->tpr, b->stages));
+        if (b->smem <= kNormRingSmem) break;
+    }
+    b->grid = (int)std::min<int64_t>(sms, (T + groups - 1) / groups);
+    return b->stages >= 2;
 }
 
-template <int C, int MAXT>
-cudaError_t norm_bwd_launch(const fe::NormBwdParams& q, bool vec, bool r32, const NormBwdPlan& b, cudaStream_t s)
+// Opts a kernel into kNormRingSmem of shared memory, once per device.
+template <typename K>
+cudaError_t norm_ring_ready(K kernel, std::atomic<bool>* ready)
 {
-    if (vec)
-        return r32 ? launch(fe::block_norm_backward_kernel<8, C, true, MAXT>, b.grid, b.threads, b.smem, s, q, b.tpr)
-                   : launch(fe::block_norm_backward_kernel<8, C, false, MAXT>, b.grid, b.threads, b.smem, s, q, b.tpr);
-    return r32 ? launch(fe::block_norm_backward_kernel<1, C, true, MAXT>, b.grid, b.threads, b.smem, s, q, b.tpr)
-               : launch(fe::block_norm_backward_kernel<1, C, false, MAXT>, b.grid, b.threads, b.smem, s, q, b.tpr);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNormRingSmem);
+        if (e != cudaSuccess) return e;
+        ready[dev].store(true, std::memory_order_release);
+    }
+    return cudaSuccess;
+}
+
+template <bool R32, int GATE>
+cudaError_t norm_ring_launch(const fe::NormParams& p, const NormRingPlan& b, cudaStream_t s)
+{
+    static std::atomic<bool> ready[64];
+    const cudaError_t e = norm_ring_ready(fe::block_norm_ring_kernel<R32, GATE>, ready);
+    if (e != cudaSuccess) return e;
+    return launch(fe::block_norm_ring_kernel<R32, GATE>, b.grid, b.threads, b.smem, s, p, b.tpr, b.stages);
+}
+
+template <bool R32>
+cudaError_t norm_ring(const fe::NormParams& p, const NormRingPlan& b, cudaStream_t s)
+{
+    if (p.gate_kind == FE_GATE_CHANNEL) return norm_ring_launch<R32, fe::kByColumn>(p, b, s);
+    if (p.gate_kind == FE_GATE_FULL) return norm_ring_launch<R32, fe::kByElement>(p, b, s);
+    return norm_ring_launch<R32, fe::kByRow>(p, b, s);
+}
+
+template <bool R32, int GATE, bool RING, int C, int MAXT>
+cudaError_t norm_bwd_launch(const fe::NormBwdParams& q, const NormRingPlan& b, cudaStream_t s)
+{
+    static std::atomic<bool> ready[64];
+    const auto kernel = fe::block_norm_backward_kernel<R32, GATE, RING, C, MAXT>;
+    const cudaError_t e = norm_ring_ready(kernel, ready);
+    if (e != cudaSuccess) return e;
+    return launch(kernel, b.grid, b.threads, b.smem, s, q, b.tpr, b.stages);
+}
+
+// Through the ring when rows are whole aligned chunks; otherwise from registers, 8 columns per thread up to
+// 4096 columns of 512 threads, 8192 of 1024, and 16 beyond.
+template <bool R32, int GATE>
+cudaError_t norm_bwd_any(const fe::NormBwdParams& q, bool vec, uint32_t stage, int sms, int* partials, cudaStream_t s)
+{
+    const int H = q.f.H;
+    NormRingPlan b;
+    if (vec && norm_ring_plan(q.f.T, H, stage, sms, &b)) {
+        b.smem = std::max(b.smem, b.threads > b.tpr ? sizeof(float) * 3 * H : 0);
+        *partials = b.grid;
+        return norm_bwd_launch<R32, GATE, true, fe::kRingC, 512>(q, b, s);
+    }
+    b.tpr = norm_threads(H, H <= 8192 ? 1 : 2);
+    b.threads = std::max(512, b.tpr);
+    b.stages = 0;
+    const int groups = b.threads / b.tpr;
+    b.grid = (int)std::min<int64_t>(sms, (q.f.T + groups - 1) / groups);
+    b.smem = std::max((size_t)groups * fe::norm_group_extra(b.tpr, 0), groups > 1 ? sizeof(float) * 3 * H : 0);
+    *partials = b.grid;
+    if (H > 8192) return norm_bwd_launch<R32, GATE, false, 2, 1024>(q, b, s);
+    if (b.threads > 512) return norm_bwd_launch<R32, GATE, false, 1, 1024>(q, b, s);
+    return norm_bwd_launch<R32, GATE, false, 1, 512>(q, b, s);
+}
+
+template <bool R32>
+cudaError_t norm_bwd(const fe::NormBwdParams& q, bool vec, uint32_t stage, int sms, int* partials, cudaStream_t s)
+{
+    if (q.f.gate_kind == FE_GATE_CHANNEL) return norm_bwd_any<R32, fe::kByColumn>(q, vec, stage, sms, partials, s);
+    if (q.f.gate_kind == FE_GATE_FULL) return norm_bwd_any<R32, fe::kByElement>(q, vec, stage, sms, partials, s);
+    return norm_bwd_any<R32, fe::kByRow>(q, vec, stage, sms, partials, s);
 }
 
 // ---- balance loss -------------------------------------------------------------------------
@@ -605,6 +672,15 @@ fe_status fe_moe_block_norm(const void* r, int r_dtype, const void* y, const voi
     p.u = static_cast<uint16_t*>(u);
     const bool r32 = r_dtype == FE_DTYPE_F32;
     const cudaStream_t s = (cudaStream_t)stream;
+    NormRingPlan ring;
+    const int sms = sm_count();
+    if (sms < 1) return record_cuda(cudaErrorInvalidDevice, "device");
+    if (norm_vec(p) &&
+        norm_ring_plan(T, H, fe::norm_fwd_stage(H, r32, y != nullptr, p.gate_kind == FE_GATE_FULL), sms, &ring) &&
+        T >= (getenv("NR") ? atoi(getenv("NR")) : 4) * (int64_t)ring.grid * (512 / ring.tpr)) {
+        FE_CUDA_TRY(r32 ? norm_ring<true>(p, ring, s) : norm_ring<false>(p, ring, s));
+        return FE_OK;
+    }
     FE_CUDA_TRY(H <= 8192 ? norm_launch<1>(p, r32, norm_threads(H, 1), s) : norm_launch<2>(p, r32, norm_threads(H, 2), s));
     return FE_OK;
 }
@@ -666,17 +742,15 @@ fe_status fe_moe_block_norm_backward(const void* dr_out, const void* du, const v
     q.dy = static_cast<uint16_t*>(dy);
     q.dgate = kind == FE_GATE_CHANNEL ? nullptr : dgate;
     q.part = sums ? static_cast<float*>(workspace) : nullptr;
-    const NormBwdPlan b = norm_bwd_plan(T, H, sms);
-    q.rows_per_cta = b.rows_per_cta;
     const bool vec = norm_vec(q.f) && aligned(dr_out, 16) && aligned(du, 16) && aligned(dr, 16) && aligned(dy, 16) &&
                      (kind != FE_GATE_FULL || aligned(dgate, 16));
     const bool r32 = r_dtype == FE_DTYPE_F32;
-    if (b.chunk == 2) FE_CUDA_TRY((norm_bwd_launch<2, 1024>(q, vec, r32, b, s)));
-    else if (b.threads > 512) FE_CUDA_TRY((norm_bwd_launch<1, 1024>(q, vec, r32, b, s)));
-    else FE_CUDA_TRY((norm_bwd_launch<1, 512>(q, vec, r32, b, s)));
+    const uint32_t stage = fe::norm_bwd_stage(H, r32, y != nullptr, kind == FE_GATE_FULL, dr_out != nullptr, du != nullptr);
+    int partials = 0;
+    FE_CUDA_TRY(r32 ? norm_bwd<true>(q, vec, stage, sms, &partials, s) : norm_bwd<false>(q, vec, stage, sms, &partials, s));
     if (sums)
         FE_CUDA_TRY(launch(fe::column_sum_kernel, dim3((H + 31) / 32, 3), dim3(1024), 0, s,
-                           static_cast<const float*>(workspace), b.grid, H, 3, dw_post, dw_pre,
+                           static_cast<const float*>(workspace), partials, H, 3, dw_post, dw_pre,
                            kind == FE_GATE_CHANNEL ? static_cast<float*>(dgate) : static_cast<float*>(nullptr)));
     return FE_OK;
 }

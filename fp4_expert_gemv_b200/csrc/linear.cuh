@@ -25,9 +25,6 @@ namespace fe {
 
 enum { kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3, kActSwiglu = 4 };
 
-// Device-side problems of the entry points without a handle (kDevTcTimeout).
-__device__ uint32_t g_op_status;
-
 // Phi(z) and exp(-z^2 / 2).  The tail Q(|z|) = erfc(|z| / sqrt 2) / 2 by Abramowitz and Stegun, formula
 // 7.1.26 (a polynomial in t = 1 / (1 + p x) times exp(-x^2), |error of erf| <= 1.5e-7), which keeps the
 // small tail relatively exact: one exponential, shared with the density, and one division.  erff took
