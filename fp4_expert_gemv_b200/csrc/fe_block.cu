@@ -8,7 +8,6 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
-#include <cstdlib>
 #include <type_traits>
 
 #include "../../include/fe_moe.h"
@@ -195,63 +194,56 @@ cudaError_t norm_ring_ready(K kernel, std::atomic<bool>* ready)
     return cudaSuccess;
 }
 
-template <bool R32, int GATE>
+template <bool R32, int GATE, bool Y>
 cudaError_t norm_ring_launch(const fe::NormParams& p, const NormRingPlan& b, cudaStream_t s)
 {
     static std::atomic<bool> ready[64];
-    const cudaError_t e = norm_ring_ready(fe::block_norm_ring_kernel<R32, GATE>, ready);
+    const auto kernel = fe::block_norm_ring_kernel<R32, GATE, Y>;
+    const cudaError_t e = norm_ring_ready(kernel, ready);
     if (e != cudaSuccess) return e;
-    return launch(fe::block_norm_ring_kernel<R32, GATE>, b.grid, b.threads, b.smem, s, p, b.tpr, b.stages);
+    return launch(kernel, b.grid, b.threads, b.smem, s, p, b.tpr, b.stages);
 }
 
 template <bool R32>
 cudaError_t norm_ring(const fe::NormParams& p, const NormRingPlan& b, cudaStream_t s)
 {
-    if (p.gate_kind == FE_GATE_CHANNEL) return norm_ring_launch<R32, fe::kByColumn>(p, b, s);
-    if (p.gate_kind == FE_GATE_FULL) return norm_ring_launch<R32, fe::kByElement>(p, b, s);
-    return norm_ring_launch<R32, fe::kByRow>(p, b, s);
+    if (!p.y) return norm_ring_launch<R32, fe::kByRow, false>(p, b, s);
+    if (p.gate_kind == FE_GATE_CHANNEL) return norm_ring_launch<R32, fe::kByColumn, true>(p, b, s);
+    if (p.gate_kind == FE_GATE_FULL) return norm_ring_launch<R32, fe::kByElement, true>(p, b, s);
+    return norm_ring_launch<R32, fe::kByRow, true>(p, b, s);
 }
 
-template <bool R32, int GATE, bool RING, int C, int MAXT>
-cudaError_t norm_bwd_launch(const fe::NormBwdParams& q, const NormRingPlan& b, cudaStream_t s)
-{
-    static std::atomic<bool> ready[64];
-    const auto kernel = fe::block_norm_backward_kernel<R32, GATE, RING, C, MAXT>;
-    const cudaError_t e = norm_ring_ready(kernel, ready);
-    if (e != cudaSuccess) return e;
-    return launch(kernel, b.grid, b.threads, b.smem, s, q, b.tpr, b.stages);
-}
-
-// Through the ring when rows are whole aligned chunks; otherwise from registers, 8 columns per thread up to
-// 4096 columns of 512 threads, 8192 of 1024, and 16 beyond.
+// Through the ring when rows are whole aligned chunks and every operand is there, else column by column.
 template <bool R32, int GATE>
-cudaError_t norm_bwd_any(const fe::NormBwdParams& q, bool vec, uint32_t stage, int sms, int* partials, cudaStream_t s)
+cudaError_t norm_bwd_any(const fe::NormBwdParams& q, bool vec, int sms, int* partials, cudaStream_t s)
 {
+    static std::atomic<bool> ring_ready[64], any_ready[64];
     const int H = q.f.H;
     NormRingPlan b;
-    if (vec && norm_ring_plan(q.f.T, H, stage, sms, &b)) {
-        b.smem = std::max(b.smem, b.threads > b.tpr ? sizeof(float) * 3 * H : 0);
+    if (vec && q.f.y && q.du && q.dr_out &&
+        norm_ring_plan(q.f.T, H, fe::norm_bwd_stage(H, R32, GATE == fe::kByElement), sms, &b)) {
+        b.smem = std::max(b.smem, sizeof(float) * 3 * H * (b.threads / b.tpr));   // the groups' column sums at the end
         *partials = b.grid;
-        return norm_bwd_launch<R32, GATE, true, fe::kRingC, 512>(q, b, s);
+        const auto kernel = fe::block_norm_backward_ring_kernel<R32, GATE>;
+        const cudaError_t e = norm_ring_ready(kernel, ring_ready);
+        if (e != cudaSuccess) return e;
+        return launch(kernel, b.grid, b.threads, b.smem, s, q, b.tpr, b.stages);
     }
-    b.tpr = norm_threads(H, H <= 8192 ? 1 : 2);
-    b.threads = std::max(512, b.tpr);
-    b.stages = 0;
-    const int groups = b.threads / b.tpr;
-    b.grid = (int)std::min<int64_t>(sms, (q.f.T + groups - 1) / groups);
-    b.smem = std::max((size_t)groups * fe::norm_group_extra(b.tpr, 0), groups > 1 ? sizeof(float) * 3 * H : 0);
-    *partials = b.grid;
-    if (H > 8192) return norm_bwd_launch<R32, GATE, false, 2, 1024>(q, b, s);
-    if (b.threads > 512) return norm_bwd_launch<R32, GATE, false, 1, 1024>(q, b, s);
-    return norm_bwd_launch<R32, GATE, false, 1, 512>(q, b, s);
+    const int tpr = std::min(512, norm_threads(H, 1)), groups = 512 / tpr;
+    const size_t smem = sizeof(float) * groups * (2 * (size_t)fe::norm_red_floats(tpr) + 2 * (size_t)H);
+    *partials = (int)std::min<int64_t>(2 * sms, (q.f.T + groups - 1) / groups);
+    const auto kernel = fe::block_norm_backward_any_kernel<R32, GATE>;
+    const cudaError_t e = norm_ring_ready(kernel, any_ready);
+    if (e != cudaSuccess) return e;
+    return launch(kernel, *partials, 512, smem, s, q, tpr);
 }
 
 template <bool R32>
-cudaError_t norm_bwd(const fe::NormBwdParams& q, bool vec, uint32_t stage, int sms, int* partials, cudaStream_t s)
+cudaError_t norm_bwd(const fe::NormBwdParams& q, bool vec, int sms, int* partials, cudaStream_t s)
 {
-    if (q.f.gate_kind == FE_GATE_CHANNEL) return norm_bwd_any<R32, fe::kByColumn>(q, vec, stage, sms, partials, s);
-    if (q.f.gate_kind == FE_GATE_FULL) return norm_bwd_any<R32, fe::kByElement>(q, vec, stage, sms, partials, s);
-    return norm_bwd_any<R32, fe::kByRow>(q, vec, stage, sms, partials, s);
+    if (q.f.gate_kind == FE_GATE_CHANNEL) return norm_bwd_any<R32, fe::kByColumn>(q, vec, sms, partials, s);
+    if (q.f.gate_kind == FE_GATE_FULL) return norm_bwd_any<R32, fe::kByElement>(q, vec, sms, partials, s);
+    return norm_bwd_any<R32, fe::kByRow>(q, vec, sms, partials, s);
 }
 
 // ---- balance loss -------------------------------------------------------------------------
@@ -672,12 +664,15 @@ fe_status fe_moe_block_norm(const void* r, int r_dtype, const void* y, const voi
     p.u = static_cast<uint16_t*>(u);
     const bool r32 = r_dtype == FE_DTYPE_F32;
     const cudaStream_t s = (cudaStream_t)stream;
+    // The streamed kernel pays from a few rows per group: at H = 2048 (four groups on each of 148 SMs) bf16 rows
+    // take 3.5 us with it and 3.4 without at T = 512, 8.7 and 10.3 at 2048, 24.6 and 38.5 at 8192; fp32
+    // rows 14.0 and 12.0 at 2048, 20.8 and 20.9 at 4096, 35.0 and 38.2 at 8192.
     NormRingPlan ring;
     const int sms = sm_count();
     if (sms < 1) return record_cuda(cudaErrorInvalidDevice, "device");
     if (norm_vec(p) &&
         norm_ring_plan(T, H, fe::norm_fwd_stage(H, r32, y != nullptr, p.gate_kind == FE_GATE_FULL), sms, &ring) &&
-        T >= (getenv("NR") ? atoi(getenv("NR")) : 4) * (int64_t)ring.grid * (512 / ring.tpr)) {
+        T >= (int64_t)(r32 ? 6 : 2) * sms * (512 / ring.tpr)) {
         FE_CUDA_TRY(r32 ? norm_ring<true>(p, ring, s) : norm_ring<false>(p, ring, s));
         return FE_OK;
     }
@@ -745,9 +740,8 @@ fe_status fe_moe_block_norm_backward(const void* dr_out, const void* du, const v
     const bool vec = norm_vec(q.f) && aligned(dr_out, 16) && aligned(du, 16) && aligned(dr, 16) && aligned(dy, 16) &&
                      (kind != FE_GATE_FULL || aligned(dgate, 16));
     const bool r32 = r_dtype == FE_DTYPE_F32;
-    const uint32_t stage = fe::norm_bwd_stage(H, r32, y != nullptr, kind == FE_GATE_FULL, dr_out != nullptr, du != nullptr);
     int partials = 0;
-    FE_CUDA_TRY(r32 ? norm_bwd<true>(q, vec, stage, sms, &partials, s) : norm_bwd<false>(q, vec, stage, sms, &partials, s));
+    FE_CUDA_TRY(r32 ? norm_bwd<true>(q, vec, sms, &partials, s) : norm_bwd<false>(q, vec, sms, &partials, s));
     if (sums)
         FE_CUDA_TRY(launch(fe::column_sum_kernel, dim3((H + 31) / 32, 3), dim3(1024), 0, s,
                            static_cast<const float*>(workspace), partials, H, 3, dw_post, dw_pre,

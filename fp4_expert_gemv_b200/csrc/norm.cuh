@@ -238,13 +238,20 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(NormParams p, int tpr)
 // ---- many rows: the rows stream through shared memory ------------------------------------------
 // With one row per group at a time a group loads, waits, reduces, waits and stores, and most of its time
 // nothing is on its way from memory.  Here every group of tpr threads walks its rows with the next
-// ones already being copied (cp.async.bulk, one thread) into its own ring of stages, synchronises alone (a
-// named barrier per group) and keeps what belongs to its columns in registers: weights, channel gate,
-// the sums over rows.  A thread has 16 columns: the sums' shuffles and barriers are paid per thread
-// and row, and with 8 columns they were half of all instructions.  What varies per element is a
-// template parameter or a neutral factor, never a branch: the instruction count bounds these kernels
-// next to memory (the first backward pass spent 114 instructions per element and 82 us at T = 4096,
-// H = 2048, where memory needs 16).
+// ones already being copied (cp.async.bulk) into its own ring of stages, synchronises alone (a named
+// barrier per group) and keeps what belongs to its columns in registers: weights, channel gate, the
+// sums over rows.
+// One exchange per row: with q = scale w_post a(g) y the second norm's sum is
+//   sum r'^2 = sum r^2 + 2 rho_y sum r q + rho_y^2 sum q^2,
+// and the backward pass's other sums follow from seven products of the operands as they lie in memory
+// (block_norm_backward_kernel), so the sums of all of them travel together and a second walk over
+// the stage writes every output.  Where r' is small next to what cancels in it (sum r'^2 below an
+// eighth of its positive parts, or not finite), the group takes the sums of the rounded r' itself,
+// which costs that row two more exchanges.  With an exchange per norm and one for dm, the group's
+// warps spent 10,000 cycles a row in latencies: 44 us for T = 4096, H = 2048 backward, where memory
+// needs 16.
+// A thread has 16 columns: the exchange is paid per thread and row, and with 8 columns it was half of all
+// instructions.  What varies per element is a template parameter or a neutral factor, never a branch.
 
 FE_DEV void group_bar(int group, int tpr)
 {
@@ -252,7 +259,7 @@ FE_DEV void group_bar(int group, int tpr)
     else asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
 }
 
-constexpr int kRedSums = 2;   // sums per exchange, at most
+constexpr int kRedSums = 7;   // sums per exchange, at most
 
 __host__ __device__ constexpr int norm_red_floats(int tpr) { return kRedSums * (tpr / 32 < 4 ? 4 : tpr / 32); }
 
@@ -296,13 +303,36 @@ FE_DEV void unpack8(const uint4& q, float (&v)[8])
     }
 }
 
-FE_DEV void ring_get(const uint16_t* row, int chunk, float (&v)[8]) { unpack8(reinterpret_cast<const uint4*>(row)[chunk], v); }
-
-FE_DEV void ring_get(const float* row, int chunk, float (&v)[8])
+// Chunk `ch` of 8 of the row of bf16 (fp32) at shared address `row`.
+template <bool F32>
+FE_DEV void ring_get(uint32_t row, int ch, float (&v)[8])
 {
-    const float4 a = reinterpret_cast<const float4*>(row)[2 * chunk], b = reinterpret_cast<const float4*>(row)[2 * chunk + 1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    if constexpr (F32) {
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                     : "r"(row + 32 * ch));
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                     : "r"(row + 32 * ch + 16));
+    } else {
+        uint4 q;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+                     : "r"(row + 16 * ch));
+        unpack8(q, v);
+    }
+}
+
+FE_DEV void put8(uint16_t* p, const float (&v)[8])
+{
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]), bf16x2_rn(v[4], v[5]), bf16x2_rn(v[6], v[7]));
+}
+
+FE_DEV void put8(float* p, const float (&v)[8])
+{
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
 
 constexpr unsigned long long kNormTimeoutNs = 2000ull * 1000 * 1000;
@@ -318,18 +348,96 @@ __host__ __device__ inline uint32_t norm_fwd_stage(int H, bool r32, bool y, bool
 {
     return (uint32_t)H * ((r32 ? 4 : 2) + (y ? 2 : 0) + (full ? 2 : 0));
 }
-__host__ __device__ inline uint32_t norm_bwd_stage(int H, bool r32, bool y, bool full, bool dr, bool du)
+__host__ __device__ inline uint32_t norm_bwd_stage(int H, bool r32, bool full)
 {
-    return (uint32_t)H * ((r32 ? 4 : 2) * (dr ? 2 : 1) + (y ? 2 : 0) + (full ? 2 : 0) + (du ? 2 : 0));
+    return (uint32_t)H * ((r32 ? 8 : 4) + 4 + (full ? 2 : 0));
 }
 
 // A thread's 16 columns: chunks t and t + tpr of 8.
 constexpr int kRingC = 2;
 
+// Two fp32 operations per instruction.
+FE_DEV void fma2(float (&d)[8], int j, float a0, float a1, float b0, float b1, float c0, float c1)
+{
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d[j]), "=f"(d[j + 1])
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
+
+FE_DEV void mul2(float (&d)[8], int j, float a0, float a1, float b0, float b1)
+{
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d[j]), "=f"(d[j + 1])
+        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
+// Over 8 columns: d = a b + c, d = a b, and the same with one factor for all.
+FE_DEV void vfma(float (&d)[8], const float (&a)[8], const float (&b)[8], const float (&c)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) fma2(d, j, a[j], a[j + 1], b[j], b[j + 1], c[j], c[j + 1]);
+}
+FE_DEV void vfma(float (&d)[8], float a, const float (&b)[8], const float (&c)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) fma2(d, j, a, a, b[j], b[j + 1], c[j], c[j + 1]);
+}
+FE_DEV void vmul(float (&d)[8], const float (&a)[8], const float (&b)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) mul2(d, j, a[j], a[j + 1], b[j], b[j + 1]);
+}
+FE_DEV void vmul(float (&d)[8], float a, const float (&b)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) mul2(d, j, a, a, b[j], b[j + 1]);
+}
+
+// s += sum of a[j] b[j], in two chains that the caller adds at the end.
+FE_DEV void vdot(float (&s)[2], const float (&a)[8], const float (&b)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; j += 2)
+        asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%0, %1};\n\t"
+            "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+            : "+f"(s[0]), "+f"(s[1])
+            : "f"(a[j]), "f"(a[j + 1]), "f"(b[j]), "f"(b[j + 1]));
+}
+
 // How the gate enters a row: one factor, a factor per column, or one per element.
 enum { kByRow = 0, kByColumn = 1, kByElement = 2 };
 
-template <bool R32, int GATE>
+// Whether the expanded sum of squares lost too much, given its positive parts (also if it is not finite).
+FE_DEV bool sum_cancelled(float sum, float parts) { return !(sum >= 0.125f * parts) || isinf(sum); }
+
+// Copies of a row's operands: lane k of the group's first warp holds operand k.
+struct RowCopies {
+    const char* src;
+    uint32_t off, bytes;
+    int n;
+
+    FE_DEV RowCopies() : src(nullptr), off(0), bytes(0), n(0) {}
+    FE_DEV void add(int t, const void* p, uint32_t at, uint32_t nb)
+    {
+        if (t == n) {
+            src = static_cast<const char*>(p);
+            off = at;
+            bytes = nb;
+        }
+        ++n;
+    }
+    // Row `row` into the stage at dst; by the group's first warp, converged.
+    FE_DEV void fill(int t, int64_t row, int64_t rows, uint32_t dst, uint32_t stage, uint32_t bar) const
+    {
+        if (t >= 32 || row >= rows) return;
+        if (t == 0) mbar_expect_tx(bar, stage);
+        __syncwarp();
+        if (t < n) bulk_g2s(dst + off, src + (size_t)row * bytes, bytes, bar);
+    }
+};
+
+template <bool R32, int GATE, bool Y>
 __global__ void __launch_bounds__(512) block_norm_ring_kernel(NormParams p, int tpr, int stages)
 {
     using RT = typename std::conditional<R32, float, uint16_t>::type;
@@ -337,8 +445,9 @@ __global__ void __launch_bounds__(512) block_norm_ring_kernel(NormParams p, int 
     extern __shared__ __align__(128) uint8_t norm_dyn[];
     const int t = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = blockDim.x / tpr;
     const int H = p.H;
-    const bool has_y = p.y != nullptr, token = p.gate_kind == kGateToken, has_u = p.u != nullptr, has_r = p.r_out != nullptr;
-    const uint32_t stage = norm_fwd_stage(H, R32, has_y, GATE == kByElement);
+    const bool token = p.gate_kind == kGateToken, has_u = p.u != nullptr, has_r = p.r_out != nullptr;
+    const uint32_t stage = norm_fwd_stage(H, R32, Y, GATE == kByElement);
+    const uint32_t oy = H * sizeof(RT), og = oy + 2 * H;
     uint8_t* base = norm_dyn + (size_t)group * (stages * stage + norm_group_extra(tpr, stages));
     float* red = reinterpret_cast<float*>(base + stages * stage);
     const uint32_t bar = smem_addr(red + 2 * norm_red_floats(tpr));
@@ -350,16 +459,12 @@ __global__ void __launch_bounds__(512) block_norm_ring_kernel(NormParams p, int 
     griddep_wait();
     griddep_launch();
     const int64_t step = (int64_t)gridDim.x * groups, first = (int64_t)blockIdx.x * groups + group;
-    auto fill = [&](int64_t row, int s) {
-        if (t != 0 || row >= p.T) return;
-        const uint32_t dst = smem_addr(base + s * stage), b = bar + 8 * s;
-        mbar_expect_tx(b, stage);
-        const size_t at = (size_t)row * H;
-        bulk_g2s(dst, static_cast<const RT*>(p.r) + at, H * sizeof(RT), b);
-        if (has_y) bulk_g2s(dst + H * sizeof(RT), p.y + at, 2 * H, b);
-        if (GATE == kByElement) bulk_g2s(dst + H * sizeof(RT) + 2 * H, p.gate + at, 2 * H, b);
-    };
-    for (int s = 0; s < stages; ++s) fill(first + s * step, s);
+    RowCopies rc;
+    rc.add(t, p.r, 0, H * sizeof(RT));
+    if (Y) rc.add(t, p.y, oy, 2 * H);
+    if (GATE == kByElement) rc.add(t, p.gate, og, 2 * H);
+    const uint32_t base_a = smem_addr(base);
+    for (int s = 0; s < stages; ++s) rc.fill(t, first + s * step, p.T, base_a + s * stage, stage, bar + 8 * s);
     // cw: scale * w_post (* the column's gate); neutral factors for what is not there
     float cw[C][8];
     uint4 qpre[C];
@@ -381,75 +486,89 @@ __global__ void __launch_bounds__(512) block_norm_ring_kernel(NormParams p, int 
     int s = 0, half = 0;
     uint32_t parity = 0;
     bool dead = false;
-    float gate1 = token && first < p.T ? bf16_bits_to_f32(p.gate[first]) : 1.0f;
+    uint16_t graw = token && first < p.T ? p.gate[first] : 0;   // the coming row's gate
     const float inv_h = 1.0f / (float)H;
     for (int64_t row = first; row < p.T; row += step) {
         if (!dead && !mbar_wait(bar + 8 * s, parity, kNormTimeoutNs)) dead = true;
-        const uint8_t* src = base + s * stage;
-        float r[C][8], y[C][8];
+        const uint32_t src = base_a + s * stage;
         float k = 1.0f;
         if (token) {
-            k = p.gate_sigmoid ? sigmoidf(gate1) : gate1;
-            gate1 = row + step < p.T ? bf16_bits_to_f32(p.gate[row + step]) : 0.0f;   // the next row's
+            k = bf16_bits_to_f32(graw);
+            if (p.gate_sigmoid) k = sigmoidf(k);
+            if (row + step < p.T) graw = p.gate[row + step];
         }
-        const size_t at = (size_t)row * H;
-        if (has_y) {
-            float sum[1] = {0.0f};
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const int ch = t + c * tpr;
-                if (ch * 8 < H) ring_get(reinterpret_cast<const uint16_t*>(src + H * sizeof(RT)), ch, y[c]);
-                else
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) y[c][j] = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) sum[0] = fmaf(y[c][j], y[c][j], sum[0]);
-            }
-            if (p.w_post) {
-                ring_sum<1>(sum, group, tpr, red + half * norm_red_floats(tpr));
-                half ^= 1;
-                k *= rsqrtf(sum[0] * inv_h + p.eps);
-            }
-        }
-        float sq[1] = {0.0f};
+        // the row's chunks of r, and q = cw a y
+        float r[C][8], q[C][8], syy[2] = {0, 0}, srr[2] = {0, 0}, srq[2] = {0, 0}, sqq[2] = {0, 0};
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int ch = t + c * tpr;
-            const bool mine = ch * 8 < H;
-            if (mine) ring_get(reinterpret_cast<const RT*>(src), ch, r[c]);
-            else
+            if (ch * 8 < H) {
+                ring_get<R32>(src, ch, r[c]);
+                vdot(srr, r[c], r[c]);
+                if (Y) {
+                    ring_get<false>(src + oy, ch, q[c]);
+                    vdot(syy, q[c], q[c]);
+                    vmul(q[c], q[c], cw[c]);
+                    if (GATE == kByElement) {
+                        float a[8];
+                        ring_get<false>(src + og, ch, a);
+                        if (p.gate_sigmoid) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) r[c][j] = 0.0f;
-            if (has_y) {
-                if (GATE == kByElement) {
-                    float a[8];
-                    unpack8(mine ? reinterpret_cast<const uint4*>(src + H * sizeof(RT) + 2 * H)[ch] : make_uint4(0, 0, 0, 0), a);
-                    if (p.gate_sigmoid) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) a[j] = sigmoidf(a[j]);
+                            for (int j = 0; j < 8; ++j) a[j] = sigmoidf(a[j]);
+                        }
+                        vmul(q[c], q[c], a);
                     }
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) y[c][j] *= a[j];
+                    vdot(srq, r[c], q[c]);
+                    vdot(sqq, q[c], q[c]);
                 }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) r[c][j] = fmaf(cw[c][j] * k, y[c][j], r[c][j]);
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sq[0] = fmaf(r[c][j], r[c][j], sq[0]);
-            if (has_r && mine && !dead) norm_store<8>(static_cast<RT*>(p.r_out) + at, c, t, tpr, H, r[c]);
         }
-        ring_sum<1>(sq, group, tpr, red + half * norm_red_floats(tpr));   // also: everyone has read the stage
-        half ^= 1;
-        fill(row + stages * step, s);
-        if (has_u) {
-            const float rho = rsqrtf(sq[0] * inv_h + p.eps);
+        float ss;
+        if (Y) {
+            float sum[4] = {srr[0] + srr[1], syy[0] + syy[1], srq[0] + srq[1], sqq[0] + sqq[1]};
+            ring_sum<4>(sum, group, tpr, red + half * norm_red_floats(tpr));   // also: everyone has read the stage
+            half ^= 1;
+            if (p.w_post) k *= rsqrtf(sum[1] * inv_h + p.eps);
+            const float parts = sum[0] + k * k * sum[3];
+            ss = parts + 2.0f * k * sum[2];
+            rc.fill(t, row + stages * step, p.T, src, stage, bar + 8 * s);
+            if (has_u && sum_cancelled(ss, parts)) {   // the same for the whole group
+                float d[2] = {0, 0}, v[8];
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                float w[8];
-                unpack8(qpre[c], w);
+                for (int c = 0; c < C; ++c)
+                    if ((t + c * tpr) * 8 < H) {
+                        vfma(v, k, q[c], r[c]);
+                        vdot(d, v, v);
+                    }
+                float one[1] = {d[0] + d[1]};
+                ring_sum<1>(one, group, tpr, red + half * norm_red_floats(tpr));
+                half ^= 1;
+                ss = one[0];
+            }
+        } else {
+            float one[1] = {srr[0] + srr[1]};
+            ring_sum<1>(one, group, tpr, red + half * norm_red_floats(tpr));
+            half ^= 1;
+            rc.fill(t, row + stages * step, p.T, src, stage, bar + 8 * s);
+            ss = one[0];
+        }
+        const float rho = has_u ? rsqrtf(ss * inv_h + p.eps) : 0.0f;
+        const size_t at = (size_t)row * H;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] *= r[c][j] * rho;
-                if ((t + c * tpr) * 8 < H && !dead) norm_store<8>(p.u + at, c, t, tpr, H, w);
+        for (int c = 0; c < C; ++c) {
+            const int ch = t + c * tpr;
+            if (ch * 8 < H && !dead) {
+                if (Y) {
+                    vfma(r[c], k, q[c], r[c]);   // r'
+                    if (has_r) put8(static_cast<RT*>(p.r_out) + at + 8 * ch, r[c]);
+                }
+                if (has_u) {
+                    float w[8];
+                    unpack8(qpre[c], w);
+                    vmul(w, rho, w);
+                    vmul(w, w, r[c]);
+                    put8(p.u + at + 8 * ch, w);
+                }
             }
         }
         if (++s == stages) {
@@ -460,69 +579,67 @@ __global__ void __launch_bounds__(512) block_norm_ring_kernel(NormParams p, int 
     if (dead) atomicOr(&g_op_status, kDevLoadTimeout);
 }
 
-// The gradients.  With n = r' rho and dn = du w_pre:
-//   D  = dr' + rho (dn - n mean(dn n))            gradient at r', and at r
+// The gradients.  With n = r' rho and x = du w_pre:
+//   D  = dr' + rho (x - n mean(x n))              gradient at r', and at r
 //   dv = s a D,  dg = s v D a'(g),  dm = dv w_post
 //   dy = rho_y (dm - m mean(dm m))                (dy = dv without w_post)
 //   dw_pre = sum_t du n,  dw_post = sum_t dv m,  dg summed over what the gate was broadcast to
 // r' is rebuilt in fp32 from r and y, which the gradients need anyway, so the forward pass saves
-// nothing.  With e = D m, dw_post and a channel gate's gradient are column factors times the same sum
-// of e over rows.  The sums over rows stay in the registers of the thread that owns the column; one
-// partial per CTA, added in a fixed order by column_sum_kernel.
-// RING: rows of whole 16-byte chunks, through the ring, two chunks of 8 columns per thread (C = 2), or 1
-// where a row needs no more; otherwise any width and alignment, the row's operands in registers, one
-// chunk of columns t, t + tpr, ... per thread (C = 2 beyond 8192 columns).
-template <bool R32, int GATE, bool RING, int C, int MAXT>
-__global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(NormBwdParams q, int tpr, int stages)
+// nothing.  Every row sum follows from y y, r r, r q, q q, x r, x q and dr' q (q = s a w_post y): with
+// k = rho mean(x n),
+//   sum x r' = sum x r + rho_y sum x q,
+//   sum dm m = rho_y (sum dr' q + rho sum x q - k rho (sum r q + rho_y sum q q)).
+// With e = D m, dw_post and a channel gate's gradient are column factors times the same sum of e over
+// rows.  The sums over rows stay in the registers of the thread that owns the column; one partial per
+// CTA, added in a fixed order by column_sum_kernel.
+// RING: rows of whole aligned 16-byte chunks and every operand there, through the ring; otherwise any width,
+// alignment and set of operands, straight from memory (the second walk finds them in L1), columns strided by the group's threads.
+template <bool R32, int GATE>
+__global__ void __launch_bounds__(512) block_norm_backward_ring_kernel(NormBwdParams q, int tpr, int stages)
 {
     using RT = typename std::conditional<R32, float, uint16_t>::type;
-    constexpr int VEC = RING ? 8 : 1;
+    constexpr int C = kRingC;
     extern __shared__ __align__(128) uint8_t norm_dyn[];
     const NormParams& p = q.f;
     const int t = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = blockDim.x / tpr;
     const int H = p.H;
-    const bool has_y = p.y != nullptr, has_du = q.du != nullptr, has_dr = q.dr_out != nullptr;
     const bool token = p.gate_kind == kGateToken, w_post = p.w_post != nullptr;
-    const uint32_t stage = RING ? norm_bwd_stage(H, R32, has_y, GATE == kByElement, has_dr, has_du) : 0;
-    const uint32_t oy = H * sizeof(RT), odr = oy + (has_y ? 2 * H : 0), odu = odr + (has_dr ? H * sizeof(RT) : 0),
-                   og = odu + (has_du ? 2 * H : 0);
+    const uint32_t stage = norm_bwd_stage(H, R32, GATE == kByElement);
+    const uint32_t oy = H * sizeof(RT), odr = oy + 2 * H, odu = odr + H * sizeof(RT), og = odu + 2 * H;
     uint8_t* base = norm_dyn + (size_t)group * (stages * stage + norm_group_extra(tpr, stages));
     float* red = reinterpret_cast<float*>(base + stages * stage);
     const uint32_t bar = smem_addr(red + 2 * norm_red_floats(tpr));
     for (int i = t; i < 2 * norm_red_floats(tpr); i += tpr) red[i] = 0.0f;
-    if (RING && t == 0)
+    if (t == 0)
         for (int s = 0; s < stages; ++s) mbar_init(bar + 8 * s, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncthreads();
     griddep_wait();
     griddep_launch();
     const int64_t step = (int64_t)gridDim.x * groups, first = (int64_t)blockIdx.x * groups + group;
-    auto fill = [&](int64_t row, int s) {
-        if (t != 0 || row >= p.T) return;
-        const uint32_t dst = smem_addr(base + s * stage), b = bar + 8 * s;
-        mbar_expect_tx(b, stage);
-        const size_t at = (size_t)row * H;
-        bulk_g2s(dst, static_cast<const RT*>(p.r) + at, H * sizeof(RT), b);
-        if (has_y) bulk_g2s(dst + oy, p.y + at, 2 * H, b);
-        if (has_dr) bulk_g2s(dst + odr, static_cast<const RT*>(q.dr_out) + at, H * sizeof(RT), b);
-        if (has_du) bulk_g2s(dst + odu, q.du + at, 2 * H, b);
-        if (GATE == kByElement) bulk_g2s(dst + og, p.gate + at, 2 * H, b);
-    };
-    if (RING)
-        for (int s = 0; s < stages; ++s) fill(first + s * step, s);
+    RowCopies rc;
+    rc.add(t, p.r, 0, H * sizeof(RT));
+    rc.add(t, p.y, oy, 2 * H);
+    rc.add(t, q.dr_out, odr, H * sizeof(RT));
+    rc.add(t, q.du, odu, 2 * H);
+    if (GATE == kByElement) rc.add(t, p.gate, og, 2 * H);
+    const uint32_t base_a = smem_addr(base);
+    for (int s = 0; s < stages; ++s) rc.fill(t, first + s * step, p.T, base_a + s * stage, stage, bar + 8 * s);
     // cw: scale * w_post (* the column's gate), wq: w_pre; the sums over rows
-    float cw[C][8], wq[C][8], E[C][8], gw_pre[C][8];
+    float cw[C][8], E[C][8], gw_pre[C][8];
+    uint4 wq[C];   // in bf16: 16 registers less than two chunks of fp32
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         float g[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             cw[c][j] = 1.0f;
-            wq[c][j] = E[c][j] = gw_pre[c][j] = 0.0f;
+            E[c][j] = gw_pre[c][j] = g[j] = 0.0f;
         }
-        if (w_post) norm_load<VEC>(p.w_post, c, t, tpr, H, true, cw[c]);
-        if (has_du) norm_load<VEC>(p.w_pre, c, t, tpr, H, true, wq[c]);
-        if (GATE == kByColumn) norm_load<VEC>(p.gate, c, t, tpr, H, true, g);
+        if (w_post) norm_load<8>(p.w_post, c, t, tpr, H, true, cw[c]);
+        norm_load<8>(p.w_pre, c, t, tpr, H, true, g);
+        wq[c] = make_uint4(bf16x2_rn(g[0], g[1]), bf16x2_rn(g[2], g[3]), bf16x2_rn(g[4], g[5]), bf16x2_rn(g[6], g[7]));
+        if (GATE == kByColumn) norm_load<8>(p.gate, c, t, tpr, H, true, g);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             cw[c][j] *= p.scale;
@@ -532,159 +649,189 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(NormBwdParams
     int s = 0, half = 0;
     uint32_t parity = 0;
     bool dead = false;
-    float gate1 = token && first < p.T ? bf16_bits_to_f32(p.gate[first]) : 1.0f;
+    uint16_t graw = token && first < p.T ? p.gate[first] : 0;   // the coming row's gate
     const float inv_h = 1.0f / (float)H;
     for (int64_t row = first; row < p.T; row += step) {
-        if (RING && !dead && !mbar_wait(bar + 8 * s, parity, kNormTimeoutNs)) dead = true;
-        const uint8_t* src = base + s * stage;
+        if (!dead && !mbar_wait(bar + 8 * s, parity, kNormTimeoutNs)) dead = true;
+        const uint32_t src = base_a + s * stage;
         const size_t at = (size_t)row * H;
-        // chunk c of an operand, from the stage or from memory
-        auto get = [&](const auto* global, uint32_t off, int c, float (&v)[8]) {
-            if constexpr (RING) {
-                using OT = typename std::remove_const<typename std::remove_pointer<decltype(global)>::type>::type;
-                if ((t + c * tpr) * 8 < H) ring_get(reinterpret_cast<const OT*>(src + off), t + c * tpr, v);
-                else
+        // chunk c of an operand of the row, for chunks inside it
+        auto inside = [&](int c) { return (t + c * tpr) * 8 < H; };
+        auto get_r = [&](int c, float (&v)[8]) { ring_get<R32>(src, t + c * tpr, v); };
+        auto get_y = [&](int c, float (&v)[8]) { ring_get<false>(src + oy, t + c * tpr, v); };
+        auto get_dr = [&](int c, float (&v)[8]) { ring_get<R32>(src + odr, t + c * tpr, v); };
+        auto get_du = [&](int c, float (&v)[8]) { ring_get<false>(src + odu, t + c * tpr, v); };
+        auto get_a = [&](int c, float (&v)[8]) {
+            ring_get<false>(src + og, t + c * tpr, v);
+            if (p.gate_sigmoid) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-            } else {
-                norm_load<1>(global + at, c, t, tpr, H, true, v);
+                for (int j = 0; j < 8; ++j) v[j] = sigmoidf(v[j]);
             }
         };
-        const RT* gr = static_cast<const RT*>(p.r);
-        const RT* gdr = static_cast<const RT*>(q.dr_out);
-        float r[C][8], y[C][8], dn[C][8], D[C][8], a[C][8];
-        if (!RING) {   // everything on its way at once
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                if (has_y) get(p.y, oy, c, y[c]);
-                get(gr, 0, c, r[c]);
-                if (has_du) get(q.du, odu, c, dn[c]);
-                if (has_dr) get(gdr, odr, c, D[c]);
-                if (GATE == kByElement) get(p.gate, og, c, a[c]);
-            }
-        }
+        auto put = [&](auto* global, int c, const float (&v)[8]) { put8(global + at + 8 * (t + c * tpr), v); };
         float g1 = 1.0f, d1 = 1.0f;
         if (token) {
-            g1 = gate1;
-            gate1 = row + step < p.T ? bf16_bits_to_f32(p.gate[row + step]) : 0.0f;   // the next row's
+            g1 = bf16_bits_to_f32(graw);
+            if (row + step < p.T) graw = p.gate[row + step];
             if (p.gate_sigmoid) {
                 g1 = sigmoidf(g1);
                 d1 = g1 * (1.0f - g1);
             }
         }
-        float rho_y = 1.0f;
-        if (has_y) {
-            float sum[1] = {0.0f};
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                if (RING) get(p.y, oy, c, y[c]);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) sum[0] = fmaf(y[c][j], y[c][j], sum[0]);
-                if (GATE == kByElement) {
-                    if (RING) get(p.gate, og, c, a[c]);
-                    if (p.gate_sigmoid) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) a[c][j] = sigmoidf(a[c][j]);
-                    }
-                }
-            }
-            if (w_post) {
-                ring_sum<1>(sum, group, tpr, red + half * norm_red_floats(tpr));
-                half ^= 1;
-                rho_y = rsqrtf(sum[0] * inv_h + p.eps);
-            }
-#pragma unroll
-            for (int c = 0; c < C; ++c)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) y[c][j] *= rho_y;   // m
-        }
-        float rho = 0.0f, rk = 0.0f;
-        if (has_du) {
-            float sum[2] = {0.0f, 0.0f};
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                if (RING) {
-                    get(gr, 0, c, r[c]);
-                    get(q.du, odu, c, dn[c]);
-                }
-                if (has_y) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float f = GATE == kByElement ? cw[c][j] * a[c][j] : GATE == kByRow ? cw[c][j] * g1 : cw[c][j];
-                        r[c][j] = fmaf(f, y[c][j], r[c][j]);   // r'
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    sum[0] = fmaf(r[c][j], r[c][j], sum[0]);
-                    sum[1] = fmaf(dn[c][j] * wq[c][j], r[c][j], sum[1]);
-                }
-            }
-            ring_sum<2>(sum, group, tpr, red + half * norm_red_floats(tpr));
-            half ^= 1;
-            rho = rsqrtf(sum[0] * inv_h + p.eps);
-            rk = sum[1] * inv_h * rho * rho * rho;   // rho mean(dn n) rho
-        }
-        float sum[2] = {0.0f, 0.0f};
+        // ---- first walk: the seven sums (a row gate stays out of q: it is a factor of the row) -----------
+        float syy[2] = {0, 0}, srr[2] = {0, 0}, srq[2] = {0, 0}, sqq[2] = {0, 0}, sxr[2] = {0, 0}, sxq[2] = {0, 0},
+              sdq[2] = {0, 0};
 #pragma unroll
         for (int c = 0; c < C; ++c) {
-            if (!has_dr) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) D[c][j] = 0.0f;
-            } else if (RING) {
-                get(gdr, odr, c, D[c]);
+            if (!inside(c)) continue;
+            float r[8], y[8], x[8], f[8];
+            get_y(c, y);
+            get_r(c, r);
+            get_du(c, x);
+            get_dr(c, f);
+            vdot(syy, y, y);
+            vmul(y, y, cw[c]);
+            if (GATE == kByElement) {
+                float a[8];
+                get_a(c, a);
+                vmul(y, y, a);
             }
-            if (has_du) {
-                if (RING) get(q.du, odu, c, dn[c]);   // read again: 16 registers less over the exchange
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    gw_pre[c][j] = fmaf(dn[c][j], r[c][j] * rho, gw_pre[c][j]);
-                    D[c][j] = fmaf(rho * wq[c][j], dn[c][j], fmaf(-rk, r[c][j], D[c][j]));
-                }
-            }
-            if (q.dr && !dead) norm_store<VEC>(static_cast<RT*>(q.dr) + at, c, t, tpr, H, D[c]);
-            if (!has_y) continue;
-            float dgf[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float e = D[c][j] * y[c][j];
-                if (GATE == kByRow) {
-                    E[c][j] = fmaf(g1, e, E[c][j]);
-                    sum[1] = fmaf(cw[c][j], e, sum[1]);        // a token gate's gradient, and mean(dm m)
-                    D[c][j] *= cw[c][j] * g1;                  // dm
-                } else if (GATE == kByColumn) {
-                    E[c][j] += e;
-                    sum[0] = fmaf(cw[c][j], e, sum[0]);
-                    D[c][j] *= cw[c][j];
-                } else {
-                    const float ca = cw[c][j] * a[c][j];
-                    E[c][j] = fmaf(a[c][j], e, E[c][j]);
-                    sum[0] = fmaf(ca, e, sum[0]);
-                    dgf[j] = cw[c][j] * e * (p.gate_sigmoid ? a[c][j] * (1.0f - a[c][j]) : 1.0f);
-                    D[c][j] *= ca;
-                }
-            }
-            if (GATE == kByElement && q.dgate && !dead)
-                norm_store<VEC>(static_cast<uint16_t*>(q.dgate) + at, c, t, tpr, H, dgf);
+            vdot(sdq, f, y);
+            vdot(srr, r, r);
+            vdot(srq, r, y);
+            vdot(sqq, y, y);
+            unpack8(wq[c], f);
+            vmul(x, x, f);
+            vdot(sxr, x, r);
+            vdot(sxq, x, y);
         }
-        if (GATE == kByRow) sum[0] = sum[1];
-        {
-            float one[1] = {sum[0]};
-            ring_sum<1>(one, group, tpr, red + half * norm_red_floats(tpr));   // also: everyone has read the stage
+        float sum[7] = {syy[0] + syy[1], srr[0] + srr[1], srq[0] + srq[1], sqq[0] + sqq[1],
+                        sxr[0] + sxr[1], sxq[0] + sxq[1], sdq[0] + sdq[1]};
+        ring_sum<7>(sum, group, tpr, red + half * norm_red_floats(tpr));
+        half ^= 1;
+        // everyone is past the row before: its stage takes the row that follows the ones under way
+        if (row != first) {
+            const int sp = s == 0 ? stages - 1 : s - 1;
+            rc.fill(t, row + (stages - 1) * step, p.T, base_a + sp * stage, stage, bar + 8 * sp);
+        }
+        const float rho_y = w_post ? rsqrtf(sum[0] * inv_h + p.eps) : 1.0f;
+        const float k1 = g1 * rho_y;   // v's factor of q
+        const float parts = sum[1] + k1 * k1 * sum[3];
+        float ss = parts + 2.0f * k1 * sum[2], sx = sum[4] + k1 * sum[5];
+        const bool direct = sum_cancelled(ss, parts);   // the same for the whole group
+        if (direct) {
+            float d0[2] = {0, 0}, d1s[2] = {0, 0};
+#pragma unroll 1
+            for (int c = 0; c < C; ++c) {
+                if (!inside(c)) continue;
+                float r[8], y[8], x[8], f[8];
+                get_y(c, y);
+                get_r(c, r);
+                get_du(c, x);
+#pragma unroll
+                for (int cc = 0; cc < C; ++cc)
+                    if (cc == c) {
+                        vmul(f, rho_y, y);
+                        vmul(y, f, cw[cc]);
+                        unpack8(wq[cc], f);
+                    }
+                vmul(x, x, f);
+                if (GATE == kByElement) {
+                    get_a(c, f);
+                    vmul(y, y, f);
+                }
+                vfma(r, g1, y, r);
+                vdot(d0, r, r);
+                vdot(d1s, x, r);
+            }
+            float two[2] = {d0[0] + d0[1], d1s[0] + d1s[1]};
+            ring_sum<2>(two, group, tpr, red + half * norm_red_floats(tpr));
             half ^= 1;
-            sum[0] = one[0];
+            ss = two[0];
+            sx = two[1];
         }
-        if (RING) fill(row + stages * step, s);
-        if (has_y) {
-            if (token && q.dgate && t == 0 && !dead) static_cast<float*>(q.dgate)[row] = sum[0] * d1;
-            if (q.dy && !dead) {
-                const float k = w_post ? sum[0] * (GATE == kByRow ? g1 : 1.0f) * inv_h : 0.0f;
+        const float rho = rsqrtf(ss * inv_h + p.eps);
+        const float rk = sx * inv_h * rho * rho * rho;   // rho mean(x n) rho
+        float sdm = k1 * (sum[6] + rho * sum[5] - rk * (sum[2] + k1 * sum[3]));   // sum dm m; over d1 / g1: dg of a token
+        float sdg = rho_y * (sum[6] + rho * sum[5] - rk * (sum[2] + k1 * sum[3]));
+        if (direct) {
+            float d0[2] = {0, 0};
+#pragma unroll 1
+            for (int c = 0; c < C; ++c) {
+                if (!inside(c)) continue;
+                float r[8], y[8], x[8], f[8], D[8];
+                get_y(c, y);
+                get_r(c, r);
+                get_du(c, x);
+                get_dr(c, D);
 #pragma unroll
-                for (int c = 0; c < C; ++c) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) D[c][j] = rho_y * fmaf(-k, y[c][j], D[c][j]);
-                    norm_store<VEC>(q.dy + at, c, t, tpr, H, D[c]);
+                for (int cc = 0; cc < C; ++cc)
+                    if (cc == c) {
+                        vmul(f, rho_y, y);
+                        vmul(y, f, cw[cc]);
+                        unpack8(wq[cc], f);
+                    }
+                vmul(x, x, f);
+                if (GATE == kByElement) {
+                    get_a(c, f);
+                    vmul(y, y, f);
                 }
+                vfma(r, g1, y, r);
+                vfma(D, -rk, r, D);
+                vfma(D, rho, x, D);
+                vdot(d0, D, y);
+            }
+            float one[1] = {d0[0] + d0[1]};
+            ring_sum<1>(one, group, tpr, red + half * norm_red_floats(tpr));
+            half ^= 1;
+            sdg = one[0];
+            sdm = g1 * sdg;
+        }
+        if (token && q.dgate && t == 0 && !dead) static_cast<float*>(q.dgate)[row] = sdg * d1;
+        const float kd = w_post ? sdm * inv_h : 0.0f;
+        // ---- second walk: every output ---------------------------------------------------------------
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            if (!inside(c)) continue;
+            float r[8], m[8], D[8], f[8], a[8];
+            get_y(c, m);
+            get_r(c, r);
+            get_dr(c, D);
+            vmul(m, rho_y, m);
+            if (GATE == kByElement) {
+                get_a(c, a);
+                vmul(f, cw[c], a);
+            } else if (GATE == kByRow) {
+                vmul(f, g1, cw[c]);
+            } else {
+                vmul(f, 1.0f, cw[c]);
+            }
+            float x[8], e[8];
+            vfma(r, f, m, r);   // r'
+            get_du(c, x);
+            vmul(x, rho, x);
+            vfma(gw_pre[c], x, r, gw_pre[c]);
+            vfma(D, -rk, r, D);
+            unpack8(wq[c], e);
+            vfma(D, x, e, D);
+            if (q.dr && !dead) put(static_cast<RT*>(q.dr), c, D);
+            vmul(e, D, m);
+            if (GATE == kByRow) vfma(E[c], g1, e, E[c]);
+            else if (GATE == kByColumn) vfma(E[c], 1.0f, e, E[c]);
+            else vfma(E[c], a, e, E[c]);
+            if (GATE == kByElement && q.dgate && !dead) {
+                vmul(e, cw[c], e);
+                if (p.gate_sigmoid) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) e[j] *= a[j] * (1.0f - a[j]);
+                }
+                put(static_cast<uint16_t*>(q.dgate), c, e);
+            }
+            if (q.dy && !dead) {
+                vmul(D, f, D);        // dm
+                vfma(D, -kd, m, D);
+                vmul(D, rho_y, D);
+                put(q.dy, c, D);
             }
         }
         if (++s == stages) {
@@ -694,40 +841,186 @@ __global__ void __launch_bounds__(MAXT) block_norm_backward_kernel(NormBwdParams
     }
     if (dead) atomicOr(&g_op_status, kDevLoadTimeout);
     if (!q.part) return;
-    // the CTA's groups join in order, over the stages (every copy has landed and been read), then one
-    // partial per CTA
+    // the CTA's groups join over the stages (every copy has landed and been read): each leaves its column
+    // sums, then they are added in group order, one partial per CTA
     __syncthreads();
-    float* cols = reinterpret_cast<float*>(norm_dyn);   // [3][H] when the CTA has more than one group
+    float* cols = reinterpret_cast<float*>(norm_dyn);   // [groups][3][H]
+    float* own = cols + (size_t)group * 3 * H;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        float ga[8], wp[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ga[j] = wp[j] = 1.0f;
+        if (GATE == kByColumn) {
+            norm_load<8>(p.gate, c, t, tpr, H, true, ga);
+            if (w_post) norm_load<8>(p.w_post, c, t, tpr, H, true, wp);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            float da = 1.0f;
+            if (GATE == kByColumn && p.gate_sigmoid) {
+                ga[j] = sigmoidf(ga[j]);
+                da = ga[j] * (1.0f - ga[j]);
+            }
+            wp[j] *= p.scale * da * E[c][j];
+            E[c][j] *= p.scale * ga[j];
+        }
+        norm_store<8>(own, c, t, tpr, H, E[c]);
+        norm_store<8>(own + H, c, t, tpr, H, gw_pre[c]);
+        if (GATE == kByColumn) norm_store<8>(own + 2 * H, c, t, tpr, H, wp);
+    }
+    __syncthreads();
     float* out = q.part + (size_t)blockIdx.x * 3 * H;
-    for (int g = 0; g < groups; ++g) {
-        if (group == g) {
-            float* to = g < groups - 1 ? cols : out;
-#pragma unroll
-            for (int c = 0; c < C; ++c) {
-                float ga[8], wp[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) ga[j] = wp[j] = 1.0f;
-                if (GATE == kByColumn) {
-                    norm_load<VEC>(p.gate, c, t, tpr, H, true, ga);
-                    if (w_post) norm_load<VEC>(p.w_post, c, t, tpr, H, true, wp);
-                }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int e = norm_elem<VEC>(c, j, t, tpr);
-                    if (e >= H) continue;
-                    float da = 1.0f;
-                    if (GATE == kByColumn && p.gate_sigmoid) {
-                        ga[j] = sigmoidf(ga[j]);
-                        da = ga[j] * (1.0f - ga[j]);
-                    }
-                    const float v[3] = {p.scale * (GATE == kByColumn ? ga[j] : 1.0f) * E[c][j], gw_pre[c][j],
-                                        p.scale * wp[j] * da * E[c][j]};
-#pragma unroll
-                    for (int i = 0; i < 3; ++i) to[i * H + e] = g > 0 ? cols[i * H + e] + v[i] : v[i];
-                }
+    for (int e = threadIdx.x; e < (GATE == kByColumn ? 3 : 2) * H; e += blockDim.x) {
+        float v = cols[e];
+        for (int g = 1; g < groups; ++g) v += cols[(size_t)g * 3 * H + e];
+        out[e] = v;
+    }
+}
+
+// A row's columns one at a time, t, t + tpr, ...: any width, alignment and set of operands.  The same sums and
+// the same two walks, over memory (the second finds the row in L1); the sums over rows lie in shared
+// memory, where each column has one thread per group.
+template <typename OT>
+FE_DEV float any_get(const OT* p, size_t i)
+{
+    if constexpr (std::is_same<OT, float>::value) return p[i];
+    else return bf16_bits_to_f32(p[i]);
+}
+
+template <bool R32, int GATE>
+__global__ void __launch_bounds__(512) block_norm_backward_any_kernel(NormBwdParams q, int tpr)
+{
+    using RT = typename std::conditional<R32, float, uint16_t>::type;
+    extern __shared__ __align__(128) uint8_t norm_dyn[];
+    const NormParams& p = q.f;
+    const int t = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = blockDim.x / tpr;
+    const int H = p.H;
+    const bool has_y = p.y != nullptr, has_du = q.du != nullptr, has_dr = q.dr_out != nullptr;
+    const bool token = p.gate_kind == kGateToken, w_post = p.w_post != nullptr, sig = p.gate_sigmoid != 0;
+    // [groups] reduction halves, then [groups][2][H] sums over rows: of e (times the row's or element's
+    // gate) and of du n
+    float* red = reinterpret_cast<float*>(norm_dyn) + (size_t)group * 2 * norm_red_floats(tpr);
+    float* sums = reinterpret_cast<float*>(norm_dyn) + (size_t)groups * 2 * norm_red_floats(tpr);
+    float* E = sums + (size_t)group * 2 * H;
+    float* gw_pre = E + H;
+    for (int i = t; i < 2 * norm_red_floats(tpr); i += tpr) red[i] = 0.0f;
+    for (int e = t; e < 2 * H; e += tpr) E[e] = 0.0f;
+    __syncthreads();
+    griddep_wait();
+    griddep_launch();
+    const RT* pr = static_cast<const RT*>(p.r);
+    const RT* pdr = static_cast<const RT*>(q.dr_out);
+    const int64_t step = (int64_t)gridDim.x * groups, first = (int64_t)blockIdx.x * groups + group;
+    const float inv_h = 1.0f / (float)H;
+    int half = 0;
+    for (int64_t row = first; row < p.T; row += step) {
+        const size_t at = (size_t)row * H;
+        float g1 = 1.0f, d1 = 1.0f;
+        if (token) {
+            g1 = bf16_bits_to_f32(p.gate[row]);
+            if (sig) {
+                g1 = sigmoidf(g1);
+                d1 = g1 * (1.0f - g1);
             }
         }
-        if (groups > 1) __syncthreads();
+        // the gate of column e and scale w_post (a row gate stays out of both)
+        auto gate_at = [&](int e) {
+            if (GATE == kByRow) return 1.0f;
+            const float g = bf16_bits_to_f32(p.gate[GATE == kByElement ? at + e : (size_t)e]);
+            return sig ? sigmoidf(g) : g;
+        };
+        auto cw_at = [&](int e) { return p.scale * (w_post ? bf16_bits_to_f32(p.w_post[e]) : 1.0f); };
+        auto x_at = [&](int e) { return has_du ? bf16_bits_to_f32(q.du[at + e]) * bf16_bits_to_f32(p.w_pre[e]) : 0.0f; };
+        auto y_at = [&](int e) { return has_y ? bf16_bits_to_f32(p.y[at + e]) : 0.0f; };
+        auto d_at = [&](int e) { return has_dr ? any_get(pdr, at + e) : 0.0f; };
+        float sum[7] = {0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 4
+        for (int e = t; e < H; e += tpr) {
+            const float y = y_at(e), r = any_get(pr, at + e), x = x_at(e), d = d_at(e);
+            const float f = cw_at(e) * gate_at(e) * y;
+            sum[0] = fmaf(y, y, sum[0]);
+            sum[1] = fmaf(r, r, sum[1]);
+            sum[2] = fmaf(r, f, sum[2]);
+            sum[3] = fmaf(f, f, sum[3]);
+            sum[4] = fmaf(x, r, sum[4]);
+            sum[5] = fmaf(x, f, sum[5]);
+            sum[6] = fmaf(d, f, sum[6]);
+        }
+        ring_sum<7>(sum, group, tpr, red + half * norm_red_floats(tpr));
+        half ^= 1;
+        const float rho_y = w_post ? rsqrtf(sum[0] * inv_h + p.eps) : 1.0f;
+        const float k1 = g1 * rho_y;
+        const float parts = sum[1] + k1 * k1 * sum[3];
+        float ss = parts + 2.0f * k1 * sum[2], sx = sum[4] + k1 * sum[5];
+        const bool direct = sum_cancelled(ss, parts);
+        if (direct) {
+            float two[2] = {0, 0};
+#pragma unroll 1
+            for (int e = t; e < H; e += tpr) {
+                const float r = any_get(pr, at + e) + cw_at(e) * gate_at(e) * g1 * (rho_y * y_at(e));
+                two[0] = fmaf(r, r, two[0]);
+                two[1] = fmaf(x_at(e), r, two[1]);
+            }
+            ring_sum<2>(two, group, tpr, red + half * norm_red_floats(tpr));
+            half ^= 1;
+            ss = two[0];
+            sx = two[1];
+        }
+        const float rho = has_du ? rsqrtf(ss * inv_h + p.eps) : 0.0f;
+        const float rk = has_du ? sx * inv_h * rho * rho * rho : 0.0f;
+        float sdg = rho_y * (sum[6] + rho * sum[5] - rk * (sum[2] + k1 * sum[3]));
+        if (direct) {
+            float one[1] = {0};
+#pragma unroll 1
+            for (int e = t; e < H; e += tpr) {
+                const float f = cw_at(e) * gate_at(e), m = rho_y * y_at(e);
+                const float r = any_get(pr, at + e) + f * g1 * m;
+                one[0] = fmaf(d_at(e) + rho * x_at(e) - rk * r, f * m, one[0]);
+            }
+            ring_sum<1>(one, group, tpr, red + half * norm_red_floats(tpr));
+            half ^= 1;
+            sdg = one[0];
+        }
+        if (token && q.dgate && t == 0) static_cast<float*>(q.dgate)[row] = sdg * d1;
+        const float kd = w_post ? sdg * g1 * inv_h : 0.0f;
+#pragma unroll 2
+        for (int e = t; e < H; e += tpr) {
+            const float m = rho_y * y_at(e), a = gate_at(e), cw = cw_at(e), f = cw * a * g1;
+            const float r = fmaf(f, m, any_get(pr, at + e));   // r'
+            const float D = d_at(e) + rho * x_at(e) - rk * r;
+            if (has_du) gw_pre[e] = fmaf(bf16_bits_to_f32(q.du[at + e]), r * rho, gw_pre[e]);
+            if (q.dr) {
+                if constexpr (R32) static_cast<float*>(q.dr)[at + e] = D;
+                else static_cast<uint16_t*>(q.dr)[at + e] = (uint16_t)(bf16x2_rn(D, 0.0f) & 0xffffu);
+            }
+            const float em = D * m;
+            E[e] = fmaf(GATE == kByRow ? g1 : GATE == kByElement ? a : 1.0f, em, E[e]);
+            if (GATE == kByElement && q.dgate)
+                static_cast<uint16_t*>(q.dgate)[at + e] = (uint16_t)(bf16x2_rn(cw * em * (sig ? a * (1.0f - a) : 1.0f), 0.0f) & 0xffffu);
+            if (q.dy) q.dy[at + e] = (uint16_t)(bf16x2_rn(rho_y * (D * f - kd * m), 0.0f) & 0xffffu);
+        }
+    }
+    if (!q.part) return;
+    __syncthreads();
+    float* out = q.part + (size_t)blockIdx.x * 3 * H;
+    for (int e = threadIdx.x; e < H; e += blockDim.x) {
+        float v = 0.0f, g = 0.0f;
+        for (int k = 0; k < groups; ++k) {
+            v += sums[(size_t)k * 2 * H + e];
+            g += sums[(size_t)k * 2 * H + H + e];
+        }
+        float a = 1.0f, da = 1.0f;
+        if (GATE == kByColumn) {
+            a = bf16_bits_to_f32(p.gate[e]);
+            if (sig) {
+                a = sigmoidf(a);
+                da = a * (1.0f - a);
+            }
+            out[2 * H + e] = p.scale * (w_post ? bf16_bits_to_f32(p.w_post[e]) : 1.0f) * da * v;
+        }
+        out[e] = p.scale * a * v;
+        out[H + e] = g;
     }
 }
 
