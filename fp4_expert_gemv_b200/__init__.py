@@ -641,10 +641,10 @@ def balance_loss(logits, idx, mask=None, balance_coef=1.0, z_coef=0.0, loss=None
     counts = _out(counts, "counts", i32, (E,), dev)
     n_tokens = _out(n_tokens, "n_tokens", i32, (1,), dev)
     nb = fe_moe_balance_workspace(T, E)
-    ws = torch.empty(max(nb, 1), dtype=torch.uint8, device=dev)
+    ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
     with _device(dev):
         check(fe_moe_balance_loss(lp, ip, mp, T, E, k, balance_coef, z_coef, loss.data_ptr(), counts.data_ptr(),
-                                  n_tokens.data_ptr(), ws.data_ptr(), nb, _current_stream(dev)), "fe_moe_balance_loss")
+                                  n_tokens.data_ptr(), _dptr(ws), nb, _current_stream(dev)), "fe_moe_balance_loss")
     return loss, counts, n_tokens
 
 

@@ -9,6 +9,8 @@
 // (all -inf) has p = 0 and adds nothing to P and z.
 #pragma once
 
+#include "bulk.cuh"
+#include "cluster.cuh"
 #include "common.cuh"
 #include "norm.cuh"
 
@@ -82,12 +84,15 @@ FE_DEV void bal_softmax(float (&l)[N], float& inv, float& lse)
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float mm = m == -INFINITY ? 0.0f : m;
-    float s = 0.0f;
+    float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+    for (int i = 0; i < N; i += 2) {
         l[i] = __expf(l[i] - mm);
-        s += l[i];
+        l[i + 1] = __expf(l[i + 1] - mm);
+        s0 += l[i];
+        s1 += l[i + 1];
     }
+    float s = s0 + s1;
     s = bal_row_sum<L>(s);
     inv = s == 0.0f ? 0.0f : 1.0f / s;
     lse = s == 0.0f ? 0.0f : mm + logf(s);
@@ -236,6 +241,128 @@ __global__ void __launch_bounds__(kBalThreads, N == 16 ? 3 : 1) balance_kernel(B
         n_all = nn;
     }
     bal_finish(p, sums, &n_all, rank, ranks);
+}
+
+// The first pass over many rows: as balance_kernel leaves its partials, but every warp's groups of rows stream
+// through its own ring in shared memory (one cp.async.bulk per group: its rows are neighbours), so
+// that the loads of several groups are under way per warp while its chain of shuffles and exponentials
+// runs (T = 65536, E = 512: 38 us with one group ahead in registers).  Padded rows travel too and
+// are left out.  A CTA per SM.
+constexpr int kBalRingSmem = 224 * 1024;
+constexpr int kBalRingStages = 8;   // at most
+
+__host__ __device__ constexpr int bal_ring_warps(int N) { return N == 16 ? 24 : 12; }
+
+template <int L, int N>
+__global__ void __launch_bounds__(32 * bal_ring_warps(N)) balance_ring_kernel(BalanceParams p, int stages)
+{
+    constexpr int W = bal_ring_warps(N), R = 32 / L;
+    extern __shared__ __align__(128) uint8_t bal_dyn[];
+    __shared__ int cnt[L * N];
+    __shared__ float scratch[32];
+    __shared__ int ns[32];
+    __shared__ uint64_t bars[W * kBalRingStages];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r = lane % L, sub = lane / L;
+    const uint32_t stage = 4u * R * p.E;   // a group of rows
+    const uint32_t ring = smem_addr(bal_dyn) + warp * stages * stage, bar = smem_addr(&bars[kBalRingStages * warp]);
+    for (int e = threadIdx.x; e < p.E; e += 32 * W) cnt[e] = 0;
+    if (lane < stages) mbar_init(bar + 8 * lane, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncthreads();
+    griddep_wait();
+    griddep_launch();
+    const int64_t step = (int64_t)gridDim.x * W * R;
+    auto fill = [&](int64_t t0, int s) {
+        if (lane != 0 || t0 >= p.T) return;
+        const uint32_t bytes = 4u * p.E * (uint32_t)min((int64_t)R, p.T - t0);
+        mbar_expect_tx(bar + 8 * s, bytes);
+        bulk_g2s(ring + s * stage, p.logits + (size_t)t0 * p.E, bytes, bar + 8 * s);
+    };
+    const int64_t first = ((int64_t)blockIdx.x * W + warp) * R;
+    for (int s = 0; s < stages; ++s) fill(first + s * step, s);
+    float acc[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+    float z = 0.0f;
+    int n = 0, s = 0;
+    uint32_t parity = 0;
+    bool dead = false;
+    // the next group's mask byte and chosen id are fetched a group ahead
+    uint32_t keep_next = 0;
+    int id_next = -1;
+    auto ahead = [&](int64_t t) {
+        keep_next = t < p.T;
+        id_next = -1;
+        if (t < p.T) {
+            if (p.mask) keep_next = p.mask[t];
+            if (r < p.k) id_next = p.idx[(size_t)t * p.k + r];
+        }
+    };
+    ahead(first + sub);
+    for (int64_t t0 = first; t0 < p.T; t0 += step) {
+        const int64_t t = t0 + sub;
+        const bool on = keep_next != 0;
+        const int id = on ? id_next : -1;
+        ahead(t + step);
+        if (!dead && !mbar_wait(bar + 8 * s, parity, kNormTimeoutNs)) dead = true;
+        float l[N], inv, lse;
+        const uint32_t row = ring + s * stage + 4u * sub * p.E;
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const int e = bal_elem<L, 4>(i, r);
+            l[i] = l[i + 1] = l[i + 2] = l[i + 3] = -INFINITY;
+            if (on && e < p.E)
+                asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                             : "=f"(l[i]), "=f"(l[i + 1]), "=f"(l[i + 2]), "=f"(l[i + 3])
+                             : "r"(row + 4u * e));
+        }
+        bal_softmax<L, N>(l, inv, lse);   // a row that is off is all -inf: zeros
+        __syncwarp();                     // the warp has read the stage
+        fill(t0 + stages * step, s);
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] += l[i] * inv;
+        if (r == 0) {
+            z += lse * lse;
+            n += on;
+        }
+        if ((unsigned)id < (unsigned)p.E) atomicAdd(&cnt[id], 1);   // integers: any order, one result
+        if (on && p.k > L)
+            for (int j = r + L; j < p.k; j += L) {
+                const int e = p.idx[(size_t)t * p.k + j];
+                if ((unsigned)e < (unsigned)p.E) atomicAdd(&cnt[e], 1);
+            }
+        __syncwarp();
+        if (++s == stages) {
+            s = 0;
+            parity ^= 1;
+        }
+    }
+    if (dead) atomicOr(&g_op_status, kDevLoadTimeout);
+    const float zz = bal_block_sum(z, scratch);   // and every warp is done with its ring
+    float(*ps)[L * N] = reinterpret_cast<float(*)[L * N]>(bal_dyn);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+#pragma unroll
+        for (int o = L; o < 32; o <<= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+        if (sub == 0) ps[warp][bal_elem<L, 4>(i, r)] = acc[i];
+    }
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (lane == 0) ns[warp] = n;
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += 32 * W) {
+        float v = 0.0f;
+#pragma unroll 8
+        for (int w = 0; w < W; ++w) v += ps[w][e];
+        p.part[(size_t)blockIdx.x * p.E + e] = v;
+        p.ipart[(size_t)blockIdx.x * p.E + e] = cnt[e];
+    }
+    if (threadIdx.x == 0) {
+        int nn = 0;
+        for (int w = 0; w < W; ++w) nn += ns[w];
+        p.part[(size_t)p.G * p.E + blockIdx.x] = zz;
+        p.ipart[(size_t)p.G * p.E + blockIdx.x] = nn;
+    }
 }
 
 // Joins the CTAs' partials in a fixed order and writes the loss and the counts: one cluster, each CTA an

@@ -213,11 +213,24 @@ cudaError_t norm_ring(const fe::NormParams& p, const NormRingPlan& b, cudaStream
     return norm_ring_launch<R32, fe::kByRow, true>(p, b, s);
 }
 
+template <bool R32, int GATE, bool ALL>
+cudaError_t norm_bwd_columns(const fe::NormBwdParams& q, int sms, int* partials, cudaStream_t s)
+{
+    static std::atomic<bool> ready[64];
+    const int H = q.f.H, tpr = std::min(512, norm_threads(H, 1)), groups = 512 / tpr;
+    const size_t smem = sizeof(float) * groups * (2 * (size_t)fe::norm_red_floats(tpr) + 2 * (size_t)H);
+    *partials = (int)std::min<int64_t>(2 * sms, (q.f.T + groups - 1) / groups);
+    const auto kernel = fe::block_norm_backward_any_kernel<R32, GATE, ALL>;
+    const cudaError_t e = norm_ring_ready(kernel, ready);
+    if (e != cudaSuccess) return e;
+    return launch(kernel, *partials, 512, smem, s, q, tpr);
+}
+
 // Through the ring when rows are whole aligned chunks and every operand is there, else column by column.
 template <bool R32, int GATE>
 cudaError_t norm_bwd_any(const fe::NormBwdParams& q, bool vec, int sms, int* partials, cudaStream_t s)
 {
-    static std::atomic<bool> ring_ready[64], any_ready[64];
+    static std::atomic<bool> ring_ready[64];
     const int H = q.f.H;
     NormRingPlan b;
     if (vec && q.f.y && q.du && q.dr_out &&
@@ -229,13 +242,8 @@ cudaError_t norm_bwd_any(const fe::NormBwdParams& q, bool vec, int sms, int* par
         if (e != cudaSuccess) return e;
         return launch(kernel, b.grid, b.threads, b.smem, s, q, b.tpr, b.stages);
     }
-    const int tpr = std::min(512, norm_threads(H, 1)), groups = 512 / tpr;
-    const size_t smem = sizeof(float) * groups * (2 * (size_t)fe::norm_red_floats(tpr) + 2 * (size_t)H);
-    *partials = (int)std::min<int64_t>(2 * sms, (q.f.T + groups - 1) / groups);
-    const auto kernel = fe::block_norm_backward_any_kernel<R32, GATE>;
-    const cudaError_t e = norm_ring_ready(kernel, any_ready);
-    if (e != cudaSuccess) return e;
-    return launch(kernel, *partials, 512, smem, s, q, tpr);
+    const bool all = q.f.y && q.f.w_post && q.du && q.dr_out;
+    return all ? norm_bwd_columns<R32, GATE, true>(q, sms, partials, s) : norm_bwd_columns<R32, GATE, false>(q, sms, partials, s);
 }
 
 template <bool R32>
@@ -264,8 +272,11 @@ int balance_ctas(int64_t T, int E)
     return (int)std::max<int64_t>(1, std::min<int64_t>(kMaxBalanceCtas, (T + rows - 1) / rows));
 }
 
-// Groups of rows per warp up to which one cluster takes the whole loss.
-constexpr int kBalanceFusedGroups = 4;
+// Whether one cluster takes the whole loss: up to four groups of rows per warp.
+bool balance_fused(int64_t T, int E)
+{
+    return T <= (int64_t)4 * fe::kBalCluster * fe::kBalWarps * (32 / balance_lanes(E));
+}
 
 fe_status check_balance(const float* logits, const uint8_t*, int64_t T, int E, int top_k)
 {
@@ -291,6 +302,50 @@ cudaError_t balance_run(const fe::BalanceParams& p, bool backward, int grid, cud
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, fe::balance_kernel<L, N, VEC>, p);
+}
+
+// Dynamic shared memory of the streamed pass, and the stages of a warp's ring (to eight) that fit, each a
+// group of 32 / L rows.
+constexpr int balance_ring_room(int L, int N)
+{
+    return fe::kBalRingSmem - 4 * L * N - 1024 - 8 * fe::kBalRingStages * fe::bal_ring_warps(N);
+}
+
+int balance_stages(int E, int L, int N)
+{
+    return std::min(fe::kBalRingStages, balance_ring_room(L, N) / (4 * (32 / L) * E * fe::bal_ring_warps(N)));
+}
+
+template <int L, int N>
+cudaError_t balance_ring_run(const fe::BalanceParams& p, cudaStream_t s)
+{
+    static std::atomic<bool> ready[64];
+    const int W = fe::bal_ring_warps(N), stages = balance_stages(p.E, L, N);
+    const size_t smem = std::max((size_t)stages * W * 4 * (32 / L) * p.E, sizeof(float) * W * L * N);
+    const auto kernel = fe::balance_ring_kernel<L, N>;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, balance_ring_room(L, N));
+        if (e != cudaSuccess) return e;
+        ready[dev].store(true, std::memory_order_release);
+    }
+    return launch(kernel, p.G, 32 * W, smem, s, p, stages);
+}
+
+cudaError_t balance_ring_dispatch(const fe::BalanceParams& p, cudaStream_t s)
+{
+    if (p.E > 512) return balance_ring_run<32, 32>(p, s);
+    switch (balance_lanes(p.E)) {
+        case 1: return balance_ring_run<1, 16>(p, s);
+        case 2: return balance_ring_run<2, 16>(p, s);
+        case 4: return balance_ring_run<4, 16>(p, s);
+        case 8: return balance_ring_run<8, 16>(p, s);
+        case 16: return balance_ring_run<16, 16>(p, s);
+    }
+    return balance_ring_run<32, 16>(p, s);
 }
 
 template <int L, int N>
@@ -751,7 +806,7 @@ fe_status fe_moe_block_norm_backward(const void* dr_out, const void* du, const v
 
 size_t fe_moe_balance_workspace(int64_t T, int E)
 {
-    if (T < 0 || E < 1 || E > fe::kBalMaxE) return 0;
+    if (T < 0 || E < 1 || E > fe::kBalMaxE || balance_fused(T, E)) return 0;
     return 8 * (size_t)balance_ctas(T, E) * ((size_t)E + 1);
 }
 
@@ -761,10 +816,11 @@ fe_status fe_moe_balance_loss(const float* logits, const int32_t* idx, const uin
 {
     const fe_status st = check_balance(logits, mask, T, E, top_k);
     if (st != FE_OK) return st;
-    if ((T > 0 && !idx) || !loss || !counts || !n_tokens || !workspace || !aligned(idx, 4) || !aligned(loss, 4) ||
+    if ((T > 0 && !idx) || !loss || !counts || !n_tokens || !aligned(idx, 4) || !aligned(loss, 4) ||
         !aligned(counts, 4) || !aligned(n_tokens, 4) || !aligned(workspace, 4))
         return FE_ERR_INVALID_ARG;
     const size_t need = fe_moe_balance_workspace(T, E);
+    if (need > 0 && !workspace) return FE_ERR_INVALID_ARG;
     if (workspace_bytes < need) return FE_ERR_CAPACITY;
     const void* ins[3] = {logits, idx, mask};
     const size_t in_n[3] = {4 * (size_t)T * E, 4 * (size_t)T * top_k, (size_t)T};
@@ -791,7 +847,7 @@ fe_status fe_moe_balance_loss(const float* logits, const int32_t* idx, const uin
     const int ctas = balance_ctas(T, E);
     const bool vec = E % 4 == 0 && aligned(logits, 16);
     const cudaStream_t s = (cudaStream_t)stream;
-    if (T <= (int64_t)kBalanceFusedGroups * fe::kBalCluster * fe::kBalWarps * (32 / balance_lanes(E))) {
+    if (balance_fused(T, E)) {
         int n = 1;   // CTAs of the cluster: a group per warp, to eight
         while (n < fe::kBalCluster && n < ctas) n *= 2;
         p.G = 0;
@@ -801,7 +857,16 @@ fe_status fe_moe_balance_loss(const float* logits, const int32_t* idx, const uin
     p.G = ctas;
     p.part = static_cast<float*>(workspace);
     p.ipart = reinterpret_cast<int32_t*>(p.part + (size_t)p.G * (E + 1));
-    FE_CUDA_TRY(balance_dispatch(p, false, p.G, vec, s));
+    const int sms = sm_count();
+    if (sms < 1) return record_cuda(cudaErrorInvalidDevice, "device");
+    const int64_t groups = (T + 32 / balance_lanes(E) - 1) / (32 / balance_lanes(E));
+    if (vec && ctas >= sms && groups >= 4 * (int64_t)sms * fe::bal_ring_warps(E > 512 ? 32 : 16)) {
+        p.G = sms;
+        p.ipart = reinterpret_cast<int32_t*>(p.part + (size_t)p.G * (E + 1));
+        FE_CUDA_TRY(balance_ring_dispatch(p, s));
+    } else {
+        FE_CUDA_TRY(balance_dispatch(p, false, p.G, vec, s));
+    }
     FE_CUDA_TRY(launch(fe::balance_final_kernel, dim3(fe::kBalCluster), dim3(1024), 0, s, p));
     return FE_OK;
 }
@@ -942,6 +1007,7 @@ fe_status fe_moe_linear_backward(const void* dy, int64_t lddy, const void* x, in
     const void* dz = direct ? dy : dzbuf;
     float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                            align256(2 * (size_t)M * (((size_t)N + 7) / 8 * 8)));
+    int partials = 0;
     if (!direct || db) {
         fe::LinDzParams p{};
         p.dy = static_cast<const uint16_t*>(dy);
@@ -962,30 +1028,32 @@ fe_status fe_moe_linear_backward(const void* dy, int64_t lddy, const void* x, in
         const dim3 grid((cols + per - 1) / per, used);
         FE_CUDA_TRY(vec ? launch(fe::linear_dz_kernel<8>, grid, dim3(256), 0, s, p)
                         : launch(fe::linear_dz_kernel<1>, grid, dim3(256), 0, s, p));
-        if (db)
-            FE_CUDA_TRY(launch(fe::column_sum_kernel, dim3((N + 31) / 32, 1), dim3(1024), 0, s,
-                               static_cast<const float*>(part), used, N, 1, db, static_cast<float*>(nullptr),
-                               static_cast<float*>(nullptr)));
+        partials = used;
     }
-    if (!dx && !dw) return FE_OK;
-    // dW [N][K] = dZ^T X (longest tiles first), dX [M][K] = dZ W: one launch
-    fe::LinParams P{};
-    Product prod[2];
-    int n = 0;
-    if (dw) {
-        prod[n] = {{dz, M, N, lddz}, {x, M, K, ldx}, true, true, N, K, (int)M};
-        P.p[n].out = static_cast<uint16_t*>(dw);
-        P.p[n].ldo = P.p[n].cols = K;
-        ++n;
+    if (dx || dw) {
+        // dW [N][K] = dZ^T X (longest tiles first), dX [M][K] = dZ W: one launch
+        fe::LinParams P{};
+        Product prod[2];
+        int n = 0;
+        if (dw) {
+            prod[n] = {{dz, M, N, lddz}, {x, M, K, ldx}, true, true, N, K, (int)M};
+            P.p[n].out = static_cast<uint16_t*>(dw);
+            P.p[n].ldo = P.p[n].cols = K;
+            ++n;
+        }
+        if (dx) {
+            prod[n] = {{dz, M, N, lddz}, {w, N, K, K}, false, true, (int)M, K, N};
+            P.p[n].out = static_cast<uint16_t*>(dx);
+            P.p[n].ldo = lddx;
+            P.p[n].cols = K;
+            ++n;
+        }
+        FE_CUDA_TRY(lin_run(P, prod, n, s));
     }
-    if (dx) {
-        prod[n] = {{dz, M, N, lddz}, {w, N, K, K}, false, true, (int)M, K, N};
-        P.p[n].out = static_cast<uint16_t*>(dx);
-        P.p[n].ldo = lddx;
-        P.p[n].cols = K;
-        ++n;
-    }
-    FE_CUDA_TRY(lin_run(P, prod, n, s));
+    if (db)   // last: the products need not wait for it
+        FE_CUDA_TRY(launch(fe::column_sum_kernel, dim3((N + 31) / 32, 1), dim3(1024), 0, s,
+                           static_cast<const float*>(part), partials, N, 1, db, static_cast<float*>(nullptr),
+                           static_cast<float*>(nullptr)));
     return FE_OK;
 }
 

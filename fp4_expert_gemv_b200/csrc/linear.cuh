@@ -185,6 +185,21 @@ FE_DEV bool elect_one()
     return p != 0;
 }
 
+// Position in a ring of S stages: the stage and the parity of its current round.
+struct RingPos {
+    uint32_t s, parity;
+    bool full_round;   // the ring has been filled once
+    FE_DEV RingPos() : s(0), parity(0), full_round(false) {}
+    FE_DEV void next(uint32_t S)
+    {
+        if (++s == S) {
+            s = 0;
+            parity ^= 1;
+            full_round = true;
+        }
+    }
+};
+
 FE_DEV void expect_tx(uint32_t bar, uint32_t bytes)
 {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
@@ -392,7 +407,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
 
     if (warp == 0) {
         // ---- producer: this CTA's boxes of A and B into its ring, reported to the leader ------------
-        uint32_t it = 0;
+        RingPos at;
+        uint32_t loads = 0;
         for (int i = 0; i < P.n; ++i) {
             const LinProblem& p = P.p[i];
             const int nk = (p.K + 63) / 64, tiles_n = p.tiles_n, a_mn = p.a_mn, b_mn = p.b_mn, cols = p.cols;
@@ -404,9 +420,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                 // swiglu: the leader's columns are gate rows of W, the other's the up rows of the same
                 // output columns
                 const int n0 = glu ? tn * (BN / 2) + (rank ? cols : 0) : tn * BN + (BN / 2) * rank;
-                for (int k = 0; k < nk; ++k, ++it) {
-                    const uint32_t s = it % S;
-                    if (it >= S && !lin_wait_warp(empty(s), (it / S - 1) & 1)) {
+                for (int k = 0; k < nk; ++k, at.next(S), ++loads) {
+                    const uint32_t s = at.s;
+                    if (at.full_round && !lin_wait_warp(empty(s), at.parity ^ 1)) {
                         *abort = 1;
                         break;
                     }
@@ -434,11 +450,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
         }
         // no copy outlives the loop: the leader sees those of both CTAs land
         if (rank == 0)
-            for (uint32_t j = it > S ? it - S : 0; j < it; ++j) lin_wait_warp(full(j % S), (j / S) & 1);
+            for (uint32_t j = loads > S ? loads - S : 0; j < loads; ++j) lin_wait_warp(full(j % S), (j / S) & 1);
     } else if (warp == 1) {
         if (rank == 0) {
             // ---- MMA issue, for both CTAs ------------------------------------------------------------
-            uint32_t it = 0, done = 0;
+            RingPos at;
+            uint32_t done = 0;
             for (int i = 0; i < P.n; ++i) {
                 const LinProblem& p = P.p[i];
                 const int nk = (p.K + 63) / 64, a_mn = p.a_mn, b_mn = p.b_mn;
@@ -450,9 +467,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                     const int acc = done & 1;
                     if (done >= 2 && !lin_wait_warp(accempty(acc), (done / 2 - 1) & 1)) *abort = 1;
                     tc_fence_after();
-                    for (int k = 0; k < nk && !*abort; ++k, ++it) {
-                        const uint32_t s = it % S;
-                        if (!lin_wait_warp(full(s), (it / S) & 1)) {
+                    for (int k = 0; k < nk && !*abort; ++k, at.next(S)) {
+                        const uint32_t s = at.s;
+                        if (!lin_wait_warp(full(s), at.parity)) {
                             *abort = 1;
                             break;
                         }
@@ -717,10 +734,11 @@ __global__ void __launch_bounds__(kSplThreads) linear_split_kernel(const __grid_
     griddep_launch();
     if (warp == 0) {
         const int n0 = GLU ? tn * 32 : tn * 64, n1 = GLU ? n0 + p.cols : n0 + 32;
+        RingPos ri;
         uint32_t i = 0;
-        for (int k = k0; k < k1; ++k, ++i) {
-            const uint32_t s = i % S;
-            if (i >= S && !lin_wait_warp(empty(s), (i / S - 1) & 1)) {
+        for (int k = k0; k < k1; ++k, ++i, ri.next(S)) {
+            const uint32_t s = ri.s;
+            if (ri.full_round && !lin_wait_warp(empty(s), ri.parity ^ 1)) {
                 *abort = 1;
                 break;
             }
@@ -737,10 +755,10 @@ __global__ void __launch_bounds__(kSplThreads) linear_split_kernel(const __grid_
     } else if (warp == 1) {
         const uint32_t idesc = lin_idesc(0, 0, 128, kSplN);
         const uint64_t a0 = tc_smem_desc(ring), b0 = tc_smem_desc(ring + 128 * 128);
-        uint32_t i = 0;
-        for (int k = k0; k < k1; ++k, ++i) {
-            const uint32_t s = i % S;
-            if (!lin_wait_warp(full(s), (i / S) & 1)) {
+        RingPos ri;
+        for (int k = k0; k < k1; ++k, ri.next(S)) {
+            const uint32_t s = ri.s;
+            if (!lin_wait_warp(full(s), ri.parity)) {
                 *abort = 1;
                 break;
             }
@@ -749,7 +767,7 @@ __global__ void __launch_bounds__(kSplThreads) linear_split_kernel(const __grid_
                 const uint64_t a = a0 + s * (kSplStage >> 4), b = b0 + s * (kSplStage >> 4);
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    tc_mma_f16(tmem, a + 2 * ks, b + 2 * ks, idesc, (i > 0 || ks > 0) ? 1u : 0u);
+                    tc_mma_f16(tmem, a + 2 * ks, b + 2 * ks, idesc, (k > k0 || ks > 0) ? 1u : 0u);
                 tc_commit(empty(s));
             }
             __syncwarp();
@@ -785,11 +803,20 @@ __global__ void __launch_bounds__(kSplThreads) linear_split_kernel(const __grid_
     constexpr int TPR = GLU ? 8 : 16;   // threads per row, four columns each
     const int cc = 4 * (tid % TPR), col0 = tn * (GLU ? 32 : 64) + cc, left = p.cols - col0;
     if (left > 0) {
-#pragma unroll 1
+        // a thread's columns are the same in every row: the bias once; a row's residual is asked for before
+        // its partials are added
+        float bv[4] = {0, 0, 0, 0}, bu[4] = {0, 0, 0, 0};
+        if (p.bias) {
+            spl_add4(p.bias + col0, left, bv);
+            if (GLU) spl_add4(p.bias + p.cols + col0, left, bu);
+        }
+#pragma unroll 2
         for (int i = tid / TPR; i < per; i += kSplThreads / TPR) {
             const int row = (i << lg) + rank;
             if (row >= rows) break;
-            float v[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0};
+            const size_t grow = (size_t)(m0 + row);
+            float v[4] = {bv[0], bv[1], bv[2], bv[3]}, u[4] = {bu[0], bu[1], bu[2], bu[3]}, add[4] = {0, 0, 0, 0};
+            if (p.res) spl_add4(p.res + grow * p.ldr + col0, left, add);
             const float* from = part + i * kSplLd + cc;
 #pragma unroll 2
             for (int s = 0; s < p.splits; ++s, from += per * kSplLd) {
@@ -799,11 +826,6 @@ __global__ void __launch_bounds__(kSplThreads) linear_split_kernel(const __grid_
                     const float4 w = *reinterpret_cast<const float4*>(from + 32);
                     u[0] += w.x; u[1] += w.y; u[2] += w.z; u[3] += w.w;
                 }
-            }
-            const size_t grow = (size_t)(m0 + row);
-            if (p.bias) {
-                spl_add4(p.bias + col0, left, v);
-                if (GLU) spl_add4(p.bias + p.cols + col0, left, u);
             }
             if (p.z) {
                 spl_store4(p.z + grow * p.N + col0, left, v);
@@ -815,7 +837,8 @@ __global__ void __launch_bounds__(kSplThreads) linear_split_kernel(const __grid_
             } else {
                 act_all<4>(p.act, v);
             }
-            if (p.res) spl_add4(p.res + grow * p.ldr + col0, left, v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] += add[j];
             spl_store4(p.out + grow * p.ldo + col0, left, v);
         }
     }
@@ -849,11 +872,12 @@ FE_DEV void fma8(const uint4& a, const uint4& b, float& acc)
 
 constexpr int kLinRowsWarps = 4;
 
-// A warp per output column (two weight rows for swiglu), MR rows of x.
+// A warp per output column (two weight rows for swiglu), MR rows of x (used for one).
 template <int MR, bool GLU>
 __global__ void __launch_bounds__(32 * kLinRowsWarps) linear_rows_kernel(LinRowsParams p)
 {
     griddep_wait();
+    griddep_launch();
     const int lane = threadIdx.x & 31;
     const int c = blockIdx.x * kLinRowsWarps + (threadIdx.x >> 5);
     if (c >= p.cols) return;

@@ -166,6 +166,7 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(NormParams p, int tpr)
     using RT = typename std::conditional<R32, float, uint16_t>::type;
     __shared__ float red[2][32][1];
     griddep_wait();
+    griddep_launch();
     const int t = threadIdx.x & (tpr - 1);
     const int64_t row = (int64_t)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
     const bool on = row < p.T;
@@ -888,16 +889,17 @@ FE_DEV float any_get(const OT* p, size_t i)
     else return bf16_bits_to_f32(p[i]);
 }
 
-template <bool R32, int GATE>
-__global__ void __launch_bounds__(512) block_norm_backward_any_kernel(NormBwdParams q, int tpr)
+template <bool R32, int GATE, bool ALL>
+__global__ void __launch_bounds__(512, 2) block_norm_backward_any_kernel(NormBwdParams q, int tpr)
 {
     using RT = typename std::conditional<R32, float, uint16_t>::type;
     extern __shared__ __align__(128) uint8_t norm_dyn[];
     const NormParams& p = q.f;
     const int t = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = blockDim.x / tpr;
     const int H = p.H;
-    const bool has_y = p.y != nullptr, has_du = q.du != nullptr, has_dr = q.dr_out != nullptr;
-    const bool token = p.gate_kind == kGateToken, w_post = p.w_post != nullptr, sig = p.gate_sigmoid != 0;
+    // ALL: every operand is there
+    const bool has_y = ALL || p.y != nullptr, has_du = ALL || q.du != nullptr, has_dr = ALL || q.dr_out != nullptr;
+    const bool token = p.gate_kind == kGateToken, w_post = ALL || p.w_post != nullptr, sig = p.gate_sigmoid != 0;
     // [groups] reduction halves, then [groups][2][H] sums over rows: of e (times the row's or element's
     // gate) and of du n
     float* red = reinterpret_cast<float*>(norm_dyn) + (size_t)group * 2 * norm_red_floats(tpr);
@@ -984,12 +986,13 @@ __global__ void __launch_bounds__(512) block_norm_backward_any_kernel(NormBwdPar
         }
         if (token && q.dgate && t == 0) static_cast<float*>(q.dgate)[row] = sdg * d1;
         const float kd = w_post ? sdg * g1 * inv_h : 0.0f;
-#pragma unroll 2
+#pragma unroll 4
         for (int e = t; e < H; e += tpr) {
             const float m = rho_y * y_at(e), a = gate_at(e), cw = cw_at(e), f = cw * a * g1;
             const float r = fmaf(f, m, any_get(pr, at + e));   // r'
-            const float D = d_at(e) + rho * x_at(e) - rk * r;
-            if (has_du) gw_pre[e] = fmaf(bf16_bits_to_f32(q.du[at + e]), r * rho, gw_pre[e]);
+            const float u = has_du ? bf16_bits_to_f32(q.du[at + e]) * rho : 0.0f;
+            const float D = d_at(e) + (has_du ? u * bf16_bits_to_f32(p.w_pre[e]) : 0.0f) - rk * r;
+            if (has_du) gw_pre[e] = fmaf(u, r, gw_pre[e]);
             if (q.dr) {
                 if constexpr (R32) static_cast<float*>(q.dr)[at + e] = D;
                 else static_cast<uint16_t*>(q.dr)[at + e] = (uint16_t)(bf16x2_rn(D, 0.0f) & 0xffffu);

@@ -485,7 +485,8 @@ fe_status fe_moe_block_norm_backward(const void* dr_out, const void* du, const v
                                      float* dw_post, float* dw_pre, void* workspace, size_t workspace_bytes,
                                      fe_stream_t stream);
 
-/* Bytes of workspace fe_moe_balance_loss needs (0 for sizes it refuses). */
+/* Bytes of workspace fe_moe_balance_loss needs (0 for small batches, which need none,
+ * and for sizes it refuses). */
 size_t fe_moe_balance_workspace(int64_t T, int E);
 
 /* The router's balance loss and the experts' token counts, over the n tokens that
@@ -495,7 +496,7 @@ size_t fe_moe_balance_workspace(int64_t T, int E);
  *   z = (1/n) sum_t logsumexp(logits_t)^2,  loss = balance_coef * balance + z_coef * z.
  *   logits float [T][E] and idx int32 [T][top_k], as fe_moe_router writes them (ids
  *   outside [0, E) are not counted; an id given twice counts twice);
- *   mask   uint8 [T], 0 = padding (its rows are not read), or NULL;
+ *   mask   uint8 [T], 0 = padding (its logits and ids count for nothing), or NULL;
  *   loss   float [3]: loss, balance, z;  counts int32 [E];  n_tokens int32 [1].
  * -inf logits have p = 0; a row of them alone adds nothing to balance and z; a NaN or
  * +inf logit makes the loss NaN.  n = 0: all zeros.  1 <= E <= 1024, T * top_k < 2^31

@@ -49,8 +49,8 @@ def test_norm_backward_refusals(kw, want):
 
 
 def balance(**kw):
-    a = dict(logits=A, idx=B, mask=None, T=16, E=8, k=2, a=1.0, b=0.0, loss=C, counts=D, n=F, ws=G,
-             nb=fe.fe_moe_balance_workspace(16, 8))
+    a = dict(logits=A, idx=B, mask=None, T=50000, E=8, k=2, a=1.0, b=0.0, loss=C, counts=D, n=F, ws=G,
+             nb=fe.fe_moe_balance_workspace(50000, 8))
     a.update(kw)
     return fe.fe_moe_balance_loss(*a.values(), None)
 
@@ -118,6 +118,7 @@ def test_linear_backward_refusals(kw, want):
 def test_workspace_queries_answer_zero_for_refused_sizes():
     assert fe.fe_moe_block_norm_workspace(4, 0) == 0 and fe.fe_moe_block_norm_workspace(4, 16385) == 0
     assert fe.fe_moe_balance_workspace(4, 1025) == 0 and fe.fe_moe_balance_workspace(-1, 8) == 0
+    assert fe.fe_moe_balance_workspace(64, 128) == 0 and fe.fe_moe_balance_workspace(50000, 128) > 8 * 128
     assert fe.fe_moe_linear_workspace(4, 8, 12, 0) == 0 and fe.fe_moe_linear_workspace(4, 7, 16, 4) == 0
     assert fe.fe_moe_forward_block_workspace(None, 4, 8) == 0
     # at least dz [M][N rounded up to 8] in bf16 and one partial row of column sums
