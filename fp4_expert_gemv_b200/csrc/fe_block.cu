@@ -381,7 +381,8 @@ fe_status check_linear_shape(int64_t M, int N, int K, int act)
     if (M < 0 || N < 1 || K < 1 || !act_ok(act, N)) return FE_ERR_INVALID_ARG;
     // TMA rows are multiples of 16 bytes; tile counts and coordinates are 32-bit
     if (K % 8 != 0 || M > INT32_MAX - 256 || N > INT32_MAX - 256 || K > INT32_MAX - 256 ||
-        (M / 128 + 1) * (int64_t)(std::max(N, K) / 64 + 1) > INT32_MAX / 4)
+        (M / 128 + 1) * (int64_t)(std::max(N, K) / 64 + 1) > INT32_MAX / 4 ||
+        (int64_t)(N / 128 + 1) * (K / 64 + 1) > INT32_MAX / 4)
         return FE_ERR_UNSUPPORTED;
     return FE_OK;
 }

@@ -947,7 +947,7 @@ namespace {
 
 // The body of fe_moe_forward (also run by the stack for each of its layers).
 fe_status forward_impl(fe_moe_t h, const void* x_bf16, const float* router_logits, int T, int top_k, void* y_bf16,
-                       fe_stream_t stream)
+                       fe_stream_t stream, bool check_only = false)
 {
     if (!h || T < 0 || top_k < 1 || top_k > h->E) return FE_ERR_INVALID_ARG;
     if (T == 0) return FE_OK;
@@ -967,6 +967,7 @@ fe_status forward_impl(fe_moe_t h, const void* x_bf16, const float* router_logit
     if (h->path == FE_PATH_AUTO || h->path == FE_PATH_FUSED_DECODE) {
         const uint32_t wbytes = decode_weight_bytes(h, T, top_k);
         if (wbytes > 0) {
+            if (check_only) return FE_OK;
             fe_status st = decode_path(h, x_bf16, router_logits, T, top_k, y_bf16, wbytes, s);
             if (st == FE_OK) {
                 h->last_T = T;
@@ -983,6 +984,7 @@ fe_status forward_impl(fe_moe_t h, const void* x_bf16, const float* router_logit
     if (h->path == FE_PATH_NVFP4) {
         if (!h->nv_gu || !h->nv_b || !h->tc_tiles) return FE_ERR_UNSUPPORTED;
         if (!aligned16(x_bf16)) return FE_ERR_INVALID_ARG;   // the x rows are read in 16-byte pieces
+        if (check_only) return FE_OK;
         const fe_status rs = route_and_group(h, router_logits, T, top_k, nullptr, s);
         if (rs != FE_OK) return rs;
         const fe_status st = nvfp4_path(h, static_cast<const uint16_t*>(x_bf16), T, top_k, s);
@@ -999,6 +1001,7 @@ fe_status forward_impl(fe_moe_t h, const void* x_bf16, const float* router_logit
         return FE_OK;
     }
 
+    if (check_only) return FE_OK;
     const bool use_tc = tc_ok && (h->path == FE_PATH_TCGEN05 || (h->path == FE_PATH_AUTO && P >= kTcAutoPairs));
     SgSetup sg;
     const bool use_stream = !use_tc && stream_setup(h, T, sg);
@@ -1124,7 +1127,7 @@ fe_status fe_moe_forward_block(fe_moe_t h, const fe_moe_block_t* b, const void* 
     fe_status st = FE_OK;
     if (!u_in) st = fe_host::check_block_norm(r, r_dtype, nullptr, nullptr, nullptr, FE_GATE_NONE, b->w_pre, b->eps, T, H, nullptr, ub);
     if (st == FE_OK) st = router_impl(h, u, b->w_router, T, top_k, logits, nullptr, nullptr, nullptr, true);
-    if (st == FE_OK && top_k > h->max_k) st = FE_ERR_CAPACITY;
+    if (st == FE_OK) st = forward_impl(h, u, logits, T, top_k, y, nullptr, true);
     if (st == FE_OK && shared)
         st = fe_host::check_linear(u, H, b->shared_gate_up, nullptr, nullptr, 0, T, 2 * I, H, FE_ACT_SWIGLU, a, I, nullptr);
     if (st == FE_OK && shared)

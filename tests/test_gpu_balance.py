@@ -39,6 +39,33 @@ def test_loss_counts_and_gradient(T, E, k, pad):
     check(fe, *make(T, E, k, pad, seed=T + E), up=None if pad else -1.75)
 
 
+@pytest.mark.parametrize("T, E, k", [(15003, 512, 10), (60001, 128, 8), (8001, 1024, 40), (30000, 200, 3)])
+def test_streamed_batches(T, E, k):
+    """Enough rows for the pass that streams them, padded rows holding anything, rows of -inf."""
+    import fp4_expert_gemv_b200 as fe
+    l, idx, mask = make(T, E, k, True, seed=T)
+    l[mask == 0] = float("nan")
+    idx[::7, 0] = -1
+    l[::11] = -math.inf
+    l[5::11, 1:] = -math.inf
+    mask[5::11] = 0
+    check(fe, l, idx, mask)
+    a = fe.balance_loss(l, idx, mask=mask)
+    b = fe.balance_loss(l, idx, mask=mask)
+    assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+def test_large_logits_keep_their_differences():
+    """Softmax depends on differences alone, however large the logits (exact multiples of 2 here)."""
+    import fp4_expert_gemv_b200 as fe
+    l, idx, _ = make(300, 64, 4, False, seed=8)
+    l = torch.round(l * 4) * 2
+    base = fe.balance_loss(l, idx)
+    for off in (1e4, -1e6, 2.0 ** 23):
+        got = fe.balance_loss(l + off, idx)
+        assert torch.equal(got[0][1], base[0][1]) and torch.isfinite(got[0]).all()
+
+
 def test_chosen_ids_given_twice_or_out_of_range():
     import fp4_expert_gemv_b200 as fe
     l, idx, mask = make(50, 40, 4, False, seed=3)

@@ -118,7 +118,47 @@ def test_block_refusals():
         call(r, 2, p["w_router"], w_pre=p["w_pre"], shared=(p["shared"][0], p["shared"][1][:, :32]))
     with pytest.raises(ValueError):
         call(r, 2, p["w_router"], w_pre=p["w_pre"], u_out=r.to(bf))
+    # a path that cannot run the call is refused before the norm in front of it is launched
+    gl.layer.set_path(fe.PATH_NVFP4)
+    logits = torch.full((4, 8), 3.0, device="cuda")
+    with pytest.raises(fe.FeMoeError):
+        call(r, 2, p["w_router"], w_pre=p["w_pre"], logits=logits)
+    torch.cuda.synchronize()
+    assert (logits == 3).all()
     gl.layer.close()
+
+
+def test_first_calls_inside_a_capture():
+    """A process whose first calls are captured: nothing in them synchronises or allocates."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch, fp4_expert_gemv_b200 as fe
+bf = torch.bfloat16
+x, w = torch.randn(3000, 256, device="cuda").to(bf), torch.randn(512, 256, device="cuda").to(bf)
+h = torch.ones(256, device="cuda").to(bf)
+l = torch.randn(3000, 16, device="cuda")
+idx = torch.zeros(3000, 2, dtype=torch.int32, device="cuda")
+def step():
+    y = fe.linear(x, w)
+    z = fe.linear(x[:70], w)
+    _, u = fe.block_norm(x, w_pre=h)
+    g = fe.block_norm_backward(x, u, x, x, h, h)
+    loss, c, n = fe.balance_loss(l, idx)
+    return y, z, u, *g[:2], loss, fe.balance_loss_backward(l, c, n, 2), *fe.linear_backward(y, x, w)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = step()
+g.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(out, step()))
+print("same")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=root, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
 
 
 def test_training_the_router_on_the_balance_loss():

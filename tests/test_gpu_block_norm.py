@@ -78,6 +78,46 @@ def test_many_rows_walk_several_times():
     check_backward(fe, c, "channel", True)
 
 
+@pytest.mark.parametrize("T, H, rt, gate", [(700, 4096, torch.bfloat16, "token"), (15001, 64, torch.float32, "full"),
+                                            (2500, 512, torch.bfloat16, "full"), (1300, 2048, torch.bfloat16, "none"),
+                                            (3700, 2048, torch.float32, "channel"), (320, 8192, torch.bfloat16, "channel")])
+def test_streamed_rows(T, H, rt, gate):
+    """Enough rows per group for the kernels that stream them, with a ragged last round."""
+    import fp4_expert_gemv_b200 as fe
+    c = make(T, H, rt, gate, seed=T)
+    check_forward(fe, c, gate, True)
+    check_backward(fe, c, gate, True)
+    # the norm alone, and without its weight
+    c["g"] = c["y"] = c["w_post"] = None
+    check_forward(fe, c, "none", False)
+
+
+@pytest.mark.parametrize("T, H", [(5, 256), (5, 255), (5003, 136), (15001, 64)])
+@pytest.mark.parametrize("gate", ["none", "token", "channel", "full"])
+def test_rows_where_the_residual_cancels(T, H, gate):
+    """r' = r + s a v where r is -s a v but for a thousandth: the sum of squares of r' is a millionth of its
+    parts, so an expansion into products of r and v alone would lose it.  The bound is the rows' own
+    magnitudes' (the fp32 error of r' relative to |r| + |s a v|, through rho)."""
+    import fp4_expert_gemv_b200 as fe
+    c = make(T, H, torch.float32, gate, seed=31)
+    zero = dict(c, r=torch.zeros_like(c["r"]))
+    sav = ref.norm_forward(zero["r"], c["y"], c["w_post"], None, c["g"], gate, False, 0.5, EPS)["r_out"][0]
+    c["r"] = (-sav + 1e-3 * torch.randn(T, H, device="cuda", dtype=torch.float64)).float()
+    c["r"][::3] = torch.randn(T, H, device="cuda")[::3]         # other rows stay ordinary
+    check_forward(fe, c, gate, False)
+    check_backward(fe, c, gate, False)
+
+
+def test_without_weight_gradients():
+    import fp4_expert_gemv_b200 as fe
+    for H in (512, 511):
+        c = make(70, H, torch.bfloat16, "channel", seed=2)
+        args = (c["dr_out"], c["du"], c["r"], c["y"], c["w_post"], c["w_pre"])
+        kw = dict(gate=c["g"], gate_kind=fe.GATE_CHANNEL, scale=0.5)
+        full, part = fe.block_norm_backward(*args, **kw), fe.block_norm_backward(*args, weight_grads=False, **kw)
+        assert torch.equal(full[0], part[0]) and torch.equal(full[1], part[1]) and part[2:] == (None, None, None)
+
+
 def test_unaligned_rows():
     """A width of whole chunks whose rows start 2 bytes off take the narrow accesses."""
     import fp4_expert_gemv_b200 as fe

@@ -46,7 +46,8 @@ def check_backward(fe, dy, x, w, z, act):
 
 
 SHAPES = [(1, 2, 8), (1, 1536, 2048), (2, 30, 264), (3, 64, 72), (5, 130, 520), (8, 66, 1000), (9, 64, 64), (17, 34, 40), (64, 2048, 768),
-          (127, 130, 200), (128, 256, 64), (129, 258, 72), (200, 1536, 2048), (1003, 1002, 1992), (700, 22, 8)]
+          (127, 130, 200), (128, 256, 64), (129, 258, 72), (200, 1536, 2048), (1003, 1002, 1992), (700, 22, 8),
+          (2000, 1300, 200), (1201, 1536, 136), (2303, 2048, 72)]   # the last: CTA pairs, 192, 128 and 256 columns wide
 
 
 @pytest.mark.parametrize("act", ACTS)
@@ -104,7 +105,7 @@ def test_small_integers_come_out_exactly(M, N, K):
     assert torch.equal(db.double(), dy.double().sum(0))
 
 
-@pytest.mark.parametrize("M", [1, 4, 40, 300])
+@pytest.mark.parametrize("M", [1, 4, 40, 300, 20000])
 def test_strided_rows_and_the_sum_in_place(M):
     import fp4_expert_gemv_b200 as fe
     x, w, bias, res, dy = make(M, 96, 128, "none", seed=M)
@@ -129,7 +130,7 @@ def test_strided_rows_and_the_sum_in_place(M):
 
 def test_infinities_and_nan_stay_in_their_rows():
     import fp4_expert_gemv_b200 as fe
-    for M in (4, 140):
+    for M in (4, 140, 20000):
         x, w, bias, res, _ = make(M, 64, 128, "silu", seed=2)
         clean = fe.linear(x, w, act=fe.ACT_SILU)
         x[1, 5] = float("nan")
@@ -194,13 +195,14 @@ def test_gradient_against_differences():
         assert abs((f[0] - f[1]) / 2e-4 - float((got[name].double() * dirn).sum())) <= tol, name
 
 
-def test_streams_and_graphs():
+@pytest.mark.parametrize("M", [384, 5000])
+def test_streams_and_graphs(M):
     import fp4_expert_gemv_b200 as fe
-    x, w, bias, res, dy = make(384, 512, 256, "swiglu", seed=3)
+    x, w, bias, res, dy = make(M, 512, 256, "swiglu", seed=3)
     x1 = x[:2].contiguous()
 
     def step(stream=None):
-        z = torch.empty(384, 512, dtype=bf, device="cuda")
+        z = torch.empty(M, 512, dtype=bf, device="cuda")
         y = fe.linear(x, w, bias=bias, act=fe.ACT_SWIGLU, residual=res, z=z, stream=stream)
         return (y, z, fe.linear(x1, w, act=fe.ACT_SWIGLU, stream=stream),
                 *fe.linear_backward(dy, x, w, z=z, act=fe.ACT_SWIGLU, stream=stream))
@@ -227,6 +229,31 @@ def test_streams_and_graphs():
     for out in got:
         assert all(torch.equal(a, b) for a, b in zip(first, out))
     assert fe.op_status() == (fe.FE_OK, 0)
+
+
+def test_rows_after_the_last_stay_as_they_were():
+    import fp4_expert_gemv_b200 as fe
+    for M in (3, 100, 2500):
+        x, w, bias, res, dy = make(M, 1536 if M > 1000 else 96, 128, "none", seed=M)
+        N = w.shape[0]
+        y = torch.full((M + 300, N), 5.0, dtype=bf, device="cuda")
+        z = torch.full((M + 300, N), 6.0, dtype=bf, device="cuda")
+        fe.linear(x, w, act=fe.ACT_SILU, y=y[:M], z=z[:M])
+        assert (y[M:] == 5).all() and (z[M:] == 6).all()
+
+
+def test_gelu_over_its_whole_range():
+    """z = x exactly (w is the identity).  Relative to z Phi(z), down to 1e-30: half a step of bf16, and 2^-14
+    for the exponential of z^2 / 2 <= 72 (its argument and the fast exponential's product each rounded to
+    2^-24 of it: 72 * 3 * 2^-24) and the polynomial."""
+    import fp4_expert_gemv_b200 as fe
+    z = torch.linspace(-12, 12, 64 * 512, device="cuda").to(bf).view(-1, 64)
+    eye = torch.eye(64, dtype=bf, device="cuda")
+    for rows in (z[:16], z, z.repeat(60, 1)):
+        y = fe.linear(rows.contiguous(), eye, act=fe.ACT_GELU).double()
+        x = rows.double()
+        want = x * 0.5 * torch.special.erfc(-x / 2 ** 0.5)
+        assert ((y - want).abs() <= (2.0 ** -8 + 2.0 ** -14) * want.abs() + 1e-30).all()
 
 
 def test_refusals():
