@@ -575,8 +575,10 @@ cudaError_t lin_run(fe::LinParams& P, const Product* f, int n, cudaStream_t s)
                        : lin_launch<128, false>(P, f, n, s);
 }
 
+constexpr int kSplSmem = 227 * 1024;   // all that a CTA can have
+
 // Products of few tiles, the contraction split over clusters.
-template <bool GLU>
+template <bool GLU, int BN, bool VEC>
 cudaError_t split_launch(const fe::LinProblem& q, const Product& f, int splits, cudaStream_t s)
 {
     static std::atomic<bool> ready[64];
@@ -585,34 +587,36 @@ cudaError_t split_launch(const fe::LinProblem& q, const Product& f, int splits, 
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     if (!ready[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(fe::linear_split_kernel<GLU>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)fe::spl_smem(fe::kSplStages));
+        e = cudaFuncSetAttribute(fe::linear_split_kernel<GLU, BN, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSplSmem);
         if (e != cudaSuccess) return e;
         ready[dev].store(true, std::memory_order_release);
     }
     fe::LinSplitParams p{};
     e = tensor_map(&p.ta, f.a.p, f.a.rows, f.a.cols, f.a.ld, 64, 128);
-    if (e == cudaSuccess) e = tensor_map(&p.tb, f.b.p, f.b.rows, f.b.cols, f.b.ld, 64, 32);
+    if (e == cudaSuccess) e = tensor_map(&p.tb, f.b.p, f.b.rows, f.b.cols, f.b.ld, 64, BN / 2);
     if (e != cudaSuccess) return e;
+    const int w = lin_tile_cols(q, BN);
     p.M = f.M;
     p.N = f.N;
     p.K = f.K;
     p.splits = splits;
-    const int steps = (f.K + 63) / 64;
-    p.stages = std::min(fe::kSplStages, (steps + splits - 1) / splits);
     p.act = q.act;
     p.cols = q.cols;
     p.bias = q.bias;
     p.res = q.res;
     p.ldr = q.ldr;
+    p.vec_res = q.cols % 8 == 0 && q.ldr % 8 == 0 && aligned(q.res, 16);
+    p.res_bytes = q.res ? 128 / splits * w * 2 : 0;
+    const int steps = (f.K + 63) / 64;
+    p.stages = std::min(fe::kSplMaxStages, (steps + splits - 1) / splits);
+    while (fe::spl_smem(BN, p.stages, p.res_bytes) > kSplSmem) --p.stages;
     p.out = q.out;
     p.ldo = q.ldo;
     p.z = q.z;
-    const int w = lin_tile_cols(q, fe::kSplN);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((q.cols + w - 1) / w, (f.M + 127) / 128, splits);
     cfg.blockDim = dim3(fe::kSplThreads);
-    cfg.dynamicSmemBytes = fe::spl_smem(p.stages);
+    cfg.dynamicSmemBytes = fe::spl_smem(BN, p.stages, p.res_bytes);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -622,19 +626,78 @@ cudaError_t split_launch(const fe::LinProblem& q, const Product& f, int splits, 
     attr[1].val.clusterDim.z = splits;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, fe::linear_split_kernel<GLU>, p);
+    return cudaLaunchKernelEx(&cfg, fe::linear_split_kernel<GLU, BN, VEC>, p);
 }
 
-// CTAs that share a tile's contraction: as many (a power of two, to 8) as fill the SMs and leave each at
-// least two k steps; 0 if the tiles alone fill them.
-int split_ways(const fe::LinProblem& q, const Product& f, int sms)
+template <bool GLU>
+cudaError_t split_run(const fe::LinProblem& q, const Product& f, int BN, int splits, cudaStream_t s)
 {
-    const int w = lin_tile_cols(q, fe::kSplN);
-    const int64_t tiles = (int64_t)((q.cols + w - 1) / w) * ((f.M + 127) / 128);
-    if (tiles > sms) return 0;
-    int n = 1;
-    while (n < 8 && tiles * 2 * n <= sms && (f.K + 63) / 64 >= 4 * n) n *= 2;
-    return n;
+    const bool vec = q.cols % 4 == 0 && q.ldo % 4 == 0 && aligned(q.out, 8) && aligned(q.z, 8);
+    if (BN == 64)
+        return vec ? split_launch<GLU, 64, true>(q, f, splits, s) : split_launch<GLU, 64, false>(q, f, splits, s);
+    return vec ? split_launch<GLU, 128, true>(q, f, splits, s) : split_launch<GLU, 128, false>(q, f, splits, s);
+}
+
+// Clusters of 2^lg CTAs, one to an SM, that run at once (looked up once per device): a cluster lies within
+// one of the GPU's groups of SMs, so those of 8 leave some of them over.
+cudaError_t split_room(int lg, int* clusters)
+{
+    static std::atomic<int> known[64][4];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    int n = known[dev][lg].load(std::memory_order_acquire);
+    if (n == 0) {
+        e = cudaFuncSetAttribute(fe::linear_split_kernel<false, 128, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSplSmem);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(1, 1, 1 << lg);
+        cfg.blockDim = dim3(fe::kSplThreads);
+        cfg.dynamicSmemBytes = kSplSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1 << lg;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&n, fe::linear_split_kernel<false, 128, true>, &cfg);
+        if (e != cudaSuccess) return e;
+        if (n < 1) return cudaErrorLaunchOutOfResources;
+        known[dev][lg].store(n, std::memory_order_release);
+    }
+    *clusters = n;
+    return cudaSuccess;
+}
+
+// CTAs that share a tile's contraction (a power of two, to 8) and the tile's columns: of those whose
+// clusters all run at once, with two k steps or more a CTA, the least that an SM has to take in, its k
+// steps' operands and its share of the other CTAs' partial sums, which is what bounds these products (64
+// bytes a clock).  1024 x 1000 at K = 2048: 10.6 us with 64 columns and no split, 9.6 us with 128 and two
+// CTAs.  0 if the tiles alone fill the SMs.
+cudaError_t split_ways(const fe::LinProblem& q, const Product& f, int* ways, int* BN)
+{
+    *ways = 0;
+    int64_t least = INT64_MAX;
+    const int steps = (f.K + 63) / 64;
+    for (const int bn : {64, 128}) {
+        const int w = lin_tile_cols(q, bn);
+        const int64_t tiles = (int64_t)((q.cols + w - 1) / w) * ((f.M + 127) / 128);
+        for (int lg = bn == 64 ? 0 : 1; lg <= 3; ++lg) {   // 128 columns' sums and stages fit with a split only
+            const int n = 1 << lg;
+            int room = 0;
+            const cudaError_t e = split_room(lg, &room);
+            if (e != cudaSuccess) return e;
+            if (tiles > room || (lg > 0 && steps < 2 * n)) break;
+            const int64_t cost = (int64_t)((steps + n - 1) / n) * fe::spl_stage(bn) + 512 * bn / n * (n - 1);
+            if (cost < least) {
+                least = cost;
+                *ways = n;
+                *BN = bn;
+            }
+        }
+    }
+    return cudaSuccess;
 }
 
 template <bool GLU>
@@ -642,7 +705,7 @@ cudaError_t rows_launch(const fe::LinRowsParams& p, cudaStream_t s)
 {
     if (p.M == 1) {
         const int grid = (p.cols + fe::kLinRowsWarps - 1) / fe::kLinRowsWarps;
-        return launch(fe::linear_rows_kernel<1, GLU>, grid, 32 * fe::kLinRowsWarps, 0, s, p);
+        return launch(fe::linear_rows_kernel<GLU>, grid, 32 * fe::kLinRowsWarps, 0, s, p);
     }
     const int grid = (p.cols + (GLU ? 7 : 15)) / (GLU ? 8 : 16);
     if (p.M <= 8) return launch(fe::linear_skinny_kernel<1, GLU>, grid, 256, 0, s, p);
@@ -951,10 +1014,9 @@ fe_status fe_moe_linear(const void* x, int64_t ldx, const void* w, const void* b
     p.out = static_cast<uint16_t*>(y);
     p.ldo = ldy;
     p.z = static_cast<uint16_t*>(z);
-    const int sms = sm_count();
-    if (sms < 1) return record_cuda(cudaErrorInvalidDevice, "device");
-    const int ways = split_ways(p, f, sms);
-    if (ways > 0) FE_CUDA_TRY(act == FE_ACT_SWIGLU ? split_launch<true>(p, f, ways, s) : split_launch<false>(p, f, ways, s));
+    int BN = 0, ways = 0;
+    FE_CUDA_TRY(split_ways(p, f, &ways, &BN));
+    if (ways > 0) FE_CUDA_TRY(act == FE_ACT_SWIGLU ? split_run<true>(p, f, BN, ways, s) : split_run<false>(p, f, BN, ways, s));
     else FE_CUDA_TRY(lin_run(P, &f, 1, s));
     return FE_OK;
 }

@@ -637,22 +637,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
 
 // ---- few tiles: the contraction split over a cluster --------------------------------------
 
-constexpr int kSplN = 64;                     // columns of a tile (swiglu: 32 gate and their 32 up columns)
-constexpr int kSplStages = 7;
-constexpr int kSplThreads = 256;              // warp 0: TMA, 1: MMA, 2: TMEM; then all finish
-constexpr uint32_t kSplStage = 128 * 128 + kSplN * 128;
-constexpr int kSplLd = kSplN + 4;             // fp32 rows in shared memory: 16-byte accesses of 8 rows hit every bank
-constexpr uint32_t kSplPart = 128 * kSplLd * 4;   // [splits][128 / splits][kSplLd] partial rows this CTA finishes
+constexpr int kSplMaxStages = 7;
+constexpr int kSplThreads = 256;              // warp 0: TMA, 1: MMA, 2: TMEM, 4-7: residual; then all finish
+// A tile's columns are BN (64 or 128): for swiglu half of them gate columns, half their up columns.
+__host__ __device__ constexpr uint32_t spl_stage(int BN) { return 128 * 128 + BN * 128; }
+__host__ __device__ constexpr int spl_ld(int BN) { return BN + 4; }   // fp32 rows: 16-byte accesses of 8 rows hit every bank
+__host__ __device__ constexpr uint32_t spl_part(int BN) { return 128 * spl_ld(BN) * 4; }   // [splits][128 / splits] partial rows
 // Shared memory for `stages` stages: short contractions take few, so that CTAs of consecutive launches fit
-// an SM together.
-__host__ __device__ constexpr uint32_t spl_smem(int stages)
+// an SM together.  res: bytes of the finished rows' residual.
+__host__ __device__ constexpr uint32_t spl_smem(int BN, int stages, uint32_t res)
 {
-    return 1024 + stages * kSplStage + kSplPart + 8 * (2 * stages + 1) + 16;
+    return 1024 + stages * spl_stage(BN) + spl_part(BN) + res + 8 * (2 * stages + 1) + 16;
 }
 
 struct LinSplitParams {
-    CUtensorMap ta, tb;      // x: boxes of 64 k x 128 rows; w: 64 k x 32 rows
+    CUtensorMap ta, tb;      // x: boxes of 64 k x 128 rows; w: 64 k x BN / 2 rows
     int M, N, K, splits, stages, act, cols;
+    int vec_res;             // residual rows in 16-byte pieces
+    uint32_t res_bytes;      // of shared memory for the residual
     const uint16_t* bias;
     const uint16_t* res;
     int64_t ldr;
@@ -661,46 +663,104 @@ struct LinSplitParams {
     uint16_t* z;
 };
 
-// Up to 4 consecutive bf16 (left: how many belong to the matrix).
-FE_DEV void spl_store4(uint16_t* o, int left, const float (&v)[4])
+// A thread's four columns of a row: consecutive ones where rows are 8-byte aligned (VEC), else `step` apart, so
+// that the lanes of a row write consecutive halfwords.
+template <bool VEC>
+FE_DEV void spl_store4(uint16_t* o, int step, int left, const float (&v)[4])
 {
     const uint32_t a = bf16x2_rn(v[0], v[1]), b = bf16x2_rn(v[2], v[3]);
-    if (left >= 4 && (reinterpret_cast<uintptr_t>(o) & 7) == 0) {
+    if (VEC) {
         *reinterpret_cast<uint2*>(o) = make_uint2(a, b);
     } else {
         o[0] = (uint16_t)a;
-        if (left > 1) o[1] = (uint16_t)(a >> 16);
-        if (left > 2) o[2] = (uint16_t)b;
-        if (left > 3) o[3] = (uint16_t)(b >> 16);
+        if (left > step) o[step] = (uint16_t)(a >> 16);
+        if (left > 2 * step) o[2 * step] = (uint16_t)b;
+        if (left > 3 * step) o[3 * step] = (uint16_t)(b >> 16);
     }
 }
 
-// v += up to 4 consecutive bf16.
-FE_DEV void spl_add4(const uint16_t* s, int left, float (&v)[4])
+// v += four bf16, the same way.
+template <bool VEC>
+FE_DEV void spl_add4(const uint16_t* s, int step, int left, float (&v)[4])
 {
-    if (left >= 4 && (reinterpret_cast<uintptr_t>(s) & 7) == 0) {
+    if (VEC) {
         const uint2 q = *reinterpret_cast<const uint2*>(s);
         v[0] += __uint_as_float(q.x << 16);
         v[1] += __uint_as_float(q.x & 0xffff0000u);
         v[2] += __uint_as_float(q.y << 16);
         v[3] += __uint_as_float(q.y & 0xffff0000u);
     } else {
-        v[0] += bf16_bits_to_f32(s[0]);
-        if (left > 1) v[1] += bf16_bits_to_f32(s[1]);
-        if (left > 2) v[2] += bf16_bits_to_f32(s[2]);
-        if (left > 3) v[3] += bf16_bits_to_f32(s[3]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (left > j * step) v[j] += bf16_bits_to_f32(s[j * step]);
     }
 }
 
-// One 128 x 64 tile per cluster of `splits` CTAs (a power of two), each over its share of the k steps.
+template <bool VEC>
+FE_DEV void spl_sum4(const float* s, int step, float (&v)[4])
+{
+    if (VEC) {
+        const float4 q = *reinterpret_cast<const float4*>(s);
+        v[0] += q.x; v[1] += q.y; v[2] += q.z; v[3] += q.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] += s[j * step];
+    }
+}
+
+// The rows that a CTA of the cluster finishes: their partials added in rank order, then the epilogue.
+template <bool GLU, int BN, bool VEC>
+FE_DEV void spl_finish(const LinSplitParams& p, const float* part, const uint16_t* res, int m0, int tn, int rows, int rank)
+{
+    constexpr int W = GLU ? BN / 2 : BN, TPR = W / 4, LD = spl_ld(BN), STEP = VEC ? 1 : TPR;
+    const int tid = threadIdx.x, lg = 31 - __clz(p.splits), per = 128 >> lg;
+    const int cc = (VEC ? 4 : 1) * (tid % TPR), col0 = tn * W + cc, left = p.cols - col0;
+    if (left <= 0) return;
+    // a thread's columns are the same in every row: the bias once
+    float bv[4] = {0, 0, 0, 0}, bu[4] = {0, 0, 0, 0};
+    if (p.bias) {
+        spl_add4<false>(p.bias + col0, STEP, left, bv);
+        if (GLU) spl_add4<false>(p.bias + p.cols + col0, STEP, left, bu);
+    }
+#pragma unroll 2
+    for (int i = tid / TPR; i < per; i += kSplThreads / TPR) {
+        const int row = (i << lg) + rank;
+        if (row >= rows) break;
+        const size_t grow = (size_t)(m0 + row);
+        float v[4] = {bv[0], bv[1], bv[2], bv[3]}, u[4] = {bu[0], bu[1], bu[2], bu[3]};
+        const float* from = part + i * LD + cc;
+#pragma unroll 2
+        for (int s = 0; s < p.splits; ++s, from += per * LD) {
+            spl_sum4<VEC>(from, STEP, v);
+            if (GLU) spl_sum4<VEC>(from + W, STEP, u);
+        }
+        if (p.z) {
+            spl_store4<VEC>(p.z + grow * p.N + col0, STEP, left, v);
+            if (GLU) spl_store4<VEC>(p.z + grow * p.N + p.cols + col0, STEP, left, u);
+        }
+        if (GLU) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] *= sigmoidf(v[j]) * u[j];
+        } else {
+            act_all<4>(p.act, v);
+        }
+        if (p.res) spl_add4<VEC>(res + i * W + cc, STEP, left, v);
+        spl_store4<VEC>(p.out + grow * p.ldo + col0, STEP, left, v);
+    }
+}
+
+// One 128 x BN tile per cluster of `splits` CTAs (a power of two), each over its share of the k steps.
 // Row i of a CTA's partial tile goes through distributed shared memory to CTA i % splits, which adds
 // that row's partials in rank order and finishes it.  For products of so few tiles that whole tiles
-// would leave most SMs idle while the weights stream through the rest.  Rows are sent, not fetched: a
+// would leave most SMs idle while the operands stream through the rest.  Rows are sent, not fetched: a
 // store needs no answer, and nothing is read across CTAs after the one barrier (fetching cost 3 us a
-// launch).  The finish is a short loop: code that runs once is bound by fetching its instructions.
-template <bool GLU>
+// launch).  The finish is a short loop: code that runs once is bound by fetching its instructions.  The
+// residual of the finished rows is brought into shared memory while the products run.
+template <bool GLU, int BN, bool VEC>
 __global__ void __launch_bounds__(kSplThreads) linear_split_kernel(const __grid_constant__ LinSplitParams p)
 {
+    constexpr uint32_t kSplStage = spl_stage(BN);
+    constexpr int LD = spl_ld(BN), W = GLU ? BN / 2 : BN;
     const uint32_t S = p.stages;
     extern __shared__ uint8_t lin_dyn[];
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -712,13 +772,15 @@ __global__ void __launch_bounds__(kSplThreads) linear_split_kernel(const __grid_
     uint8_t* sm = lin_dyn + ((1024u - (base0 & 1023u)) & 1023u);
     const uint32_t ring = tc_saddr(sm);
     float* part = reinterpret_cast<float*>(sm + S * kSplStage);
-    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S * kSplStage + kSplPart);
+    uint16_t* res = reinterpret_cast<uint16_t*>(sm + S * kSplStage + spl_part(BN));   // [128 / splits][W]
+    uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S * kSplStage + spl_part(BN) + p.res_bytes);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 1);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const uint32_t bar0 = tc_saddr(bars);
     auto full = [&](uint32_t s) { return bar0 + 8u * s; };
     auto empty = [&](uint32_t s) { return bar0 + 8u * (S + s); };
     const uint32_t accfull = bar0 + 8u * 2 * S;
+    const int rows = min(128, p.M - m0), lg = 31 - __clz(p.splits), per = 128 >> lg;
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // this CTA runs: its memory may be written
     if (tid <= 2 * (int)S) {
         tc_mbar_init(bar0 + 8u * tid, 1);
@@ -727,7 +789,7 @@ __global__ void __launch_bounds__(kSplThreads) linear_split_kernel(const __grid_
     if (tid == 32) *abort = 0;
     if (tid >= 96 && tid < 98) prefetch_tensormap(tid == 96 ? &p.ta : &p.tb);
     if (warp == 2) {
-        tc_alloc(tc_saddr(tmem_slot), kSplN);
+        tc_alloc(tc_saddr(tmem_slot), BN);
         tc_relinquish();
     }
     tc_fence_before();
@@ -737,7 +799,7 @@ __global__ void __launch_bounds__(kSplThreads) linear_split_kernel(const __grid_
     griddep_wait();
     griddep_launch();
     if (warp == 0) {
-        const int n0 = GLU ? tn * 32 : tn * 64, n1 = GLU ? n0 + p.cols : n0 + 32;
+        const int n0 = tn * W, n1 = GLU ? n0 + p.cols : n0 + BN / 2;
         RingPos ri;
         uint32_t i = 0;
         for (int k = k0; k < k1; ++k, ++i, ri.next(S)) {
@@ -751,13 +813,13 @@ __global__ void __launch_bounds__(kSplThreads) linear_split_kernel(const __grid_
                 const uint32_t a = ring + s * kSplStage, b = a + 128 * 128;
                 tma_load_2d(a, &p.ta, 64 * k, m0, full(s));
                 tma_load_2d(b, &p.tb, 64 * k, n0, full(s));
-                tma_load_2d(b + 32 * 128, &p.tb, 64 * k, n1, full(s));
+                tma_load_2d(b + BN / 2 * 128, &p.tb, 64 * k, n1, full(s));
             }
             __syncwarp();
         }
         for (uint32_t j = i > S ? i - S : 0; j < i; ++j) lin_wait_warp(full(j % S), (j / S) & 1);
     } else if (warp == 1) {
-        const uint32_t idesc = lin_idesc(0, 0, 128, kSplN);
+        const uint32_t idesc = lin_idesc(0, 0, 128, BN);
         const uint64_t a0 = tc_smem_desc(ring), b0 = tc_smem_desc(ring + 128 * 128);
         RingPos ri;
         for (int k = k0; k < k1; ++k, ri.next(S)) {
@@ -779,18 +841,36 @@ __global__ void __launch_bounds__(kSplThreads) linear_split_kernel(const __grid_
         if (elect_one()) tc_commit(accfull);
         __syncwarp();
         if (!lin_wait_warp(accfull, 0)) *abort = 1;
+    } else if (warp >= 4 && p.res) {
+        const int left = min(W, p.cols - tn * W);   // this tile's columns
+        const uint16_t* src = p.res + (size_t)m0 * p.ldr + tn * W;
+        if (p.vec_res) {
+            constexpr int C = W / 8;
+#pragma unroll 4
+            for (int i = tid - 128; i < per * C; i += 128) {
+                const int row = ((i / C) << lg) + rank, c = 8 * (i % C);
+                if (row < rows && c < left)
+                    *reinterpret_cast<uint4*>(res + 8 * i) = *reinterpret_cast<const uint4*>(src + (size_t)row * p.ldr + c);
+            }
+        } else {
+#pragma unroll 8
+            for (int i = tid - 128; i < per * W; i += 128) {
+                const int row = ((i / W) << lg) + rank, c = i % W;
+                if (row < rows && c < left) res[i] = src[(size_t)row * p.ldr + c];
+            }
+        }
     }
     __syncthreads();   // the products are done
     tc_fence_after();
-    const int rows = min(128, p.M - m0), lg = 31 - __clz(p.splits), per = 128 >> lg;
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // every CTA of the cluster runs
-    {
-        const int row = 32 * (warp & 3) + lane, c = 32 * (warp >> 2);
+#pragma unroll
+    for (int h = 0; h < BN / 64; ++h) {
+        const int row = 32 * (warp & 3) + lane, c = 32 * (warp >> 2) + 64 * h;
         uint32_t r[32];
         tc_ld32(tmem + ((uint32_t)(32 * (warp & 3)) << 16) + c, r);
         tc_wait_ld();
         if (row < rows) {
-            const uint32_t to = cluster_map(tc_saddr(part + (rank * per + (row >> lg)) * kSplLd + c), row & (p.splits - 1));
+            const uint32_t to = cluster_map(tc_saddr(part + (rank * per + (row >> lg)) * LD + c), row & (p.splits - 1));
 #pragma unroll
             for (int q = 0; q < 8; ++q)
                 asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + 16 * q), "r"(r[4 * q]),
@@ -802,50 +882,9 @@ __global__ void __launch_bounds__(kSplThreads) linear_split_kernel(const __grid_
     cluster_sync();
     if (warp == 2) {
         tc_fence_after();
-        tc_dealloc(tmem, kSplN);
+        tc_dealloc(tmem, BN);
     }
-    constexpr int TPR = GLU ? 8 : 16;   // threads per row, four columns each
-    const int cc = 4 * (tid % TPR), col0 = tn * (GLU ? 32 : 64) + cc, left = p.cols - col0;
-    if (left > 0) {
-        // a thread's columns are the same in every row: the bias once; a row's residual is asked for before
-        // its partials are added
-        float bv[4] = {0, 0, 0, 0}, bu[4] = {0, 0, 0, 0};
-        if (p.bias) {
-            spl_add4(p.bias + col0, left, bv);
-            if (GLU) spl_add4(p.bias + p.cols + col0, left, bu);
-        }
-#pragma unroll 2
-        for (int i = tid / TPR; i < per; i += kSplThreads / TPR) {
-            const int row = (i << lg) + rank;
-            if (row >= rows) break;
-            const size_t grow = (size_t)(m0 + row);
-            float v[4] = {bv[0], bv[1], bv[2], bv[3]}, u[4] = {bu[0], bu[1], bu[2], bu[3]}, add[4] = {0, 0, 0, 0};
-            if (p.res) spl_add4(p.res + grow * p.ldr + col0, left, add);
-            const float* from = part + i * kSplLd + cc;
-#pragma unroll 2
-            for (int s = 0; s < p.splits; ++s, from += per * kSplLd) {
-                const float4 q = *reinterpret_cast<const float4*>(from);
-                v[0] += q.x; v[1] += q.y; v[2] += q.z; v[3] += q.w;
-                if (GLU) {
-                    const float4 w = *reinterpret_cast<const float4*>(from + 32);
-                    u[0] += w.x; u[1] += w.y; u[2] += w.z; u[3] += w.w;
-                }
-            }
-            if (p.z) {
-                spl_store4(p.z + grow * p.N + col0, left, v);
-                if (GLU) spl_store4(p.z + grow * p.N + p.cols + col0, left, u);
-            }
-            if (GLU) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] *= sigmoidf(v[j]) * u[j];
-            } else {
-                act_all<4>(p.act, v);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] += add[j];
-            spl_store4(p.out + grow * p.ldo + col0, left, v);
-        }
-    }
+    spl_finish<GLU, BN, VEC>(p, part, res, m0, tn, rows, rank);
     if (tid == 0 && *abort) atomicOr(&g_op_status, kDevTcTimeout);
 }
 
@@ -876,8 +915,9 @@ FE_DEV void fma8(const uint4& a, const uint4& b, float& acc)
 
 constexpr int kLinRowsWarps = 4;
 
-// A warp per output column (two weight rows for swiglu), MR rows of x (used for one).
-template <int MR, bool GLU>
+// One row of x: a warp per output column (two weight rows for swiglu).  A second row's loads would take the
+// registers that keep this one's weights in flight; from two rows on the kernel below is faster.
+template <bool GLU>
 __global__ void __launch_bounds__(32 * kLinRowsWarps) linear_rows_kernel(LinRowsParams p)
 {
     griddep_wait();
@@ -887,39 +927,30 @@ __global__ void __launch_bounds__(32 * kLinRowsWarps) linear_rows_kernel(LinRows
     if (c >= p.cols) return;
     const uint16_t* w0 = p.w + (size_t)c * p.K;
     const uint16_t* w1 = p.w + (size_t)(c + p.cols) * p.K;   // read for swiglu only
-    float acc[2][MR];
-#pragma unroll
-    for (int m = 0; m < MR; ++m) acc[0][m] = acc[1][m] = 0.0f;
+    float z0 = 0.0f, z1 = 0.0f;
 #pragma unroll 4
     for (int k = 8 * lane; k < p.K; k += 256) {
         const uint4 a = ldg_stream(w0 + k);
         uint4 b = make_uint4(0, 0, 0, 0);
         if (GLU) b = ldg_stream(w1 + k);
-#pragma unroll
-        for (int m = 0; m < MR; ++m) {
-            if (m >= p.M) break;
-            const uint4 x = __ldg(reinterpret_cast<const uint4*>(p.x + (size_t)m * p.ldx + k));
-            fma8(a, x, acc[0][m]);
-            if (GLU) fma8(b, x, acc[1][m]);
-        }
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(p.x + k));
+        fma8(a, x, z0);
+        if (GLU) fma8(b, x, z1);
     }
-#pragma unroll
-    for (int m = 0; m < MR; ++m) {
-        if (m >= p.M) break;
-        float z0 = warp_sum(acc[0][m]), z1 = GLU ? warp_sum(acc[1][m]) : 0.0f;
-        if (lane != 0) continue;
-        if (p.bias) {
-            z0 += bf16_bits_to_f32(p.bias[c]);
-            if (GLU) z1 += bf16_bits_to_f32(p.bias[c + p.cols]);
-        }
-        if (p.z) {
-            p.z[(size_t)m * p.N + c] = (uint16_t)(bf16x2_rn(z0, 0.0f) & 0xffffu);
-            if (GLU) p.z[(size_t)m * p.N + c + p.cols] = (uint16_t)(bf16x2_rn(z1, 0.0f) & 0xffffu);
-        }
-        float v = GLU ? z0 * sigmoidf(z0) * z1 : act_fwd(p.act, z0);
-        if (p.res) v += bf16_bits_to_f32(p.res[(size_t)m * p.ldr + c]);
-        p.y[(size_t)m * p.ldy + c] = (uint16_t)(bf16x2_rn(v, 0.0f) & 0xffffu);
+    z0 = warp_sum(z0);
+    if (GLU) z1 = warp_sum(z1);
+    if (lane != 0) return;
+    if (p.bias) {
+        z0 += bf16_bits_to_f32(p.bias[c]);
+        if (GLU) z1 += bf16_bits_to_f32(p.bias[c + p.cols]);
     }
+    if (p.z) {
+        p.z[c] = (uint16_t)(bf16x2_rn(z0, 0.0f) & 0xffffu);
+        if (GLU) p.z[c + p.cols] = (uint16_t)(bf16x2_rn(z1, 0.0f) & 0xffffu);
+    }
+    float v = GLU ? z0 * sigmoidf(z0) * z1 : act_fwd(p.act, z0);
+    if (p.res) v += bf16_bits_to_f32(p.res[c]);
+    p.y[c] = (uint16_t)(bf16x2_rn(v, 0.0f) & 0xffffu);
 }
 
 // ---- a small batch ---------------------------------------------------------------------
