@@ -671,10 +671,11 @@ cudaError_t split_room(int lg, int* clusters)
 }
 
 // CTAs that share a tile's contraction (a power of two, to 8) and the tile's columns: of those whose
-// clusters all run at once, with two k steps or more a CTA, the least that an SM has to take in, its k
-// steps' operands and its share of the other CTAs' partial sums, which is what bounds these products (64
-// bytes a clock).  1024 x 1000 at K = 2048: 10.6 us with 64 columns and no split, 9.6 us with 128 and two
-// CTAs.  0 if the tiles alone fill the SMs.
+// clusters all run at once, with two k steps or more a CTA, the least that an SM has to take in, which is
+// what bounds these products: its k steps' operands at 72 bytes a clock (measured), and its share of the
+// other CTAs' partial sums, which cross between SMs at a fifth of that.  1024 x 1000, K = 2048: 9.5 us with
+// 128 columns and two CTAs, 10.6 us with 64 and no split; 256 x 2048, K = 768: 5.6 us with 64 columns and
+// two, 7.6 us with 128 and four.  0 if the tiles alone fill the SMs.
 cudaError_t split_ways(const fe::LinProblem& q, const Product& f, int* ways, int* BN)
 {
     *ways = 0;
@@ -689,7 +690,8 @@ cudaError_t split_ways(const fe::LinProblem& q, const Product& f, int* ways, int
             const cudaError_t e = split_room(lg, &room);
             if (e != cudaSuccess) return e;
             if (tiles > room || (lg > 0 && steps < 2 * n)) break;
-            const int64_t cost = (int64_t)((steps + n - 1) / n) * fe::spl_stage(bn) + 512 * bn / n * (n - 1);
+            const int rows = std::min(f.M, 128);
+            const int64_t cost = (int64_t)((steps + n - 1) / n) * 128 * (rows + bn) + 5 * 4 * bn * rows / n * (n - 1);
             if (cost < least) {
                 least = cost;
                 *ways = n;

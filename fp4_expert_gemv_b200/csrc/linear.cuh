@@ -708,11 +708,12 @@ FE_DEV void spl_sum4(const float* s, int step, float (&v)[4])
     }
 }
 
-// The rows that a CTA of the cluster finishes: their partials added in rank order, then the epilogue.
+// The rows that a CTA of the cluster finishes: their partials added in rank order, then the epilogue, several rows
+// of a thread at a time so that their loads do not wait for each other's stores.
 template <bool GLU, int BN, bool VEC>
 FE_DEV void spl_finish(const LinSplitParams& p, const float* part, const uint16_t* res, int m0, int tn, int rows, int rank)
 {
-    constexpr int W = GLU ? BN / 2 : BN, TPR = W / 4, LD = spl_ld(BN), STEP = VEC ? 1 : TPR;
+    constexpr int W = GLU ? BN / 2 : BN, TPR = W / 4, LD = spl_ld(BN), STEP = VEC ? 1 : TPR, R = BN / 32, ROWS = kSplThreads / TPR;
     const int tid = threadIdx.x, lg = 31 - __clz(p.splits), per = 128 >> lg;
     const int cc = (VEC ? 4 : 1) * (tid % TPR), col0 = tn * W + cc, left = p.cols - col0;
     if (left <= 0) return;
@@ -722,30 +723,43 @@ FE_DEV void spl_finish(const LinSplitParams& p, const float* part, const uint16_
         spl_add4<false>(p.bias + col0, STEP, left, bv);
         if (GLU) spl_add4<false>(p.bias + p.cols + col0, STEP, left, bu);
     }
-#pragma unroll 2
-    for (int i = tid / TPR; i < per; i += kSplThreads / TPR) {
-        const int row = (i << lg) + rank;
-        if (row >= rows) break;
-        const size_t grow = (size_t)(m0 + row);
-        float v[4] = {bv[0], bv[1], bv[2], bv[3]}, u[4] = {bu[0], bu[1], bu[2], bu[3]};
-        const float* from = part + i * LD + cc;
-#pragma unroll 2
-        for (int s = 0; s < p.splits; ++s, from += per * LD) {
-            spl_sum4<VEC>(from, STEP, v);
-            if (GLU) spl_sum4<VEC>(from + W, STEP, u);
-        }
-        if (p.z) {
-            spl_store4<VEC>(p.z + grow * p.N + col0, STEP, left, v);
-            if (GLU) spl_store4<VEC>(p.z + grow * p.N + p.cols + col0, STEP, left, u);
-        }
-        if (GLU) {
+#pragma unroll 1
+    for (int i0 = tid / TPR; i0 < per && (i0 << lg) + rank < rows; i0 += R * ROWS) {
+        float v[R][4], u[R][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] *= sigmoidf(v[j]) * u[j];
-        } else {
-            act_all<4>(p.act, v);
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[r][j] = bv[j];
+                u[r][j] = bu[j];
+            }
+#pragma unroll 1
+        for (int s = 0; s < p.splits; ++s) {
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const float* from = part + (s * per + min(i0 + r * ROWS, per - 1)) * LD + cc;
+                spl_sum4<VEC>(from, STEP, v[r]);
+                if (GLU) spl_sum4<VEC>(from + W, STEP, u[r]);
+            }
         }
-        if (p.res) spl_add4<VEC>(res + i * W + cc, STEP, left, v);
-        spl_store4<VEC>(p.out + grow * p.ldo + col0, STEP, left, v);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int i = i0 + r * ROWS, row = (i << lg) + rank;
+            if (i >= per || row >= rows) break;
+            const size_t grow = (size_t)(m0 + row);
+            if (p.z) {
+                spl_store4<VEC>(p.z + grow * p.N + col0, STEP, left, v[r]);
+                if (GLU) spl_store4<VEC>(p.z + grow * p.N + p.cols + col0, STEP, left, u[r]);
+            }
+            if (GLU) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[r][j] *= sigmoidf(v[r][j]) * u[r][j];
+            } else {
+                act_all<4>(p.act, v[r]);
+            }
+            if (p.res) spl_add4<VEC>(res + i * W + cc, STEP, left, v[r]);
+            spl_store4<VEC>(p.out + grow * p.ldo + col0, STEP, left, v[r]);
+        }
     }
 }
 
