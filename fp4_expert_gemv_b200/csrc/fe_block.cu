@@ -242,7 +242,7 @@ cudaError_t norm_bwd_any(const fe::NormBwdParams& q, bool vec, int sms, int* par
         if (e != cudaSuccess) return e;
         return launch(kernel, b.grid, b.threads, b.smem, s, q, b.tpr, b.stages);
     }
-    const bool all = q.f.y && q.f.w_post && q.du && q.dr_out;
+    const bool all = q.f.y && q.f.w_post && q.du && q.dr_out && q.dr && q.dy && (GATE != fe::kByElement || q.dgate);
     return all ? norm_bwd_columns<R32, GATE, true>(q, sms, partials, s) : norm_bwd_columns<R32, GATE, false>(q, sms, partials, s);
 }
 

@@ -880,13 +880,26 @@ __global__ void __launch_bounds__(512) block_norm_backward_ring_kernel(NormBwdPa
 }
 
 // A row's columns one at a time, t, t + tpr, ...: any width, alignment and set of operands.  The same sums and
-// the same two walks, over memory (the second finds the row in L1); the sums over rows lie in shared
-// memory, where each column has one thread per group.
+// the same two walks, over memory, four columns of a thread at a time; the second walk goes backwards, so
+// that the four it begins with are still held in registers (a whole row of up to 2048 columns), and the
+// rest of the row is found in L1.  The next row is asked for into L2 while this one is summed.  What bounds
+// it is issuing instructions, two bytes a load: a warp's columns lie 32 apart, so that one address serves
+// four of them (columns a row's threads apart took a third more time), and a batch within the row checks no
+// ends.  16384 x 1999 with a full gate takes 229 us, 1.7 TB/s; 1237 x 1999 29.9 us.  The sums over rows lie in
+// shared memory, where each column has one thread per group.
 template <typename OT>
 FE_DEV float any_get(const OT* p, size_t i)
 {
     if constexpr (std::is_same<OT, float>::value) return p[i];
     else return bf16_bits_to_f32(p[i]);
+}
+
+// Asks for `bytes` from p into L2, a 128-byte line per thread of the group.
+FE_DEV void any_prefetch(const void* p, size_t bytes, int t, int tpr)
+{
+    if (!p) return;
+    const char* b = static_cast<const char*>(p);
+    for (size_t o = (size_t)t * 128; o < bytes; o += (size_t)tpr * 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(b + o));
 }
 
 template <bool R32, int GATE, bool ALL>
@@ -897,7 +910,7 @@ __global__ void __launch_bounds__(512, 2) block_norm_backward_any_kernel(NormBwd
     const NormParams& p = q.f;
     const int t = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = blockDim.x / tpr;
     const int H = p.H;
-    // ALL: every operand is there
+    // ALL: every operand and output is there
     const bool has_y = ALL || p.y != nullptr, has_du = ALL || q.du != nullptr, has_dr = ALL || q.dr_out != nullptr;
     const bool token = p.gate_kind == kGateToken, w_post = ALL || p.w_post != nullptr, sig = p.gate_sigmoid != 0;
     // [groups] reduction halves, then [groups][2][H] sums over rows: of e (times the row's or element's
@@ -915,6 +928,9 @@ __global__ void __launch_bounds__(512, 2) block_norm_backward_any_kernel(NormBwd
     const RT* pdr = static_cast<const RT*>(q.dr_out);
     const int64_t step = (int64_t)gridDim.x * groups, first = (int64_t)blockIdx.x * groups + group;
     const float inv_h = 1.0f / (float)H;
+    // a warp has the 32 U columns from U times its place, a thread U of them, 32 apart
+    constexpr int U = 4;
+    const int col0 = U * (t & ~31) + (t & 31);
     int half = 0;
     for (int64_t row = first; row < p.T; row += step) {
         const size_t at = (size_t)row * H;
@@ -926,6 +942,14 @@ __global__ void __launch_bounds__(512, 2) block_norm_backward_any_kernel(NormBwd
                 d1 = g1 * (1.0f - g1);
             }
         }
+        if (row + step < p.T) {
+            const size_t next = (size_t)(row + step) * H;
+            any_prefetch(pr + next, sizeof(RT) * H, t, tpr);
+            if (has_dr) any_prefetch(pdr + next, sizeof(RT) * H, t, tpr);
+            if (has_y) any_prefetch(p.y + next, 2 * H, t, tpr);
+            if (has_du) any_prefetch(q.du + next, 2 * H, t, tpr);
+            if (GATE == kByElement) any_prefetch(p.gate + next, 2 * H, t, tpr);
+        }
         // the gate of column e and scale w_post (a row gate stays out of both)
         auto gate_at = [&](int e) {
             if (GATE == kByRow) return 1.0f;
@@ -936,18 +960,55 @@ __global__ void __launch_bounds__(512, 2) block_norm_backward_any_kernel(NormBwd
         auto x_at = [&](int e) { return has_du ? bf16_bits_to_f32(q.du[at + e]) * bf16_bits_to_f32(p.w_pre[e]) : 0.0f; };
         auto y_at = [&](int e) { return has_y ? bf16_bits_to_f32(p.y[at + e]) : 0.0f; };
         auto d_at = [&](int e) { return has_dr ? any_get(pdr, at + e) : 0.0f; };
+        // columns e0, e0 + 32, ... of the row: one address per operand; IN: all of them are in the row
+        float y[U], r[U], du[U], d[U], ga[U];
+        auto load = [&](auto in, int e0) {
+            constexpr bool IN = decltype(in)::value;
+            const uint16_t *py = p.y + at + e0, *pu = q.du + at + e0, *pg = p.gate + (GATE == kByElement ? at + e0 : (size_t)e0);
+            const RT *prr = pr + at + e0, *pd = pdr + at + e0;
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                if (!IN && e0 + 32 * j >= H) break;
+                y[j] = has_y ? bf16_bits_to_f32(py[32 * j]) : 0.0f;
+                r[j] = any_get(prr, 32 * j);
+                du[j] = has_du ? bf16_bits_to_f32(pu[32 * j]) : 0.0f;
+                d[j] = has_dr ? any_get(pd, 32 * j) : 0.0f;
+                if (GATE != kByRow) ga[j] = bf16_bits_to_f32(pg[32 * j]);
+            }
+            if (GATE != kByRow && sig) {
+#pragma unroll
+                for (int j = 0; j < U; ++j) {
+                    if (!IN && e0 + 32 * j >= H) break;
+                    ga[j] = sigmoidf(ga[j]);
+                }
+            }
+        };
         float sum[7] = {0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 4
-        for (int e = t; e < H; e += tpr) {
-            const float y = y_at(e), r = any_get(pr, at + e), x = x_at(e), d = d_at(e);
-            const float f = cw_at(e) * gate_at(e) * y;
-            sum[0] = fmaf(y, y, sum[0]);
-            sum[1] = fmaf(r, r, sum[1]);
-            sum[2] = fmaf(r, f, sum[2]);
-            sum[3] = fmaf(f, f, sum[3]);
-            sum[4] = fmaf(x, r, sum[4]);
-            sum[5] = fmaf(x, f, sum[5]);
-            sum[6] = fmaf(d, f, sum[6]);
+        auto add = [&](auto in, int e0) {
+            constexpr bool IN = decltype(in)::value;
+            load(in, e0);
+            const uint16_t *pw = p.w_post + e0, *pq = p.w_pre + e0;
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                if (!IN && e0 + 32 * j >= H) break;
+                float f = p.scale * y[j];
+                if (w_post) f *= bf16_bits_to_f32(pw[32 * j]);
+                if (GATE != kByRow) f *= ga[j];
+                const float x = has_du ? du[j] * bf16_bits_to_f32(pq[32 * j]) : 0.0f;
+                sum[0] = fmaf(y[j], y[j], sum[0]);
+                sum[1] = fmaf(r[j], r[j], sum[1]);
+                sum[2] = fmaf(r[j], f, sum[2]);
+                sum[3] = fmaf(f, f, sum[3]);
+                sum[4] = fmaf(x, r[j], sum[4]);
+                sum[5] = fmaf(x, f, sum[5]);
+                sum[6] = fmaf(d[j], f, sum[6]);
+            }
+        };
+        int e0 = col0;
+        for (;; e0 += U * tpr) {
+            if (e0 + 32 * (U - 1) < H) add(std::true_type{}, e0);
+            else add(std::false_type{}, e0);
+            if (e0 - col0 + U * tpr >= H) break;
         }
         ring_sum<7>(sum, group, tpr, red + half * norm_red_floats(tpr));
         half ^= 1;
@@ -986,22 +1047,40 @@ __global__ void __launch_bounds__(512, 2) block_norm_backward_any_kernel(NormBwd
         }
         if (token && q.dgate && t == 0) static_cast<float*>(q.dgate)[row] = sdg * d1;
         const float kd = w_post ? sdg * g1 * inv_h : 0.0f;
-#pragma unroll 4
-        for (int e = t; e < H; e += tpr) {
-            const float m = rho_y * y_at(e), a = gate_at(e), cw = cw_at(e), f = cw * a * g1;
-            const float r = fmaf(f, m, any_get(pr, at + e));   // r'
-            const float u = has_du ? bf16_bits_to_f32(q.du[at + e]) * rho : 0.0f;
-            const float D = d_at(e) + (has_du ? u * bf16_bits_to_f32(p.w_pre[e]) : 0.0f) - rk * r;
-            if (has_du) gw_pre[e] = fmaf(u, r, gw_pre[e]);
-            if (q.dr) {
-                if constexpr (R32) static_cast<float*>(q.dr)[at + e] = D;
-                else static_cast<uint16_t*>(q.dr)[at + e] = (uint16_t)(bf16x2_rn(D, 0.0f) & 0xffffu);
+        auto write = [&](auto in, int e0) {
+            constexpr bool IN = decltype(in)::value;
+            const uint16_t *pw = p.w_post + e0, *pq = p.w_pre + e0;
+            RT* odr = static_cast<RT*>(q.dr) + at + e0;
+            uint16_t *ody = q.dy + at + e0, *odg = static_cast<uint16_t*>(q.dgate) + at + e0;
+            float *sE = E + e0, *sw = gw_pre + e0;
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                if (!IN && e0 + 32 * j >= H) break;
+                const float m = rho_y * y[j], a = GATE == kByRow ? 1.0f : ga[j];
+                const float cw = p.scale * (w_post ? bf16_bits_to_f32(pw[32 * j]) : 1.0f), f = cw * a * g1;
+                const float ro = fmaf(f, m, r[j]);   // r'
+                const float u = du[j] * rho;
+                const float D = d[j] + (has_du ? u * bf16_bits_to_f32(pq[32 * j]) : 0.0f) - rk * ro;
+                if (has_du) sw[32 * j] = fmaf(u, ro, sw[32 * j]);
+                if (ALL || q.dr) {
+                    if constexpr (R32) odr[32 * j] = D;
+                    else odr[32 * j] = (uint16_t)(bf16x2_rn(D, 0.0f) & 0xffffu);
+                }
+                const float em = D * m;
+                sE[32 * j] = fmaf(GATE == kByRow ? g1 : GATE == kByElement ? a : 1.0f, em, sE[32 * j]);
+                if (GATE == kByElement && (ALL || q.dgate))
+                    odg[32 * j] = (uint16_t)(bf16x2_rn(cw * em * (sig ? a * (1.0f - a) : 1.0f), 0.0f) & 0xffffu);
+                if (ALL || q.dy) ody[32 * j] = (uint16_t)(bf16x2_rn(rho_y * (D * f - kd * m), 0.0f) & 0xffffu);
             }
-            const float em = D * m;
-            E[e] = fmaf(GATE == kByRow ? g1 : GATE == kByElement ? a : 1.0f, em, E[e]);
-            if (GATE == kByElement && q.dgate)
-                static_cast<uint16_t*>(q.dgate)[at + e] = (uint16_t)(bf16x2_rn(cw * em * (sig ? a * (1.0f - a) : 1.0f), 0.0f) & 0xffffu);
-            if (q.dy) q.dy[at + e] = (uint16_t)(bf16x2_rn(rho_y * (D * f - kd * m), 0.0f) & 0xffffu);
+        };
+        for (bool held = true; e0 >= 0; e0 -= U * tpr, held = false) {
+            if (e0 + 32 * (U - 1) < H) {
+                if (!held) load(std::true_type{}, e0);
+                write(std::true_type{}, e0);
+            } else {
+                if (!held) load(std::false_type{}, e0);
+                write(std::false_type{}, e0);
+            }
         }
     }
     if (!q.part) return;
