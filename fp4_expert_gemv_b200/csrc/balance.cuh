@@ -103,23 +103,28 @@ FE_DEV void bal_softmax(float (&l)[N], float& inv, float& lse)
 FE_DEV void bal_finish(const BalanceParams& p, float* sums, int* n, uint32_t rank, int ranks)
 {
     cluster_sync();
-    if (rank == 0 && threadIdx.x == 0) {
-        float d = 0.0f, z = 0.0f;
+    if (rank == 0 && threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        float ds = 0.0f, zs = 0.0f;
         int nn = 0;
-        const uint32_t fa = (uint32_t)__cvta_generic_to_shared(sums), na = (uint32_t)__cvta_generic_to_shared(n);
-        for (int s = 0; s < ranks; ++s) {
-            d += ld_cluster_f32(cluster_map(fa, s));
-            z += ld_cluster_f32(cluster_map(fa + 4, s));
-            nn += ld_cluster_s32(cluster_map(na, s));
+        if (lane < ranks) {   // a rank per lane
+            const uint32_t fa = cluster_map((uint32_t)__cvta_generic_to_shared(sums), lane);
+            ds = ld_cluster_f32(fa);
+            zs = ld_cluster_f32(fa + 4);
+            nn = ld_cluster_s32(cluster_map((uint32_t)__cvta_generic_to_shared(n), lane));
         }
-        const float fn = (float)max(nn, 1);
-        const float bal = (float)p.E * (d / (fn * (float)p.k)) / fn;
-        const float zz = z / fn;
-        // a part without a coefficient adds nothing, even where it overflowed
-        p.loss[0] = (p.a != 0.0f ? p.a * bal : 0.0f) + (p.b != 0.0f ? p.b * zz : 0.0f);
-        p.loss[1] = bal;
-        p.loss[2] = zz;
-        p.n_tokens[0] = nn;
+        const float d = warp_sum(ds), z = warp_sum(zs);
+        nn = __reduce_add_sync(0xffffffffu, nn);
+        if (lane == 0) {
+            const float fn = (float)max(nn, 1);
+            const float bal = (float)p.E * (d / (fn * (float)p.k)) / fn;
+            const float zz = z / fn;
+            // a part without a coefficient adds nothing, even where it overflowed
+            p.loss[0] = (p.a != 0.0f ? p.a * bal : 0.0f) + (p.b != 0.0f ? p.b * zz : 0.0f);
+            p.loss[1] = bal;
+            p.loss[2] = zz;
+            p.n_tokens[0] = nn;
+        }
     }
     cluster_sync();   // the others' shared memory is read until here
 }
@@ -135,6 +140,34 @@ FE_DEV float bal_block_sum(float v, float* scratch)
     if (threadIdx.x == 0)
         for (int w = 0; w < (int)blockDim.x / 32; ++w) s += scratch[w];
     return s;
+}
+
+// One cluster is the grid: its CTAs' sums (mine: of p, cnt: counts, zz, nn: of lse^2 and kept tokens, in thread
+// 0) join, each CTA finishing a share of the experts.
+FE_DEV void bal_join(const BalanceParams& p, float* mine, int* cnt, float zz, int nn, float* scratch, float* sums, int* n_all)
+{
+    cluster_sync();
+    const uint32_t rank = cluster_rank();
+    const int ranks = gridDim.x;
+    float dot = 0.0f;
+    for (int e = rank * blockDim.x + threadIdx.x; e < p.E; e += ranks * blockDim.x) {
+        const uint32_t fa = (uint32_t)__cvta_generic_to_shared(mine + e), ia = (uint32_t)__cvta_generic_to_shared(cnt + e);
+        float v = 0.0f;
+        int c = 0;
+        for (int s = 0; s < ranks; ++s) {
+            v += ld_cluster_f32(cluster_map(fa, s));
+            c += ld_cluster_s32(cluster_map(ia, s));
+        }
+        p.counts[e] = c;
+        dot += (float)c * v;
+    }
+    dot = bal_block_sum(dot, scratch);
+    if (threadIdx.x == 0) {
+        sums[0] = dot;
+        sums[1] = zz;
+        *n_all = nn;
+    }
+    bal_finish(p, sums, n_all, rank, ranks);
 }
 
 // A warp takes every so many-th group of 32 / L rows, with the next group's loads under way; per lane the
@@ -219,35 +252,14 @@ __global__ void __launch_bounds__(kBalThreads, N == 16 ? 3 : 1) balance_kernel(B
         }
         return;
     }
-    cluster_sync();
-    const uint32_t rank = cluster_rank();
-    const int ranks = gridDim.x;
-    float dot = 0.0f;
-    for (int e = rank * (32 * W) + threadIdx.x; e < p.E; e += ranks * 32 * W) {
-        const uint32_t fa = (uint32_t)__cvta_generic_to_shared(mine + e), ia = (uint32_t)__cvta_generic_to_shared(cnt + e);
-        float v = 0.0f;
-        int c = 0;
-        for (int s = 0; s < ranks; ++s) {
-            v += ld_cluster_f32(cluster_map(fa, s));
-            c += ld_cluster_s32(cluster_map(ia, s));
-        }
-        p.counts[e] = c;
-        dot += (float)c * v;
-    }
-    dot = bal_block_sum(dot, scratch);
-    if (threadIdx.x == 0) {
-        sums[0] = dot;
-        sums[1] = zz;
-        n_all = nn;
-    }
-    bal_finish(p, sums, &n_all, rank, ranks);
+    bal_join(p, mine, cnt, zz, nn, scratch, sums, &n_all);
 }
 
 // The first pass over many rows: as balance_kernel leaves its partials, but every warp's groups of rows stream
 // through its own ring in shared memory (one cp.async.bulk per group: its rows are neighbours), so
 // that the loads of several groups are under way per warp while its chain of shuffles and exponentials
-// runs (T = 65536, E = 512: 38 us with one group ahead in registers).  Padded rows travel too and
-// are left out.  A CTA per SM.
+// runs.  Padded rows travel too and are left out.  A CTA per SM, or one cluster for all of a batch of a few
+// groups per warp (p.G = 0).
 constexpr int kBalRingSmem = 224 * 1024;
 constexpr int kBalRingStages = 8;   // at most
 
@@ -260,7 +272,8 @@ __global__ void __launch_bounds__(32 * bal_ring_warps(N)) balance_ring_kernel(Ba
     extern __shared__ __align__(128) uint8_t bal_dyn[];
     __shared__ int cnt[L * N];
     __shared__ float scratch[32];
-    __shared__ int ns[32];
+    __shared__ float sums[2];
+    __shared__ int ns[32], n_all;
     __shared__ uint64_t bars[W * kBalRingStages];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int r = lane % L, sub = lane / L;
@@ -350,16 +363,23 @@ __global__ void __launch_bounds__(32 * bal_ring_warps(N)) balance_ring_kernel(Ba
     n = __reduce_add_sync(0xffffffffu, n);
     if (lane == 0) ns[warp] = n;
     __syncthreads();
+    int nn = 0;
+    if (threadIdx.x == 0)
+        for (int w = 0; w < W; ++w) nn += ns[w];
     for (int e = threadIdx.x; e < p.E; e += 32 * W) {
         float v = 0.0f;
 #pragma unroll 8
         for (int w = 0; w < W; ++w) v += ps[w][e];
-        p.part[(size_t)blockIdx.x * p.E + e] = v;
-        p.ipart[(size_t)blockIdx.x * p.E + e] = cnt[e];
+        if (p.G > 0) {
+            p.part[(size_t)blockIdx.x * p.E + e] = v;
+            p.ipart[(size_t)blockIdx.x * p.E + e] = cnt[e];
+        } else {
+            ps[0][e] = v;   // column e is this thread's alone
+        }
     }
-    if (threadIdx.x == 0) {
-        int nn = 0;
-        for (int w = 0; w < W; ++w) nn += ns[w];
+    if (p.G == 0) {
+        bal_join(p, ps[0], cnt, zz, nn, scratch, sums, &n_all);
+    } else if (threadIdx.x == 0) {
         p.part[(size_t)p.G * p.E + blockIdx.x] = zz;
         p.ipart[(size_t)p.G * p.E + blockIdx.x] = nn;
     }
@@ -378,32 +398,44 @@ __global__ void __cluster_dims__(kBalCluster, 1, 1) __launch_bounds__(1024) bala
     griddep_wait();
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
     const uint32_t rank = cluster_rank();
-    float v[B];
-    int c[B];
-#pragma unroll
-    for (int b = 0; b < B; ++b) {
-        v[b] = 0.0f;
-        c[b] = 0;
-    }
-#pragma unroll 4
-    for (int g = y; g < p.G; g += 32)
-#pragma unroll
-        for (int b = 0; b < B; ++b) {
-            const int e = 32 * (rank + kBalCluster * b) + x;
-            if (e < p.E) {
-                v[b] += p.part[(size_t)g * p.E + e];
-                c[b] += p.ipart[(size_t)g * p.E + e];
-            }
+    // rank 0's first warp also joins the other sums: its loads go out before the columns'
+    float z = 0.0f;
+    int n = 0;
+    if (rank == 0 && y == 0)
+        for (int g = x; g < p.G; g += 32) {
+            z += p.part[(size_t)p.G * p.E + g];
+            n += p.ipart[(size_t)p.G * p.E + g];
         }
 #pragma unroll
     for (int b = 0; b < B; ++b) {
-        sf[b][y][x] = v[b];
-        si[b][y][x] = c[b];
+        const int e = 32 * (rank + kBalCluster * b) + x;
+        if (32 * (rank + kBalCluster * b) >= p.E) break;
+        float v = 0.0f;
+        int c = 0;
+        // 160 partials are asked for at once: one latency for a CTA an SM
+        for (int g0 = y; g0 < p.G; g0 += 32 * 5) {
+            float w[5];
+            int i[5];
+#pragma unroll
+            for (int j = 0; j < 5; ++j) {
+                const bool on = g0 + 32 * j < p.G && e < p.E;
+                w[j] = on ? p.part[(size_t)(g0 + 32 * j) * p.E + e] : 0.0f;
+                i[j] = on ? p.ipart[(size_t)(g0 + 32 * j) * p.E + e] : 0;
+            }
+#pragma unroll
+            for (int j = 0; j < 5; ++j) {
+                v += w[j];
+                c += i[j];
+            }
+        }
+        sf[b][y][x] = v;
+        si[b][y][x] = c;
     }
     __syncthreads();
     float fp = 0.0f;   // lane 0 of warp y: sum of counts * P over its experts
 #pragma unroll
     for (int b = 0; b < B; ++b) {
+        if (32 * (rank + kBalCluster * b) >= p.E) break;
         const int e = 32 * (rank + kBalCluster * b) + y;
         const float P = warp_sum(sf[b][x][y]);
         const int cs = __reduce_add_sync(0xffffffffu, si[b][x][y]);
@@ -412,13 +444,7 @@ __global__ void __cluster_dims__(kBalCluster, 1, 1) __launch_bounds__(1024) bala
             fp += (float)cs * P;
         }
     }
-    float z = 0.0f;
-    int n = 0;
     if (rank == 0 && y == 0) {
-        for (int g = x; g < p.G; g += 32) {
-            z += p.part[(size_t)p.G * p.E + g];
-            n += p.ipart[(size_t)p.G * p.E + g];
-        }
         z = warp_sum(z);
         n = __reduce_add_sync(0xffffffffu, n);
     }

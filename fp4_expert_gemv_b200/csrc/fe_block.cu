@@ -272,10 +272,16 @@ int balance_ctas(int64_t T, int E)
     return (int)std::max<int64_t>(1, std::min<int64_t>(kMaxBalanceCtas, (T + rows - 1) / rows));
 }
 
-// Whether one cluster takes the whole loss: up to four groups of rows per warp.
+// Rows that one cluster takes by itself, two groups per warp: with the rows in registers (64 x 128: 3.9 us),
+// then through the rings, which have more warps but want whole 16-byte pieces (1024 x 128: 7.4 us, 8.1 from
+// registers).  Beyond, two launches are faster: 2048 x 128 takes 8.2 us, 9.2 in one; 4096 8.9, 13.3 in one,
+// as eight SMs take in too little.
+int64_t balance_small(int E) { return (int64_t)2 * fe::kBalCluster * fe::kBalWarps * (32 / balance_lanes(E)); }
+
 bool balance_fused(int64_t T, int E)
 {
-    return T <= (int64_t)4 * fe::kBalCluster * fe::kBalWarps * (32 / balance_lanes(E));
+    if (E % 4 != 0) return T <= 2 * balance_small(E);
+    return T <= (int64_t)2 * fe::kBalCluster * fe::bal_ring_warps(E > 512 ? 32 : 16) * (32 / balance_lanes(E));
 }
 
 fe_status check_balance(const float* logits, const uint8_t*, int64_t T, int E, int top_k)
@@ -332,7 +338,20 @@ cudaError_t balance_ring_run(const fe::BalanceParams& p, cudaStream_t s)
         if (e != cudaSuccess) return e;
         ready[dev].store(true, std::memory_order_release);
     }
-    return launch(kernel, p.G, 32 * W, smem, s, p, stages);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.G > 0 ? p.G : fe::kBalCluster);
+    cfg.blockDim = dim3(32 * W);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.G > 0 ? 1 : fe::kBalCluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, p, stages);
 }
 
 cudaError_t balance_ring_dispatch(const fe::BalanceParams& p, cudaStream_t s)
@@ -917,7 +936,8 @@ fe_status fe_moe_balance_loss(const float* logits, const int32_t* idx, const uin
         int n = 1;   // CTAs of the cluster: a group per warp, to eight
         while (n < fe::kBalCluster && n < ctas) n *= 2;
         p.G = 0;
-        FE_CUDA_TRY(balance_dispatch(p, false, n, vec, s));
+        if (vec && T > balance_small(E)) FE_CUDA_TRY(balance_ring_dispatch(p, s));
+        else FE_CUDA_TRY(balance_dispatch(p, false, n, vec, s));
         return FE_OK;
     }
     p.G = ctas;
@@ -926,8 +946,10 @@ fe_status fe_moe_balance_loss(const float* logits, const int32_t* idx, const uin
     const int sms = sm_count();
     if (sms < 1) return record_cuda(cudaErrorInvalidDevice, "device");
     const int64_t groups = (T + 32 / balance_lanes(E) - 1) / (32 / balance_lanes(E));
-    if (vec && ctas >= sms && groups >= 4 * (int64_t)sms * fe::bal_ring_warps(E > 512 ? 32 : 16)) {
-        p.G = sms;
+    const int W = fe::bal_ring_warps(E > 512 ? 32 : 16);
+    if (vec) {
+        // enough CTAs for a group of rows per two warps, a CTA an SM at most: the second pass has the fewer partials to join
+        p.G = (int)std::min<int64_t>(sms, (2 * groups + W - 1) / W);
         p.ipart = reinterpret_cast<int32_t*>(p.part + (size_t)p.G * (E + 1));
         FE_CUDA_TRY(balance_ring_dispatch(p, s));
     } else {

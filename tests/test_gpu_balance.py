@@ -39,9 +39,11 @@ def test_loss_counts_and_gradient(T, E, k, pad):
     check(fe, *make(T, E, k, pad, seed=T + E), up=None if pad else -1.75)
 
 
-@pytest.mark.parametrize("T, E, k", [(15003, 512, 10), (60001, 128, 8), (8001, 1024, 40), (30000, 200, 3)])
+@pytest.mark.parametrize("T, E, k", [(15003, 512, 10), (60001, 128, 8), (8001, 1024, 40), (30000, 200, 3),
+                                     (700, 128, 8), (1536, 128, 8), (1537, 128, 8), (300, 512, 10), (150, 1024, 4),
+                                     (9000, 16, 2), (1000, 129, 4), (1100, 129, 4), (4097, 512, 10)])
 def test_streamed_batches(T, E, k):
-    """Enough rows for the pass that streams them, padded rows holding anything, rows of -inf."""
+    """Rows for one cluster's rings, for the pass over all SMs and around the sizes between, padded rows holding anything, rows of -inf."""
     import fp4_expert_gemv_b200 as fe
     l, idx, mask = make(T, E, k, True, seed=T)
     l[mask == 0] = float("nan")
