@@ -87,8 +87,8 @@ FE_DEV void bal_softmax(float (&l)[N], float& inv, float& lse)
     float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; i += 2) {
-        l[i] = __expf(l[i] - mm);
-        l[i + 1] = __expf(l[i + 1] - mm);
+        l[i] = ex2_ftz((l[i] - mm) * kLog2e);
+        l[i + 1] = ex2_ftz((l[i + 1] - mm) * kLog2e);
         s0 += l[i];
         s1 += l[i + 1];
     }

@@ -464,12 +464,12 @@ cudaError_t lin_pairs(int* pairs)
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     int n = known[dev].load(std::memory_order_acquire);
     if (n == 0) {
-        e = cudaFuncSetAttribute(fe::linear_gemm_kernel<BN, PLAIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)fe::kLinSmem);
+        e = cudaFuncSetAttribute(fe::linear_gemm_kernel<BN, PLAIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)fe::lin_smem(BN, PLAIN));
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2);
         cfg.blockDim = dim3(fe::kLinThreads);
-        cfg.dynamicSmemBytes = fe::kLinSmem;
+        cfg.dynamicSmemBytes = fe::lin_smem(BN, PLAIN);
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = 2;
@@ -541,7 +541,7 @@ cudaError_t lin_launch(fe::LinParams& P, const Product* f, int n, cudaStream_t s
     if (e != cudaSuccess) return e;
     pairs = std::min(pairs, tiles);
     if (n == 2) lin_share(P, pairs);
-    return launch(fe::linear_gemm_kernel<BN, PLAIN>, dim3(2 * pairs), dim3(fe::kLinThreads), fe::kLinSmem, s, P);
+    return launch(fe::linear_gemm_kernel<BN, PLAIN>, dim3(2 * pairs), dim3(fe::kLinThreads), fe::lin_smem(BN, PLAIN), s, P);
 }
 
 // Runs one product, or two in one launch, with the epilogues already in P.p.

@@ -25,25 +25,32 @@ namespace fe {
 
 enum { kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3, kActSwiglu = 4 };
 
-// Phi(z) and exp(-z^2 / 2).  The tail is Q(|z|) = erfc(x) / 2 with x = |z| / sqrt 2, and erfc(x) = exp(-x^2) t
-// p(t) with t = 1 / (1 + 0.43 x): erfc(x) exp(x^2) / t is smooth in t and p its polynomial of degree 7,
-// fitted by reweighted least squares to 2e-7 relative for x up to 12, so the small tail keeps its
-// digits.  One exponential, shared with the density, and one division; erff took three times the
-// instructions, as much as a whole product's tile at K = 2048.
+// Phi(z) and exp(-z^2 / 2), two at a time.  The tail is Q(|z|) = erfc(x) / 2 with x = |z| / sqrt 2, and
+// erfc(x) = exp(-x^2) t p(t) with t = 1 / (1 + 0.43 x): erfc(x) exp(x^2) / t is smooth in t and p its
+// polynomial of degree 7, fitted by reweighted least squares to 2e-7 relative for x up to 12, so the small
+// tail keeps its digits.  One exponential, shared with the density, one reciprocal, the polynomial in
+// paired instructions: with erff a tile's epilogue took as long as its products at K = 2048.
+FE_DEV float2 phi_cdf2(float2 z, float2& e)
+{
+    const float2 y = make_float2(fabsf(z.x), fabsf(z.y));
+    const float2 u = fma2(y, make_float2(0.304055916f, 0.304055916f), make_float2(1.0f, 1.0f));   // 0.43 / sqrt 2
+    const float2 t = make_float2(rcp_ftz(u.x), rcp_ftz(u.y));
+    const float2 w = mul2(mul2(z, z), make_float2(-0.5f * kLog2e, -0.5f * kLog2e));
+    e = make_float2(ex2_ftz(w.x), ex2_ftz(w.y));
+    constexpr float c[8] = {0.121269358f, 0.121994241f, 0.103734795f, 0.119104225f, -0.0344093589f, 0.182367387f, -0.149515733f, 0.0354549963f};   // p / 2
+    float2 q = make_float2(c[7], c[7]);
+#pragma unroll
+    for (int i = 6; i >= 0; --i) q = fma2(q, t, make_float2(c[i], c[i]));
+    q = mul2(q, mul2(t, e));
+    return make_float2(z.x < 0.0f ? q.x : 1.0f - q.x, z.y < 0.0f ? q.y : 1.0f - q.y);
+}
+
 FE_DEV float phi_cdf(float z, float& e)
 {
-    const float x = fabsf(z) * 0.70710678118654752f;
-    const float t = __fdividef(1.0f, fmaf(0.43f, x, 1.0f));
-    e = __expf(-x * x);
-    float q = fmaf(0.0709099927f, t, -0.299031466f);
-    q = fmaf(q, t, 0.364734775f);
-    q = fmaf(q, t, -0.0688187177f);
-    q = fmaf(q, t, 0.23820845f);
-    q = fmaf(q, t, 0.207469591f);
-    q = fmaf(q, t, 0.243988482f);
-    q = fmaf(q, t, 0.242538717f);
-    q *= 0.5f * t * e;
-    return z < 0.0f ? q : 1.0f - q;
+    float2 e2;
+    const float2 c = phi_cdf2(make_float2(z, z), e2);
+    e = e2.x;
+    return c.x;
 }
 
 FE_DEV float act_fwd(int act, float z)
@@ -83,7 +90,12 @@ FE_DEV void act_all(int act, float (&v)[N])
         for (int j = 0; j < N; ++j) v[j] = act_fwd(kActRelu, v[j]);
     } else if (act == kActGelu) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) v[j] = act_fwd(kActGelu, v[j]);
+        for (int j = 0; j < N; j += 2) {
+            float2 e;
+            const float2 c = phi_cdf2(make_float2(v[j], v[j + 1]), e);
+            v[j] *= c.x;
+            v[j + 1] *= c.y;
+        }
     } else {
 #pragma unroll
         for (int j = 0; j < N; ++j) v[j] = act_fwd(kActSilu, v[j]);
@@ -95,15 +107,22 @@ FE_DEV void act_all(int act, float (&v)[N])
 constexpr unsigned long long kLinTimeoutNs = 2000ull * 1000 * 1000;
 constexpr int kLinThreads = 384;         // warp 0: TMA, 1: MMA, 2: TMEM, 4-11: epilogue
 constexpr int kLinM = 256;               // rows of a tile: 128 in each CTA of the pair
-constexpr int kLinStages = 5;
 constexpr uint32_t kLinABytes = 128 * 128;   // one k step of 64: 128 rows of 128 bytes
-constexpr uint32_t kLinBBytes = 128 * 128;   // at most BN / 2 = 128 columns' rows
-constexpr uint32_t kLinStage = kLinABytes + kLinBBytes;
-constexpr int kLinSlots = 4;                 // output staging of a warp: 32 rows x 32 columns of bf16 each
-constexpr uint32_t kLinSlotBytes = 32 * 64;
+constexpr uint32_t kLinSlotBytes = 32 * 64;  // output staging: 32 rows x 32 columns of bf16
 constexpr int kLinMaxPairs = 128;
-constexpr int kLinBars = 2 * kLinStages + 4 + 16;
-constexpr uint32_t kLinSmem = 1024 + kLinStages * kLinStage + 8 * kLinSlots * kLinSlotBytes + 8 * kLinBars + 16;
+// A stage: A, and BN / 2 columns' rows of 128 bytes, in boxes of 64 columns where B lies across.  What the
+// staging leaves of shared memory is the ring's.
+__host__ __device__ constexpr uint32_t lin_stage(int BN) { return kLinABytes + (BN / 2 + 63) / 64 * 8192; }
+__host__ __device__ constexpr int lin_slots(bool plain) { return plain ? 2 : 4; }   // of each of the 8 epilogue warps
+__host__ __device__ constexpr int lin_stages(int BN, bool plain)
+{
+    return (227 * 1024 - 1024 - 8 * lin_slots(plain) * (int)kLinSlotBytes - 8 * 20 - 16) / ((int)lin_stage(BN) + 16);
+}
+__host__ __device__ constexpr int lin_bars(int BN, bool plain) { return 2 * lin_stages(BN, plain) + 4 + 16; }
+__host__ __device__ constexpr uint32_t lin_smem(int BN, bool plain)
+{
+    return 1024 + lin_stages(BN, plain) * lin_stage(BN) + 8 * lin_slots(plain) * kLinSlotBytes + 8 * lin_bars(BN, plain) + 16;
+}
 
 struct LinProblem {
     CUtensorMap ta, tb;      // operand boxes: 64 of k x rows (K-major), 64 x 64 of k (across)
@@ -369,7 +388,8 @@ template <int BN, bool PLAIN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     linear_gemm_kernel(const __grid_constant__ LinParams P)
 {
-    constexpr int S = kLinStages;
+    constexpr int S = lin_stages(BN, PLAIN), kLinBars = lin_bars(BN, PLAIN), kLinSlots = lin_slots(PLAIN);
+    constexpr uint32_t kLinStage = lin_stage(BN);
     constexpr int kAccStride = 256;
     constexpr uint32_t kTmemCols = BN > 128 ? 512 : 256;
     constexpr uint32_t kAccCol = BN > 128 ? kAccStride : 128;
@@ -408,6 +428,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     griddep_wait();
+    griddep_launch();   // the next launch's CTAs start as these end
 
     if (warp == 0) {
         // ---- producer: this CTA's boxes of A and B into its ring, reported to the leader ------------
@@ -600,13 +621,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                     }
                     if (live && !stop) {
                         if (!has_res) {
-                            // all four slots go round, or two beside z's: three (one) later stores may be reading
+                            // the slots go round, or two beside z's: all later stores but the one before last may be reading
                             if (!PLAIN && zo) {
                                 slot = st.ny++ & 1;
                                 st.settle<0>();
                             } else {
-                                slot = st.ny++ & 3;
-                                st.settle<3>();
+                                slot = st.ny++ & (kLinSlots - 1);
+                                st.settle<kLinSlots - 1>();
                             }
                         }
                         st.put(slot, lane, v);
@@ -616,9 +637,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                 // the accumulator is read: the products after the next may begin
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0)
-                    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_map(accempty(acc), 0))
-                                 : "memory");
+                if (lane == 0)   // nothing in memory goes with it: a release to the cluster would wait for the stores
+                    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_map(accempty(acc), 0)) : "memory");
                 if (stop) break;
             }
         }

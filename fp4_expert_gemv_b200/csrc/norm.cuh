@@ -48,7 +48,44 @@ struct NormBwdParams {
     float* part;              // [grid][3][H] column sums (dw_post, dw_pre, dgate per channel), or null
 };
 
-FE_DEV float sigmoidf(float x) { return __fdividef(1.0f, 1.0f + __expf(-x)); }
+// 2^x and 1 / x to 2 ulp, one instruction each: no scaling around results below 2^-126, which are zero.
+FE_DEV float ex2_ftz(float x)
+{
+    float v;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(v) : "f"(x));
+    return v;
+}
+
+FE_DEV float rcp_ftz(float x)
+{
+    float v;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(v) : "f"(x));
+    return v;
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+FE_DEV float sigmoidf(float x) { return rcp_ftz(1.0f + ex2_ftz(x * -kLog2e)); }
+
+// Two fp32 fused multiply-adds in one instruction, and products.
+FE_DEV float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+FE_DEV float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 
 // A thread's chunk c of 8 elements of a row: consecutive (VEC 8, 16-byte accesses) or strided by
 // the group's threads (VEC 1: any width and alignment, still coalesced).
@@ -357,53 +394,44 @@ __host__ __device__ inline uint32_t norm_bwd_stage(int H, bool r32, bool full)
 // A thread's 16 columns: chunks t and t + tpr of 8.
 constexpr int kRingC = 2;
 
-// Two fp32 operations per instruction.
-FE_DEV void fma2(float (&d)[8], int j, float a0, float a1, float b0, float b1, float c0, float c1)
+FE_DEV float2 pair(const float (&a)[8], int j) { return make_float2(a[j], a[j + 1]); }
+FE_DEV void put2(float (&d)[8], int j, float2 v)
 {
-    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-        "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
-        : "=f"(d[j]), "=f"(d[j + 1])
-        : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
-}
-
-FE_DEV void mul2(float (&d)[8], int j, float a0, float a1, float b0, float b1)
-{
-    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
-        : "=f"(d[j]), "=f"(d[j + 1])
-        : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+    d[j] = v.x;
+    d[j + 1] = v.y;
 }
 
 // Over 8 columns: d = a b + c, d = a b, and the same with one factor for all.
 FE_DEV void vfma(float (&d)[8], const float (&a)[8], const float (&b)[8], const float (&c)[8])
 {
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) fma2(d, j, a[j], a[j + 1], b[j], b[j + 1], c[j], c[j + 1]);
+    for (int j = 0; j < 8; j += 2) put2(d, j, fma2(pair(a, j), pair(b, j), pair(c, j)));
 }
 FE_DEV void vfma(float (&d)[8], float a, const float (&b)[8], const float (&c)[8])
 {
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) fma2(d, j, a, a, b[j], b[j + 1], c[j], c[j + 1]);
+    for (int j = 0; j < 8; j += 2) put2(d, j, fma2(make_float2(a, a), pair(b, j), pair(c, j)));
 }
 FE_DEV void vmul(float (&d)[8], const float (&a)[8], const float (&b)[8])
 {
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) mul2(d, j, a[j], a[j + 1], b[j], b[j + 1]);
+    for (int j = 0; j < 8; j += 2) put2(d, j, mul2(pair(a, j), pair(b, j)));
 }
 FE_DEV void vmul(float (&d)[8], float a, const float (&b)[8])
 {
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) mul2(d, j, a, a, b[j], b[j + 1]);
+    for (int j = 0; j < 8; j += 2) put2(d, j, mul2(make_float2(a, a), pair(b, j)));
 }
 
 // s += sum of a[j] b[j], in two chains that the caller adds at the end.
 FE_DEV void vdot(float (&s)[2], const float (&a)[8], const float (&b)[8])
 {
 #pragma unroll
-    for (int j = 0; j < 8; j += 2)
-        asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%0, %1};\n\t"
-            "fma.rn.f32x2 c, a, b, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
-            : "+f"(s[0]), "+f"(s[1])
-            : "f"(a[j]), "f"(a[j + 1]), "f"(b[j]), "f"(b[j + 1]));
+    for (int j = 0; j < 8; j += 2) {
+        const float2 v = fma2(pair(a, j), pair(b, j), make_float2(s[0], s[1]));
+        s[0] = v.x;
+        s[1] = v.y;
+    }
 }
 
 // How the gate enters a row: one factor, a factor per column, or one per element.
