@@ -396,6 +396,7 @@ __global__ void __cluster_dims__(kBalCluster, 1, 1) __launch_bounds__(1024) bala
     __shared__ float sums[2];
     __shared__ int n_all;
     griddep_wait();
+    griddep_launch();
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
     const uint32_t rank = cluster_rank();
     // rank 0's first warp also joins the other sums: its loads go out before the columns'

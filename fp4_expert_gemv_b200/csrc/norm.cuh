@@ -1141,13 +1141,20 @@ __global__ void __launch_bounds__(1024) column_sum_kernel(const float* part, int
 {
     __shared__ float s[32][33];
     griddep_wait();
+    griddep_launch();
     const int x = threadIdx.x & 31, yy = threadIdx.x >> 5;
     const int seg = blockIdx.y, c = blockIdx.x * 32 + x;
     float* out = seg == 0 ? o0 : seg == 1 ? o1 : o2;
     if (!out) return;
     float v = 0.0f;
     if (c < W)
-        for (int g = yy; g < G; g += 32) v += part[((size_t)g * segs + seg) * W + c];
+        for (int g0 = yy; g0 < G; g0 += 32 * 5) {   // 160 partials asked for at once
+            float w[5];
+#pragma unroll
+            for (int j = 0; j < 5; ++j) w[j] = g0 + 32 * j < G ? part[((size_t)(g0 + 32 * j) * segs + seg) * W + c] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < 5; ++j) v += w[j];
+        }
     s[yy][x] = v;
     __syncthreads();
     v = warp_sum(s[x][yy]);   // lane x holds partial x of column yy
