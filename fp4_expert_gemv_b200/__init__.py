@@ -266,12 +266,12 @@ class MoELayer:
             Is = shared[1].shape[1]
             _arg(shared[0], "shared gate_up", bf, (2 * Is, H), dev)
             _arg(shared[1], "shared down", bf, (H, Is), dev)
-        r_out = _out(r_out, "r_out", r.dtype, (T, H), dev)
+        r_out = _out(r_out, "r_out", r.dtype, (T, H), dev, r)
         if w_next_pre is not None:
-            u_out = _out(u_out, "u_out", bf, (T, H), dev)
+            u_out = _out(u_out, "u_out", bf, (T, H), dev, r)
         elif u_out is not None:
             raise ValueError("u_out needs w_next_pre")
-        logits = _out(logits, "logits", torch.float32, (T, self.E), dev)
+        logits = _out(logits, "logits", torch.float32, (T, self.E), dev, r)
         nb = fe_moe_forward_block_workspace(self.h, T, Is)
         b = BlockWeights(_dptr(w_pre), _dptr(w_router), _dptr(shared[0]) if shared else None,
                          _dptr(shared[1]) if shared else None, Is, _dptr(w_post), _dptr(gate), gate_kind, scale,
@@ -534,10 +534,15 @@ def _arg_gate(gate, kind, T, H, dev):
     return _arg(gate, "gate", torch.bfloat16, (H,) if k == GATE_CHANNEL else (T,) if k == GATE_TOKEN else (T, H), dev)
 
 
-def _out(t, name, dtype, shape, dev):
-    import torch
+def _new(like, dtype, *shape):
+    """An uninitialised tensor on like's device (by the cheapest of torch's ways: a third of a small call's host time
+    goes into its outputs)."""
+    return like.new_empty(*shape) if like.dtype is dtype else like.new_empty(*shape, dtype=dtype)
+
+
+def _out(t, name, dtype, shape, dev, like):
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return _new(like, dtype, *shape)
     _arg(t, name, dtype, shape, dev)
     return t
 
@@ -569,9 +574,9 @@ def block_norm(r, y=None, w_post=None, w_pre=None, gate=None, gate_kind=GATE_NON
     prep = _arg(w_pre, "w_pre", bf, (H,), dev, True)
     gp = _arg_gate(gate, gate_kind, T, H, dev)
     if y is not None:
-        r_out = _out(r_out, "r_out", r.dtype, shape, dev)
+        r_out = _out(r_out, "r_out", r.dtype, shape, dev, r)
     if w_pre is not None:
-        u = _out(u, "u", bf, shape, dev)
+        u = _out(u, "u", bf, shape, dev, r)
     with _device(dev):
         check(fe_moe_block_norm(rp, dt, yp, postp, gp, gate_kind, scale, prep, eps, T, H, _dptr(r_out), _dptr(u),
                                 _current_stream(dev)), "fe_moe_block_norm")
@@ -599,22 +604,22 @@ def block_norm_backward(dr_out, du, r, y=None, w_post=None, w_pre=None, gate=Non
     prep = _arg(w_pre, "w_pre", bf, (H,), dev, True)
     gp = _arg_gate(gate, gate_kind, T, H, dev)
     kind = gate_kind & ~GATE_SIGMOID
-    dr = torch.empty(shape, dtype=r.dtype, device=dev)
-    dy = torch.empty(shape, dtype=bf, device=dev) if y is not None else None
+    dr = torch.empty_like(r)
+    dy = torch.empty_like(y) if y is not None else None
     # the float32 sums over rows and the workspace behind them share one allocation
     sums = [] if not weight_grads else [n for n, on in (("post", w_post is not None), ("pre", w_pre is not None),
                                                         ("gate", kind == GATE_CHANNEL)) if on]
     col, ws, nb = {}, None, 0
     if sums:
         nb = fe_moe_block_norm_workspace(T, H)
-        buf = torch.empty(len(sums) * H + (nb + 3) // 4, dtype=f32, device=dev)
+        buf = _new(r, f32, len(sums) * H + (nb + 3) // 4)
         col = {n: buf[i * H:(i + 1) * H] for i, n in enumerate(sums)}
         ws = buf.data_ptr() + 4 * len(sums) * H
     dgate = col.get("gate")
     if kind == GATE_FULL:
-        dgate = torch.empty(shape, dtype=bf, device=dev)
+        dgate = torch.empty_like(gate)
     elif kind == GATE_TOKEN:
-        dgate = torch.empty(T, dtype=f32, device=dev)
+        dgate = _new(r, f32, T)
     dw_post, dw_pre = col.get("post"), col.get("pre")
     with _device(dev):
         check(fe_moe_block_norm_backward(drop, dup, rp, dt, yp, postp, gp, gate_kind, scale, prep, eps, T, H, _dptr(dr),
@@ -637,11 +642,11 @@ def balance_loss(logits, idx, mask=None, balance_coef=1.0, z_coef=0.0, loss=None
     lp = _arg(logits, "logits", f32, (T, E), dev)
     ip = _arg(idx, "idx", i32, (T, k), dev)
     mp = _arg(mask, "mask", torch.uint8, (T,), dev, True)
-    loss = _out(loss, "loss", f32, (3,), dev)
-    counts = _out(counts, "counts", i32, (E,), dev)
-    n_tokens = _out(n_tokens, "n_tokens", i32, (1,), dev)
+    loss = _out(loss, "loss", f32, (3,), dev, logits)
+    counts = _out(counts, "counts", i32, (E,), dev, idx)
+    n_tokens = _out(n_tokens, "n_tokens", i32, (1,), dev, idx)
     nb = fe_moe_balance_workspace(T, E)
-    ws = torch.empty(nb, dtype=torch.uint8, device=dev) if nb else None
+    ws = logits.new_empty((nb + 3) // 4) if nb else None
     with _device(dev):
         check(fe_moe_balance_loss(lp, ip, mp, T, E, k, balance_coef, z_coef, loss.data_ptr(), counts.data_ptr(),
                                   n_tokens.data_ptr(), _dptr(ws), nb, _current_stream(dev)), "fe_moe_balance_loss")
@@ -663,7 +668,7 @@ def balance_loss_backward(logits, counts, n_tokens, top_k: int, mask=None, dloss
     np_ = _arg(n_tokens, "n_tokens", i32, (1,), dev)
     mp = _arg(mask, "mask", torch.uint8, (T,), dev, True)
     dp = _arg(dloss, "dloss", f32, (1,), dev, True)
-    dlogits = _out(dlogits, "dlogits", dtype or (f32 if dlogits is None else dlogits.dtype), (T, E), dev)
+    dlogits = _out(dlogits, "dlogits", dtype or (f32 if dlogits is None else dlogits.dtype), (T, E), dev, logits)
     dt = _dtype_of(dlogits, "dlogits")
     with _device(dev):
         check(fe_moe_balance_loss_backward(lp, cp, np_, mp, dp, T, E, top_k, balance_coef, z_coef, dlogits.data_ptr(), dt,
@@ -689,7 +694,7 @@ def linear(x, w, bias=None, act=ACT_NONE, residual=None, y=None, z=None, stream=
     zp = _arg(z, "z", bf, (M, N), dev, True)
     resp, ldr = (None, 0) if residual is None else _arg_rows(residual, "residual", bf, out, dev)
     if y is None:
-        y = torch.empty(out, dtype=bf, device=dev)
+        y = x.new_empty(*out)
     yp, ldy = _arg_rows(y, "y", bf, out, dev)
     with _device(dev):
         check(fe_moe_linear(xp, ldx, wp, bp, resp, ldr, M, N, K, act, yp, ldy, zp, _current_stream(dev)), "fe_moe_linear")
@@ -710,11 +715,11 @@ def linear_backward(dy, x, w, z=None, act=ACT_NONE, need_dx=True, need_dw=True, 
     wp = _arg(w, "w", bf, (N, K), dev)
     zp = _arg(z, "z", bf, (M, N), dev, act == ACT_NONE)
     dyp, lddy = _arg_rows(dy, "dy", bf, (M, N // 2 if act == ACT_SWIGLU else N), dev)
-    dx = torch.empty((M, K), dtype=bf, device=dev) if need_dx else None
-    dw = torch.empty((N, K), dtype=bf, device=dev) if need_dw else None
-    db = torch.empty((N,), dtype=torch.float32, device=dev) if need_db else None
+    dx = x.new_empty(M, K) if need_dx else None
+    dw = torch.empty_like(w) if need_dw else None
+    db = _new(x, torch.float32, N) if need_db else None
     nb = fe_moe_linear_workspace(M, N, K, act)
-    ws = torch.empty(max(nb, 16), dtype=torch.uint8, device=dev)
+    ws = x.new_empty(max((nb + 1) // 2, 8))
     with _device(dev):
         check(fe_moe_linear_backward(dyp, lddy, xp, ldx, wp, zp, M, N, K, act, _dptr(dx), K, _dptr(dw), _dptr(db),
                                      ws.data_ptr(), nb, _current_stream(dev)), "fe_moe_linear_backward")
