@@ -733,6 +733,18 @@ cudaError_t rows_launch(const fe::LinRowsParams& p, cudaStream_t s)
     return launch(fe::linear_skinny_kernel<2, GLU>, grid, 256, 0, s, p);
 }
 
+template <int VEC>
+cudaError_t dz_launch(int act, dim3 grid, const fe::LinDzParams& p, cudaStream_t s)
+{
+    switch (act) {
+        case FE_ACT_RELU: return launch(fe::linear_dz_kernel<VEC, fe::kActRelu>, grid, 256, 0, s, p);
+        case FE_ACT_GELU: return launch(fe::linear_dz_kernel<VEC, fe::kActGelu>, grid, 256, 0, s, p);
+        case FE_ACT_SILU: return launch(fe::linear_dz_kernel<VEC, fe::kActSilu>, grid, 256, 0, s, p);
+        case FE_ACT_SWIGLU: return launch(fe::linear_dz_kernel<VEC, fe::kActSwiglu>, grid, 256, 0, s, p);
+    }
+    return launch(fe::linear_dz_kernel<VEC, fe::kActNone>, grid, 256, 0, s, p);
+}
+
 // Backward workspace: dz [M][roundup8(N)] bf16, then the column partials.
 int dz_chunks(int64_t M) { return (int)std::max<int64_t>(1, std::min<int64_t>(256, (M + 31) / 32)); }
 
@@ -1106,15 +1118,13 @@ fe_status fe_moe_linear_backward(const void* dy, int64_t lddy, const void* x, in
         p.M = M;
         p.N = N;
         p.cols = cols;
-        p.act = act;
         const int chunks = dz_chunks(M);
         p.rows_per_cta = (M + chunks - 1) / chunks;
         const int used = (int)((M + p.rows_per_cta - 1) / p.rows_per_cta);
         const bool vec = cols % 8 == 0 && lddy % 8 == 0 && aligned(dy, 16) && (act == FE_ACT_NONE || aligned(z, 16));
         const int per = 32 * (vec ? 8 : 1);
         const dim3 grid((cols + per - 1) / per, used);
-        FE_CUDA_TRY(vec ? launch(fe::linear_dz_kernel<8>, grid, dim3(256), 0, s, p)
-                        : launch(fe::linear_dz_kernel<1>, grid, dim3(256), 0, s, p));
+        FE_CUDA_TRY(vec ? dz_launch<8>(act, grid, p, s) : dz_launch<1>(act, grid, p, s));
         partials = used;
     }
     if (dx || dw) {

@@ -102,6 +102,24 @@ FE_DEV void act_all(int act, float (&v)[N])
     }
 }
 
+// act' over an array.
+template <int ACT, int N>
+FE_DEV void act_bwd_all(float (&v)[N])
+{
+    if (N % 2 == 0 && ACT == kActGelu) {
+#pragma unroll
+        for (int j = 0; j < N; j += 2) {
+            float2 e;
+            const float2 z = make_float2(v[j], v[N > 1 ? j + 1 : j]), c = phi_cdf2(z, e);
+            v[j] = c.x + z.x * e.x * 0.39894228040143268f;
+            v[N > 1 ? j + 1 : j] = c.y + z.y * e.y * 0.39894228040143268f;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = act_bwd(ACT, v[j]);
+    }
+}
+
 // ---- tensor-core tiles ---------------------------------------------------------------
 
 constexpr unsigned long long kLinTimeoutNs = 2000ull * 1000 * 1000;
@@ -1085,7 +1103,7 @@ struct LinDzParams {
     int64_t lddz;
     float* part;          // [gridDim.y][N] or null
     int64_t M, rows_per_cta;
-    int N, cols, act;
+    int N, cols;
 };
 
 template <int VEC>
@@ -1123,7 +1141,7 @@ constexpr int kDzRows = 2;   // rows a thread has in flight
 
 // Block 32 x 8: a thread owns VEC columns, 8 threads share the rows of a chunk.  Bound by memory: dY and
 // Z are read once, dZ written once, so a thread keeps two rows' loads in flight and an SM 16 warps.
-template <int VEC>
+template <int VEC, int ACT>
 __global__ void __launch_bounds__(256, 2) linear_dz_kernel(LinDzParams p)
 {
     using W = typename DzWord<VEC>::T;
@@ -1133,7 +1151,7 @@ __global__ void __launch_bounds__(256, 2) linear_dz_kernel(LinDzParams p)
     const int x = threadIdx.x & 31, yy = threadIdx.x >> 5;
     const int c = (blockIdx.x * 32 + x) * VEC;
     const int64_t r0 = (int64_t)blockIdx.y * p.rows_per_cta, r1 = min(p.M, r0 + p.rows_per_cta);
-    const bool glu = p.act == kActSwiglu;
+    constexpr bool glu = ACT == kActSwiglu;
     float s0[VEC], s1[VEC];
 #pragma unroll
     for (int j = 0; j < VEC; ++j) s0[j] = s1[j] = 0.0f;
@@ -1145,7 +1163,7 @@ __global__ void __launch_bounds__(256, 2) linear_dz_kernel(LinDzParams p)
                 const int64_t q = r + 8 * i;
                 if (q >= r1) break;
                 wg[i] = *reinterpret_cast<const W*>(p.dy + q * p.lddy + c);
-                if (p.act != kActNone) w0[i] = *reinterpret_cast<const W*>(p.z + q * p.N + c);
+                if (ACT != kActNone) w0[i] = *reinterpret_cast<const W*>(p.z + q * p.N + c);
                 if (glu) w1[i] = *reinterpret_cast<const W*>(p.z + q * p.N + p.cols + c);
             }
 #pragma unroll
@@ -1154,8 +1172,9 @@ __global__ void __launch_bounds__(256, 2) linear_dz_kernel(LinDzParams p)
                 if (q >= r1) break;
                 float g[VEC], z0[VEC], z1[VEC];
                 dz_unpack<VEC>(wg[i], g);
-                if (p.act != kActNone) dz_unpack<VEC>(w0[i], z0);
+                if (ACT != kActNone) dz_unpack<VEC>(w0[i], z0);
                 if (glu) dz_unpack<VEC>(w1[i], z1);
+                if (!glu && ACT != kActNone) act_bwd_all<ACT>(z0);
 #pragma unroll
                 for (int j = 0; j < VEC; ++j) {
                     float d0, d1 = 0.0f;
@@ -1164,7 +1183,7 @@ __global__ void __launch_bounds__(256, 2) linear_dz_kernel(LinDzParams p)
                         d1 = g[j] * z0[j] * sg;
                         d0 = g[j] * z1[j] * sg * (1.0f + z0[j] * (1.0f - sg));
                     } else {
-                        d0 = p.act == kActNone ? g[j] : g[j] * act_bwd(p.act, z0[j]);
+                        d0 = ACT == kActNone ? g[j] : g[j] * z0[j];
                     }
                     s0[j] += d0;
                     s1[j] += d1;
