@@ -282,12 +282,14 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(NormParams p, int tpr)
 // One exchange per row: with q = scale w_post a(g) y the second norm's sum is
 //   sum r'^2 = sum r^2 + 2 rho_y sum r q + rho_y^2 sum q^2,
 // and the backward pass's other sums follow from seven products of the operands as they lie in memory
-// (block_norm_backward_kernel), so the sums of all of them travel together and a second walk over
+// (block_norm_backward_ring_kernel), so the sums of all of them travel together and a second walk over
 // the stage writes every output.  Where r' is small next to what cancels in it (sum r'^2 below an
 // eighth of its positive parts, or not finite), the group takes the sums of the rounded r' itself,
 // which costs that row two more exchanges.  With an exchange per norm and one for dm, the group's
 // warps spent 10,000 cycles a row in latencies: 44 us for T = 4096, H = 2048 backward, where memory
-// needs 16.
+// needs 16.  Now it takes 26.5 us there and 85 us at T = 16384 (4.7 TB/s) without the weights' gradients, 6 us
+// more with them (their last partials and the launch that adds them); forward with fp32 rows 21.2 us (4.75
+// TB/s).  What bounds it is one group's exchange per row, with 16 warps on an SM.
 // A thread has 16 columns: the exchange is paid per thread and row, and with 8 columns it was half of all
 // instructions.  What varies per element is a template parameter or a neutral factor, never a branch.
 

@@ -545,7 +545,8 @@ fe_status fe_moe_linear_backward(const void* dy, int64_t lddy, const void* x, in
                                  int64_t M, int N, int K, int act, void* dx, int64_t lddx, void* dw, float* db,
                                  void* workspace, size_t workspace_bytes, fe_stream_t stream);
 
-/* Device-side problem bits (FE_DEVICE_TC_TIMEOUT) of the calls above on the current
+/* Device-side problem bits (FE_DEVICE_TC_TIMEOUT, FE_DEVICE_LOAD_TIMEOUT: a wait for a
+ * product or a copy ran out) of the calls above on the current
  * device since the last query; waits for the device and clears them.  Returns
  * FE_ERR_DEVICE_STATUS if a bit is set. */
 fe_status fe_moe_get_op_status(uint32_t* bits);
