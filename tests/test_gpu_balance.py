@@ -139,6 +139,16 @@ def test_unaligned_logits_bf16_gradient_and_in_place():
     assert same is l and torch.equal(l, again)
 
 
+@pytest.mark.parametrize("T, E, k", [(600, 128, 8), (1500, 128, 8), (300, 512, 4), (5000, 128, 8), (3, 1024, 1024)])
+def test_unaligned_logits_of_every_size(T, E, k):
+    import fp4_expert_gemv_b200 as fe
+    l, idx, mask = make(T, E, k, True, seed=T)
+    buf = torch.empty(T * E + 1, device="cuda")
+    odd = buf[1:].view(T, E)
+    odd.copy_(l)
+    check(fe, odd, idx, mask)
+
+
 def test_gradient_against_differences():
     """Central differences of the 64-bit loss with the counts held (step error h^2: below 1e-7 here)."""
     import fp4_expert_gemv_b200 as fe

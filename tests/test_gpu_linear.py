@@ -231,6 +231,28 @@ def test_streams_and_graphs(M):
     assert fe.op_status() == (fe.FE_OK, 0)
 
 
+@pytest.mark.parametrize("act", ["none", "gelu", "swiglu"])
+@pytest.mark.parametrize("M", [1, 9, 40, 300, 1003, 5000])
+def test_outputs_at_odd_addresses(M, act):
+    """y, z, residual and bias two bytes off their 16-byte boundaries: the same values, nothing beside them."""
+    import fp4_expert_gemv_b200 as fe
+    x, w, bias, res, _ = make(M, 264, 200, act, seed=M)
+    C = res.shape[1]
+    z = torch.empty(M, 264, dtype=bf, device="cuda")
+    want = check_forward(fe, x, w, bias, act, res, z=z)
+
+    def odd(t):
+        buf = torch.full((t.numel() + 8,), 7.0, dtype=bf, device="cuda")
+        v = buf[1:1 + t.numel()].view(t.shape)
+        v.copy_(t)
+        return buf, v
+    (yb, y), (zb, z2), (_, r2), (_, b2) = odd(want * 0), odd(z * 0), odd(res), odd(bias)
+    fe.linear(x, w, bias=b2, act=act_id(fe, act), residual=r2, y=y, z=z2)
+    assert torch.equal(y, want) and torch.equal(z2, z)
+    for buf, n in ((yb, M * C), (zb, M * 264)):
+        assert buf[0] == 7 and (buf[1 + n:] == 7).all()
+
+
 def test_rows_after_the_last_stay_as_they_were():
     import fp4_expert_gemv_b200 as fe
     for M in (3, 100, 2500):
