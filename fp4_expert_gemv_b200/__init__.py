@@ -11,6 +11,7 @@ and streams only) and checks status codes.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -476,6 +477,12 @@ class _Nothing:
 _NOTHING = _Nothing()
 
 
+# The sizes' answers alone: a model asks for the same few at every step.
+_norm_workspace, _balance_workspace, _linear_workspace = (
+    functools.lru_cache(1024)(lambda *sizes, query=query: query(*sizes))
+    for query in (fe_moe_block_norm_workspace, fe_moe_balance_workspace, fe_moe_linear_workspace))
+
+
 def _device(dev):
     import torch
     return _NOTHING if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
@@ -611,7 +618,7 @@ def block_norm_backward(dr_out, du, r, y=None, w_post=None, w_pre=None, gate=Non
                                                         ("gate", kind == GATE_CHANNEL)) if on]
     col, ws, nb = {}, None, 0
     if sums:
-        nb = fe_moe_block_norm_workspace(T, H)
+        nb = _norm_workspace(T, H)
         buf = _new(r, f32, len(sums) * H + (nb + 3) // 4)
         col = {n: buf[i * H:(i + 1) * H] for i, n in enumerate(sums)}
         ws = buf.data_ptr() + 4 * len(sums) * H
@@ -645,7 +652,7 @@ def balance_loss(logits, idx, mask=None, balance_coef=1.0, z_coef=0.0, loss=None
     loss = _out(loss, "loss", f32, (3,), dev, logits)
     counts = _out(counts, "counts", i32, (E,), dev, idx)
     n_tokens = _out(n_tokens, "n_tokens", i32, (1,), dev, idx)
-    nb = fe_moe_balance_workspace(T, E)
+    nb = _balance_workspace(T, E)
     ws = logits.new_empty((nb + 3) // 4) if nb else None
     with _device(dev):
         check(fe_moe_balance_loss(lp, ip, mp, T, E, k, balance_coef, z_coef, loss.data_ptr(), counts.data_ptr(),
@@ -715,10 +722,10 @@ def linear_backward(dy, x, w, z=None, act=ACT_NONE, need_dx=True, need_dw=True, 
     wp = _arg(w, "w", bf, (N, K), dev)
     zp = _arg(z, "z", bf, (M, N), dev, act == ACT_NONE)
     dyp, lddy = _arg_rows(dy, "dy", bf, (M, N // 2 if act == ACT_SWIGLU else N), dev)
-    dx = x.new_empty(M, K) if need_dx else None
+    dx = (torch.empty_like(x) if x.is_contiguous() else x.new_empty(M, K)) if need_dx else None
     dw = torch.empty_like(w) if need_dw else None
     db = _new(x, torch.float32, N) if need_db else None
-    nb = fe_moe_linear_workspace(M, N, K, act)
+    nb = _linear_workspace(M, N, K, act)
     ws = x.new_empty(max((nb + 1) // 2, 8))
     with _device(dev):
         check(fe_moe_linear_backward(dyp, lddy, xp, ldx, wp, zp, M, N, K, act, _dptr(dx), K, _dptr(dw), _dptr(db),

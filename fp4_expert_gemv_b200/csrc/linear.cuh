@@ -146,6 +146,10 @@ __host__ __device__ constexpr uint32_t lin_smem(int BN, bool plain)
     return 1024 + lin_stages(BN, plain) * lin_stage(BN) + 8 * lin_slots(plain) * kLinSlotBytes + 8 * lin_bars(BN, plain) + 16;
 }
 
+static_assert(lin_smem(128, true) <= 227 * 1024 && lin_smem(128, false) <= 227 * 1024 && lin_smem(192, true) <= 227 * 1024 &&
+                  lin_smem(192, false) <= 227 * 1024 && lin_smem(256, true) <= 227 * 1024 && lin_smem(256, false) <= 227 * 1024,
+              "a CTA's shared memory");
+
 struct LinProblem {
     CUtensorMap ta, tb;      // operand boxes: 64 of k x rows (K-major), 64 x 64 of k (across)
     CUtensorMap to, tr, tz;  // out, res and z: boxes of 32 columns x 32 rows
