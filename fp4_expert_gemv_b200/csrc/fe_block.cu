@@ -29,13 +29,7 @@ namespace {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// Whether [a, a + na) and [b, b + nb) share a byte; null ranges share none.
-bool overlap(const void* a, size_t na, const void* b, size_t nb)
-{
-    if (!a || !b || na == 0 || nb == 0) return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
+using fe_host::overlap;
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 

@@ -1123,6 +1123,24 @@ fe_status fe_moe_forward_block(fe_moe_t h, const fe_moe_block_t* b, const void* 
     void* y = ws + up(2 * (size_t)T * H);
     void* a = ws + 2 * up(2 * (size_t)T * H);
     const void* u = u_in ? u_in : ub;
+    // no output or workspace touches an operand or another output, over all parts (r_out may be r, u_out u_in)
+    if (r_dtype != FE_DTYPE_BF16 && r_dtype != FE_DTYPE_F32) return FE_ERR_INVALID_ARG;
+    const size_t nr = (size_t)T * H * (r_dtype == FE_DTYPE_F32 ? 4 : 2), nu = 2 * (size_t)T * H, nw = 2 * (size_t)H;
+    const void* outs[4] = {r_out, u_out, logits, workspace};
+    const size_t out_n[4] = {nr, nu, 4 * (size_t)T * h->E, fe_moe_forward_block_workspace(h, T, shared ? I : 0)};
+    const void* ins[9] = {r, u_in, u_in ? nullptr : b->w_pre, b->w_router, b->shared_gate_up, b->shared_down, b->w_post, b->w_next_pre, b->gate};
+    const int kind = b->gate_kind & ~FE_GATE_SIGMOID;
+    const size_t ng = kind == FE_GATE_CHANNEL ? nw : kind == FE_GATE_TOKEN ? 2 * (size_t)T : kind == FE_GATE_FULL ? nu : 0;
+    const size_t ns = shared ? 2 * (size_t)I * H : 0;
+    const size_t in_n[9] = {nr, nu, nw, nw * h->E, 2 * ns, ns, nw, nw, ng};
+    for (int i = 0; i < 4; ++i) {
+        for (int j = 0; j < 9; ++j) {
+            const bool same = (i == 0 && j == 0) || (i == 1 && j == 1);
+            if (!(same && outs[i] == ins[j]) && fe_host::overlap(outs[i], out_n[i], ins[j], in_n[j])) return FE_ERR_INVALID_ARG;
+        }
+        for (int j = 0; j < i; ++j)
+            if (fe_host::overlap(outs[i], out_n[i], outs[j], out_n[j])) return FE_ERR_INVALID_ARG;
+    }
     // every part's arguments, before the first launch
     fe_status st = FE_OK;
     if (!u_in) st = fe_host::check_block_norm(r, r_dtype, nullptr, nullptr, nullptr, FE_GATE_NONE, b->w_pre, b->eps, T, H, nullptr, ub);

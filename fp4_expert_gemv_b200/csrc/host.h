@@ -1,11 +1,22 @@
 // Host helpers shared by the translation units of the library.
 #pragma once
 
+#include <cstddef>
+#include <cstdint>
+
 #include <cuda_runtime.h>
 
 #include "../../include/fe_moe.h"
 
 namespace fe_host {
+
+// Whether [a, a + na) and [b, b + nb) share a byte; null ranges share none.
+inline bool overlap(const void* a, size_t na, const void* b, size_t nb)
+{
+    if (!a || !b || na == 0 || nb == 0) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
 
 // Keeps the text of a CUDA failure for fe_moe_last_error and maps it to a status.
 fe_status record_cuda(cudaError_t e, const char* where);

@@ -575,7 +575,7 @@ size_t fe_moe_forward_block_workspace(fe_moe_t h, int T, int shared_I);
  * fe_moe_block_norm: r_out = r + scale a(gate) norm(y; w_post), u_out =
  * norm(r_out; w_next_pre).  r, r_out [T][H] of r_dtype (r_out may be r); u_in bf16
  * [T][H] or NULL (pass the previous block's u_out); u_out bf16 [T][H], given exactly
- * when w_next_pre is; logits float [T][E] (written).  Limits and errors as the calls it is
+ * when w_next_pre is (it may be u_in); logits float [T][E] (written).  Limits and errors as the calls it is
  * made of; workspace 16-byte aligned.  Asynchronous, capturable. */
 fe_status fe_moe_forward_block(fe_moe_t h, const fe_moe_block_t* b, const void* r, int r_dtype, const void* u_in, int T,
                                int top_k, void* r_out, void* u_out, float* logits, void* workspace,

@@ -125,6 +125,21 @@ def test_block_refusals():
         call(r, 2, p["w_router"], w_pre=p["w_pre"], logits=logits)
     torch.cuda.synchronize()
     assert (logits == 3).all()
+    # outputs over operands and over each other, also of different parts of the block
+    r32 = torch.ones(4, 256, device="cuda")
+    kw = dict(w_pre=p["w_pre"], w_next_pre=p["w_next_pre"])
+    gl.layer.set_path(fe.PATH_AUTO)
+    for bad in (dict(logits=r32.view(-1)[:32].view(4, 8)), dict(u_out=r32.view(bf).view(-1)[512:1536].view(4, 256)),
+                dict(u_in=r32.view(bf).view(-1)[:1024].view(4, 256), r_out=r32)):
+        with pytest.raises(fe.FeMoeError):
+            gl.layer.forward_block(r32, 2, p["w_router"], **{**kw, **bad})
+    torch.cuda.synchronize()
+    assert (r32 == 1).all()
+    # in place, as said: r_out over r and u_out over u_in
+    _, u0 = fe.block_norm(r32, w_pre=p["w_pre"])
+    want = gl.layer.forward_block(r32, 2, p["w_router"], u_in=u0, w_next_pre=p["w_next_pre"])
+    got = gl.layer.forward_block(r32, 2, p["w_router"], u_in=u0, w_next_pre=p["w_next_pre"], r_out=r32, u_out=u0)
+    assert got[0] is r32 and got[1] is u0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     gl.layer.close()
 
 
