@@ -277,11 +277,9 @@ class MoELayer:
         b = BlockWeights(_dptr(w_pre), _dptr(w_router), _dptr(shared[0]) if shared else None,
                          _dptr(shared[1]) if shared else None, Is, _dptr(w_post), _dptr(gate), gate_kind, scale,
                          _dptr(w_next_pre), eps)
-        with _device(dev):
-            ws = torch.empty(max(nb, 16), dtype=torch.uint8, device=dev)
-            check(fe_moe_forward_block(self.h, ctypes.byref(b), _dptr(r), dt, _dptr(u_in), T, top_k, _dptr(r_out),
-                                       _dptr(u_out), _dptr(logits), _dptr(ws), ws.numel(), _current_stream(dev)),
-                  "fe_moe_forward_block")
+        ws = r.new_empty(max(nb, 16), dtype=torch.uint8)
+        _run("fe_moe_forward_block", fe_moe_forward_block, dev, self.h, ctypes.byref(b), _dptr(r), dt, _dptr(u_in), T, top_k,
+             _dptr(r_out), _dptr(u_out), _dptr(logits), _dptr(ws), ws.numel())
         return r_out, u_out, logits
 
     def forward_host(self, x_bf16_host, logits_host, top_k: int, y_bf16_host, stream=None):
@@ -466,33 +464,35 @@ def pack_device(W, codes=None, scales=None, stream=None):
 # runs on the current stream of the tensors' device.
 
 
-class _Nothing:
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *_):
-        return False
-
-
-_NOTHING = _Nothing()
-
-
 # The sizes' answers alone: a model asks for the same few at every step.
 _norm_workspace, _balance_workspace, _linear_workspace = (
     functools.lru_cache(1024)(lambda *sizes, query=query: query(*sizes))
     for query in (fe_moe_block_norm_workspace, fe_moe_balance_workspace, fe_moe_linear_workspace))
 
 
-def _device(dev):
-    import torch
-    return _NOTHING if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-
-
-def _current_stream(dev):
-    """The current stream of a device, as an address (without the Stream object where torch offers that)."""
+@functools.cache
+def _current():
+    """torch's current device, and a device's current stream as an address (without the Stream object where torch
+    offers that)."""
     import torch
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(dev.index) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
+    return torch.cuda.current_device, raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _run(what, fn, dev, *args):
+    """fn(*args, the current stream of dev) with dev current; raises on a status."""
+    if dev.type != "cuda":
+        raise ValueError(f"{what}: CUDA tensors are needed, got {dev}")
+    device, stream = _current()
+    index = dev.index
+    if index == device():
+        status = fn(*args, stream(index))
+    else:
+        import torch
+        with torch.cuda.device(dev):
+            status = fn(*args, stream(index))
+    if status != FE_OK:
+        raise FeMoeError(status, what)
 
 
 def _on_stream(stream, dev):
@@ -511,7 +511,7 @@ def _arg(t, name, dtype, shape, dev, optional=False):
         if optional:
             return None
         raise ValueError(f"{name} is needed")
-    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_cuda or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} CUDA tensor of shape {tuple(shape)} on {dev} is needed, "
                          f"got {t.dtype} {tuple(t.shape)} strides {tuple(t.stride())} on {t.device}")
     return t.data_ptr()
@@ -519,7 +519,7 @@ def _arg(t, name, dtype, shape, dev, optional=False):
 
 def _arg_rows(t, name, dtype, shape, dev):
     """The address and row stride of a CUDA matrix whose rows are contiguous."""
-    if (t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_cuda
+    if (t.dtype is not dtype or t.shape != shape or t.device != dev
             or (shape[1] > 1 and shape[0] > 0 and t.stride(1) != 1)):
         raise ValueError(f"{name}: a {dtype} CUDA matrix of shape {tuple(shape)} on {dev} with contiguous rows is needed, "
                          f"got {t.dtype} {tuple(t.shape)} strides {tuple(t.stride())} on {t.device}")
@@ -549,7 +549,7 @@ def _new(like, dtype, *shape):
 
 def _out(t, name, dtype, shape, dev, like):
     if t is None:
-        return _new(like, dtype, *shape)
+        return like.new_empty(*shape) if like.dtype is dtype else like.new_empty(*shape, dtype=dtype)
     _arg(t, name, dtype, shape, dev)
     return t
 
@@ -584,9 +584,8 @@ def block_norm(r, y=None, w_post=None, w_pre=None, gate=None, gate_kind=GATE_NON
         r_out = _out(r_out, "r_out", r.dtype, shape, dev, r)
     if w_pre is not None:
         u = _out(u, "u", bf, shape, dev, r)
-    with _device(dev):
-        check(fe_moe_block_norm(rp, dt, yp, postp, gp, gate_kind, scale, prep, eps, T, H, _dptr(r_out), _dptr(u),
-                                _current_stream(dev)), "fe_moe_block_norm")
+    _run("fe_moe_block_norm", fe_moe_block_norm, dev, rp, dt, yp, postp, gp, gate_kind, scale, prep, eps, T, H,
+         _dptr(r_out), _dptr(u))
     return r_out, u
 
 
@@ -628,10 +627,8 @@ def block_norm_backward(dr_out, du, r, y=None, w_post=None, w_pre=None, gate=Non
     elif kind == GATE_TOKEN:
         dgate = _new(r, f32, T)
     dw_post, dw_pre = col.get("post"), col.get("pre")
-    with _device(dev):
-        check(fe_moe_block_norm_backward(drop, dup, rp, dt, yp, postp, gp, gate_kind, scale, prep, eps, T, H, _dptr(dr),
-                                         _dptr(dy), _dptr(dgate), _dptr(dw_post), _dptr(dw_pre), ws, nb,
-                                         _current_stream(dev)), "fe_moe_block_norm_backward")
+    _run("fe_moe_block_norm_backward", fe_moe_block_norm_backward, dev, drop, dup, rp, dt, yp, postp, gp, gate_kind,
+         scale, prep, eps, T, H, _dptr(dr), _dptr(dy), _dptr(dgate), _dptr(dw_post), _dptr(dw_pre), ws, nb)
     return dr, dy, dgate, dw_post, dw_pre
 
 
@@ -654,9 +651,8 @@ def balance_loss(logits, idx, mask=None, balance_coef=1.0, z_coef=0.0, loss=None
     n_tokens = _out(n_tokens, "n_tokens", i32, (1,), dev, idx)
     nb = _balance_workspace(T, E)
     ws = logits.new_empty((nb + 3) // 4) if nb else None
-    with _device(dev):
-        check(fe_moe_balance_loss(lp, ip, mp, T, E, k, balance_coef, z_coef, loss.data_ptr(), counts.data_ptr(),
-                                  n_tokens.data_ptr(), _dptr(ws), nb, _current_stream(dev)), "fe_moe_balance_loss")
+    _run("fe_moe_balance_loss", fe_moe_balance_loss, dev, lp, ip, mp, T, E, k, balance_coef, z_coef, loss.data_ptr(),
+         counts.data_ptr(), n_tokens.data_ptr(), _dptr(ws), nb)
     return loss, counts, n_tokens
 
 
@@ -677,9 +673,8 @@ def balance_loss_backward(logits, counts, n_tokens, top_k: int, mask=None, dloss
     dp = _arg(dloss, "dloss", f32, (1,), dev, True)
     dlogits = _out(dlogits, "dlogits", dtype or (f32 if dlogits is None else dlogits.dtype), (T, E), dev, logits)
     dt = _dtype_of(dlogits, "dlogits")
-    with _device(dev):
-        check(fe_moe_balance_loss_backward(lp, cp, np_, mp, dp, T, E, top_k, balance_coef, z_coef, dlogits.data_ptr(), dt,
-                                           _current_stream(dev)), "fe_moe_balance_loss_backward")
+    _run("fe_moe_balance_loss_backward", fe_moe_balance_loss_backward, dev, lp, cp, np_, mp, dp, T, E, top_k,
+         balance_coef, z_coef, dlogits.data_ptr(), dt)
     return dlogits
 
 
@@ -703,8 +698,7 @@ def linear(x, w, bias=None, act=ACT_NONE, residual=None, y=None, z=None, stream=
     if y is None:
         y = x.new_empty(*out)
     yp, ldy = _arg_rows(y, "y", bf, out, dev)
-    with _device(dev):
-        check(fe_moe_linear(xp, ldx, wp, bp, resp, ldr, M, N, K, act, yp, ldy, zp, _current_stream(dev)), "fe_moe_linear")
+    _run("fe_moe_linear", fe_moe_linear, dev, xp, ldx, wp, bp, resp, ldr, M, N, K, act, yp, ldy, zp)
     return y
 
 
@@ -727,9 +721,8 @@ def linear_backward(dy, x, w, z=None, act=ACT_NONE, need_dx=True, need_dw=True, 
     db = _new(x, torch.float32, N) if need_db else None
     nb = _linear_workspace(M, N, K, act)
     ws = x.new_empty(max((nb + 1) // 2, 8))
-    with _device(dev):
-        check(fe_moe_linear_backward(dyp, lddy, xp, ldx, wp, zp, M, N, K, act, _dptr(dx), K, _dptr(dw), _dptr(db),
-                                     ws.data_ptr(), nb, _current_stream(dev)), "fe_moe_linear_backward")
+    _run("fe_moe_linear_backward", fe_moe_linear_backward, dev, dyp, lddy, xp, ldx, wp, zp, M, N, K, act, _dptr(dx),
+         K, _dptr(dw), _dptr(db), ws.data_ptr(), nb)
     return dx, dw, db
 
 
