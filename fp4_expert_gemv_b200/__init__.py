@@ -612,23 +612,21 @@ def block_norm_backward(dr_out, du, r, y=None, w_post=None, w_pre=None, gate=Non
     kind = gate_kind & ~GATE_SIGMOID
     dr = torch.empty_like(r)
     dy = torch.empty_like(y) if y is not None else None
-    # the float32 sums over rows and the workspace behind them share one allocation
-    sums = [] if not weight_grads else [n for n, on in (("post", w_post is not None), ("pre", w_pre is not None),
-                                                        ("gate", kind == GATE_CHANNEL)) if on]
-    col, ws, nb = {}, None, 0
-    if sums:
-        nb = _norm_workspace(T, H)
-        buf = _new(r, f32, len(sums) * H + (nb + 3) // 4)
-        col = {n: buf[i * H:(i + 1) * H] for i, n in enumerate(sums)}
-        ws = buf.data_ptr() + 4 * len(sums) * H
-    dgate = col.get("gate")
+    dw_post = _new(r, f32, H) if weight_grads and w_post is not None else None
+    dw_pre = _new(r, f32, H) if weight_grads and w_pre is not None else None
+    dgate = None
     if kind == GATE_FULL:
         dgate = torch.empty_like(gate)
     elif kind == GATE_TOKEN:
         dgate = _new(r, f32, T)
-    dw_post, dw_pre = col.get("post"), col.get("pre")
+    elif kind == GATE_CHANNEL and weight_grads:
+        dgate = _new(r, f32, H)
+    ws, nb = None, 0
+    if dw_post is not None or dw_pre is not None or (kind == GATE_CHANNEL and weight_grads):
+        nb = _norm_workspace(T, H)
+        ws = _new(r, f32, (nb + 3) // 4)
     _run("fe_moe_block_norm_backward", fe_moe_block_norm_backward, dev, drop, dup, rp, dt, yp, postp, gp, gate_kind,
-         scale, prep, eps, T, H, _dptr(dr), _dptr(dy), _dptr(dgate), _dptr(dw_post), _dptr(dw_pre), ws, nb)
+         scale, prep, eps, T, H, _dptr(dr), _dptr(dy), _dptr(dgate), _dptr(dw_post), _dptr(dw_pre), _dptr(ws), nb)
     return dr, dy, dgate, dw_post, dw_pre
 
 
