@@ -954,8 +954,9 @@ fe_status fe_moe_balance_loss(const float* logits, const int32_t* idx, const uin
     const int64_t groups = (T + 32 / balance_lanes(E) - 1) / (32 / balance_lanes(E));
     const int W = fe::bal_ring_warps(E > 512 ? 32 : 16);
     if (vec) {
-        // enough CTAs for a group of rows per two warps, a CTA an SM at most: the second pass has the fewer partials to join
-        p.G = (int)std::min<int64_t>(sms, (2 * groups + W - 1) / W);
+        // enough CTAs for a group of rows per two warps, a CTA an SM at most, and no more than the workspace has
+        // partials for: the second pass has the fewer to join
+        p.G = (int)std::min<int64_t>(std::min(sms, ctas), (2 * groups + W - 1) / W);
         p.ipart = reinterpret_cast<int32_t*>(p.part + (size_t)p.G * (E + 1));
         FE_CUDA_TRY(balance_ring_dispatch(p, s));
     } else {

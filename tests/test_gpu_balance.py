@@ -41,7 +41,8 @@ def test_loss_counts_and_gradient(T, E, k, pad):
 
 @pytest.mark.parametrize("T, E, k", [(15003, 512, 10), (60001, 128, 8), (8001, 1024, 40), (30000, 200, 3),
                                      (700, 128, 8), (1536, 128, 8), (1537, 128, 8), (300, 512, 10), (150, 1024, 4),
-                                     (9000, 16, 2), (1000, 129, 4), (1100, 129, 4), (4097, 512, 10)])
+                                     (9000, 16, 2), (1000, 129, 4), (1100, 129, 4), (4097, 512, 10), (200, 1024, 4),
+                                     (900, 1024, 4), (193, 516, 3)])
 def test_streamed_batches(T, E, k):
     """Rows for one cluster's rings, for the pass over all SMs and around the sizes between, padded rows holding anything, rows of -inf."""
     import fp4_expert_gemv_b200 as fe
@@ -147,6 +148,25 @@ def test_unaligned_logits_of_every_size(T, E, k):
     odd = buf[1:].view(T, E)
     odd.copy_(l)
     check(fe, odd, idx, mask)
+
+
+@pytest.mark.parametrize("E", [16, 128, 512, 516, 1024, 1023])
+def test_the_workspace_is_all_that_is_written(E):
+    """Every size at which the launches change, with the bytes behind the workspace and the outputs watched."""
+    import fp4_expert_gemv_b200 as fe
+    R = max(1, 512 // E) if E <= 512 else 1
+    for T in sorted({1, 5, 128 * R, 128 * R + 1, 193, 200, 256 * R + 1, 384 * R + 1, 600, 1000, 1185, 3553 * R, 5000}):
+        l, idx, _ = make(T, E, 4, False, seed=T)
+        nb = fe.fe_moe_balance_workspace(T, E)
+        ws = torch.full((nb + 4096,), 85, dtype=torch.uint8, device="cuda")
+        out = torch.full((3 + 64,), 5.0, device="cuda")
+        ints = torch.full((E + 1 + 64,), 5, dtype=torch.int32, device="cuda")
+        st = fe.fe_moe_balance_loss(l.data_ptr(), idx.data_ptr(), None, T, E, 4, 1.0, 0.1, out.data_ptr(), ints.data_ptr(),
+                                    ints.data_ptr() + 4 * E, ws.data_ptr(), nb, torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert st == fe.FE_OK and (ws[nb:] == 85).all() and (out[3:] == 5).all() and (ints[E + 1:] == 5).all(), (T, E)
+        want = fe.balance_loss(l, idx, balance_coef=1.0, z_coef=0.1)
+        assert torch.equal(out[:3], want[0]) and torch.equal(ints[:E], want[1]) and int(ints[E]) == T
 
 
 def test_gradient_against_differences():
