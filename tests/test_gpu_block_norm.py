@@ -118,6 +118,26 @@ def test_without_weight_gradients():
         assert torch.equal(full[0], part[0]) and torch.equal(full[1], part[1]) and part[2:] == (None, None, None)
 
 
+@pytest.mark.parametrize("H", [8, 136, 255, 2048, 4096, 9000])
+def test_the_workspace_is_all_that_is_written(H):
+    """The bytes behind the workspace and the sums over rows are watched, from one row to many per group."""
+    import fp4_expert_gemv_b200 as fe
+    for T in (1, 3, 147, 149, 297, 513, 1300):
+        c = make(T, H, torch.bfloat16, "channel", seed=T)
+        nb = fe.fe_moe_block_norm_workspace(T, H)
+        ws = torch.full((nb + 4096,), 85, dtype=torch.uint8, device="cuda")
+        dr, dy = torch.full((2, T * H + 64), 5.0, dtype=torch.bfloat16, device="cuda")
+        sums = torch.full((3, H + 64), 5.0, device="cuda")
+        st = fe.fe_moe_block_norm_backward(c["dr_out"].data_ptr(), c["du"].data_ptr(), c["r"].data_ptr(), fe.DTYPE_BF16,
+                                           c["y"].data_ptr(), c["w_post"].data_ptr(), c["g"].data_ptr(), fe.GATE_CHANNEL, 0.5,
+                                           c["w_pre"].data_ptr(), EPS, T, H, dr.data_ptr(), dy.data_ptr(), sums[0].data_ptr(),
+                                           sums[1].data_ptr(), sums[2].data_ptr(), ws.data_ptr(), nb,
+                                           torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert st == fe.FE_OK and (ws[nb:] == 85).all() and (sums[:, H:] == 5).all(), (T, H)
+        assert (dr[T * H:] == 5).all() and (dy[T * H:] == 5).all()
+
+
 def test_unaligned_rows():
     """A width of whole chunks whose rows start 2 bytes off take the narrow accesses."""
     import fp4_expert_gemv_b200 as fe

@@ -253,6 +253,25 @@ def test_outputs_at_odd_addresses(M, act):
         assert buf[0] == 7 and (buf[1 + n:] == 7).all()
 
 
+@pytest.mark.parametrize("N, K", [(2, 8), (66, 72), (1002, 264), (1536, 2048)])
+def test_the_workspace_is_all_that_is_written(N, K):
+    import fp4_expert_gemv_b200 as fe
+    for M in (1, 31, 33, 129, 1000, 8200):
+        x, w, bias, res, dy = make(M, N, K, "swiglu", seed=M)
+        z = torch.empty(M, N, dtype=bf, device="cuda")
+        fe.linear(x, w, bias=bias, act=fe.ACT_SWIGLU, z=z)
+        nb = fe.fe_moe_linear_workspace(M, N, K, fe.ACT_SWIGLU)
+        ws = torch.full((nb + 4096,), 85, dtype=torch.uint8, device="cuda")
+        dx, dw = (torch.full((n * K + 64,), 5.0, dtype=bf, device="cuda") for n in (M, N))
+        db = torch.full((N + 64,), 5.0, device="cuda")
+        st = fe.fe_moe_linear_backward(dy.data_ptr(), N // 2, x.data_ptr(), K, w.data_ptr(), z.data_ptr(), M, N, K, fe.ACT_SWIGLU,
+                                       dx.data_ptr(), K, dw.data_ptr(), db.data_ptr(), ws.data_ptr(), nb,
+                                       torch.cuda.current_stream().cuda_stream)
+        torch.cuda.synchronize()
+        assert st == fe.FE_OK and (ws[nb:] == 85).all(), (M, N, K)
+        assert (dx[M * K:] == 5).all() and (dw[N * K:] == 5).all() and (db[N:] == 5).all()
+
+
 def test_rows_after_the_last_stay_as_they_were():
     import fp4_expert_gemv_b200 as fe
     for M in (3, 100, 2500):
