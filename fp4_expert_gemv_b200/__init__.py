@@ -519,6 +519,8 @@ def _arg(t, name, dtype, shape, dev, optional=False):
 
 def _arg_rows(t, name, dtype, shape, dev):
     """The address and row stride of a CUDA matrix whose rows are contiguous."""
+    if t.dtype is dtype and t.shape == shape and t.device == dev and shape[0] > 1 and t.is_contiguous():
+        return t.data_ptr(), shape[1]
     if (t.dtype is not dtype or t.shape != shape or t.device != dev
             or (shape[1] > 1 and shape[0] > 0 and t.stride(1) != 1)):
         raise ValueError(f"{name}: a {dtype} CUDA matrix of shape {tuple(shape)} on {dev} with contiguous rows is needed, "
@@ -695,7 +697,9 @@ def linear(x, w, bias=None, act=ACT_NONE, residual=None, y=None, z=None, stream=
     resp, ldr = (None, 0) if residual is None else _arg_rows(residual, "residual", bf, out, dev)
     if y is None:
         y = x.new_empty(*out)
-    yp, ldy = _arg_rows(y, "y", bf, out, dev)
+        yp, ldy = y.data_ptr(), out[1]
+    else:
+        yp, ldy = _arg_rows(y, "y", bf, out, dev)
     _run("fe_moe_linear", fe_moe_linear, dev, xp, ldx, wp, bp, resp, ldr, M, N, K, act, yp, ldy, zp)
     return y
 
