@@ -519,8 +519,8 @@ def _arg(t, name, dtype, shape, dev, optional=False):
 
 def _arg_rows(t, name, dtype, shape, dev):
     """The address and row stride of a CUDA matrix whose rows are contiguous."""
-    if t.dtype is dtype and t.shape == shape and t.device == dev and shape[0] > 1 and t.is_contiguous():
-        return t.data_ptr(), shape[1]
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr(), shape[1] if shape[0] > 1 else (shape[1] + 7) // 8 * 8
     if (t.dtype is not dtype or t.shape != shape or t.device != dev
             or (shape[1] > 1 and shape[0] > 0 and t.stride(1) != 1)):
         raise ValueError(f"{name}: a {dtype} CUDA matrix of shape {tuple(shape)} on {dev} with contiguous rows is needed, "
