@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(32 * bal_ring_warps(N)) balance_ring_kernel(Ba
             parity ^= 1;
         }
     }
-    if (dead) atomicOr(&g_op_status, kDevLoadTimeout);
+    if (dead) atomicOr(&g_op_status, kOpLoadTimeout);
     const float zz = bal_block_sum(z, scratch);   // and every warp is done with its ring
     float(*ps)[L * N] = reinterpret_cast<float(*)[L * N]>(bal_dyn);
 #pragma unroll

@@ -17,7 +17,6 @@ namespace fe {
 // Device status bits (same values as the public FE_DEVICE_* macros).
 constexpr uint32_t kDevBadExpert = 0x1;
 constexpr uint32_t kDevNanLogit = 0x2;
-constexpr uint32_t kDevLoadTimeout = 0x8;  // a copy into shared memory never completed
 constexpr uint32_t kDevTcTimeout = 0x10;   // a tensor-core tile gave up waiting for its MMAs
 
 // ---------------------------------------------------------------------------

@@ -64,6 +64,7 @@ constexpr int kDecSlots = kDecThreads / 16;   // partial-sum slots of the final 
 constexpr int kDecMaxCtas = 160;      // grid (= SMs) the final reduction is unrolled for
 constexpr int kDecArriveSlack = 8;    // CTAs still out when the column sums start reading
 constexpr uint32_t kDevBarrierTimeout = 0x4;
+constexpr uint32_t kDevLoadTimeout = 0x8;
 
 struct DecodeParams {
     const uint16_t* x;        // bf16 [T][H]

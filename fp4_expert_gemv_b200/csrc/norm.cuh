@@ -17,7 +17,9 @@
 
 namespace fe {
 
-// Device-side problems of the entry points without a handle (kDevTcTimeout, kDevLoadTimeout).
+// Device-side problems of the entry points without a handle: kDevTcTimeout, and FE_DEVICE_LOAD_TIMEOUT's bit (a copy
+// into shared memory never completed).
+constexpr uint32_t kOpLoadTimeout = 0x8;
 __device__ uint32_t g_op_status;
 
 constexpr int kNormMaxH = 16384;   // 1024 threads x 2 chunks of 8
@@ -607,7 +609,7 @@ __global__ void __launch_bounds__(512) block_norm_ring_kernel(NormParams p, int 
             parity ^= 1;
         }
     }
-    if (dead) atomicOr(&g_op_status, kDevLoadTimeout);
+    if (dead) atomicOr(&g_op_status, kOpLoadTimeout);
 }
 
 // The gradients.  With n = r' rho and x = du w_pre:
@@ -870,7 +872,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_ring_kernel(NormBwdPa
             parity ^= 1;
         }
     }
-    if (dead) atomicOr(&g_op_status, kDevLoadTimeout);
+    if (dead) atomicOr(&g_op_status, kOpLoadTimeout);
     if (!q.part) return;
     // the CTA's groups join over the stages (every copy has landed and been read): each leaves its column
     // sums, then they are added in group order, one partial per CTA

@@ -61,3 +61,10 @@ def test_nvfp4_roofline_arithmetic():
     assert r["peak"] == 5600.0 and abs(r["frac"] - r["achieved"] / 5600.0) < 1e-12
     assert abs(r["frac_of_nominal_fp4_9pflops"] - r["achieved"] / 9000.0) < 1e-12
     assert r["bound"] == "tensor" and r["unit"] == "TFLOP/s"
+
+
+def test_the_committed_traffic_record_describes_the_committed_kernel():
+    """The headline kernel's sources are those of its capture (changed sources want a new one): a constant of
+    other kernels has no place in them."""
+    traffic, kernel = bench.ncu_traffic("decode_e128_t1", 48)
+    assert kernel == "stack_decode_kernel" and traffic is not None and traffic > 48 * 8 * bench.bytes_per_expert(2048, 768)
