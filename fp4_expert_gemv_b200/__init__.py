@@ -267,6 +267,7 @@ class MoELayer:
             Is = shared[1].shape[1]
             _arg(shared[0], "shared gate_up", bf, (2 * Is, H), dev)
             _arg(shared[1], "shared down", bf, (H, Is), dev)
+        given = _given(r_out, u_out, logits)
         r_out = _out(r_out, "r_out", r.dtype, (T, H), dev, r)
         if w_next_pre is not None:
             u_out = _out(u_out, "u_out", bf, (T, H), dev, r)
@@ -280,6 +281,8 @@ class MoELayer:
         ws = r.new_empty(max(nb, 16), dtype=torch.uint8)
         _run("fe_moe_forward_block", fe_moe_forward_block, dev, self.h, ctypes.byref(b), _dptr(r), dt, _dptr(u_in), T, top_k,
              _dptr(r_out), _dptr(u_out), _dptr(logits), _dptr(ws), ws.numel())
+        if given:
+            _bump()(given)
         return r_out, u_out, logits
 
     def forward_host(self, x_bf16_host, logits_host, top_k: int, y_bf16_host, stream=None):
@@ -462,6 +465,11 @@ def pack_device(W, codes=None, scales=None, stream=None):
 # Torch CUDA tensors in and out; outputs that are not given are allocated.  `stream` (a torch
 # stream or an address) makes the call, its allocations included, on that stream; otherwise it
 # runs on the current stream of the tensors' device.
+#
+# The calls record no autograd graph: the gradients are the *_backward calls', made by hand or from a
+# torch.autograd.Function.  As torch's functions with an out= argument do, they refuse tensors that
+# require grad while grad mode is on, and a tensor that is given to be written counts as changed in
+# place, so that a backward pass that saved its old contents raises instead of using the new ones.
 
 
 # The sizes' answers alone: a model asks for the same few at every step.
@@ -495,6 +503,20 @@ def _run(what, fn, dev, *args):
         raise FeMoeError(status, what)
 
 
+def _refuse_grad(t, name):
+    import torch
+    if torch.is_grad_enabled():
+        raise ValueError(f"{name} requires grad, but this call records no graph: call it under torch.no_grad() or from a "
+                         f"torch.autograd.Function")
+
+
+@functools.cache
+def _bump():
+    """Counts a tuple of tensors as changed in place (without the checks on its argument where torch offers that)."""
+    import torch
+    return getattr(torch._C, "_increment_version", None) or torch.autograd.graph.increment_version
+
+
 def _on_stream(stream, dev):
     """The stream made current, so that what the call allocates belongs to it."""
     import torch
@@ -514,11 +536,22 @@ def _arg(t, name, dtype, shape, dev, optional=False):
     if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} CUDA tensor of shape {tuple(shape)} on {dev} is needed, "
                          f"got {t.dtype} {tuple(t.shape)} strides {tuple(t.stride())} on {t.device}")
+    if t.requires_grad:
+        _refuse_grad(t, name)
+    return t.data_ptr()
+
+
+def _first(t, name, dtype):
+    """_arg for the tensor that the others' shape and device are taken from."""
+    if t.dtype is not dtype or t.requires_grad or not t.is_contiguous():
+        return _arg(t, name, dtype, t.shape, t.device)
     return t.data_ptr()
 
 
 def _arg_rows(t, name, dtype, shape, dev):
     """The address and row stride of a CUDA matrix whose rows are contiguous."""
+    if t.requires_grad:
+        _refuse_grad(t, name)
     if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
         return t.data_ptr(), shape[1] if shape[0] > 1 else (shape[1] + 7) // 8 * 8
     if (t.dtype is not dtype or t.shape != shape or t.device != dev
@@ -549,6 +582,10 @@ def _new(like, dtype, *shape):
     return like.new_empty(*shape) if like.dtype is dtype else like.new_empty(*shape, dtype=dtype)
 
 
+def _given(*outs):
+    return tuple([t for t in outs if t is not None])
+
+
 def _out(t, name, dtype, shape, dev, like):
     if t is None:
         return like.new_empty(*shape) if like.dtype is dtype else like.new_empty(*shape, dtype=dtype)
@@ -577,17 +614,20 @@ def block_norm(r, y=None, w_post=None, w_pre=None, gate=None, gate_kind=GATE_NON
     bf, dev, shape = torch.bfloat16, r.device, r.shape
     T, H = shape
     dt = _dtype_of(r, "r")
-    rp = _arg(r, "r", r.dtype, shape, dev)
+    rp = _first(r, "r", r.dtype)
     yp = _arg(y, "y", bf, shape, dev, True)
     postp = _arg(w_post, "w_post", bf, (H,), dev, True)
     prep = _arg(w_pre, "w_pre", bf, (H,), dev, True)
     gp = _arg_gate(gate, gate_kind, T, H, dev)
+    given = _given(r_out, u)
     if y is not None:
         r_out = _out(r_out, "r_out", r.dtype, shape, dev, r)
     if w_pre is not None:
         u = _out(u, "u", bf, shape, dev, r)
     _run("fe_moe_block_norm", fe_moe_block_norm, dev, rp, dt, yp, postp, gp, gate_kind, scale, prep, eps, T, H,
          _dptr(r_out), _dptr(u))
+    if given:
+        _bump()(given)
     return r_out, u
 
 
@@ -604,7 +644,7 @@ def block_norm_backward(dr_out, du, r, y=None, w_post=None, w_pre=None, gate=Non
     bf, f32, dev, shape = torch.bfloat16, torch.float32, r.device, r.shape
     T, H = shape
     dt = _dtype_of(r, "r")
-    rp = _arg(r, "r", r.dtype, shape, dev)
+    rp = _first(r, "r", r.dtype)
     drop = _arg(dr_out, "dr_out", r.dtype, shape, dev, True)
     dup = _arg(du, "du", bf, shape, dev, True)
     yp = _arg(y, "y", bf, shape, dev, True)
@@ -643,9 +683,10 @@ def balance_loss(logits, idx, mask=None, balance_coef=1.0, z_coef=0.0, loss=None
     i32, f32, dev = torch.int32, torch.float32, logits.device
     T, E = logits.shape
     k = idx.shape[1]
-    lp = _arg(logits, "logits", f32, (T, E), dev)
+    lp = _first(logits, "logits", f32)
     ip = _arg(idx, "idx", i32, (T, k), dev)
     mp = _arg(mask, "mask", torch.uint8, (T,), dev, True)
+    given = _given(loss, counts, n_tokens)
     loss = _out(loss, "loss", f32, (3,), dev, logits)
     counts = _out(counts, "counts", i32, (E,), dev, idx)
     n_tokens = _out(n_tokens, "n_tokens", i32, (1,), dev, idx)
@@ -653,6 +694,8 @@ def balance_loss(logits, idx, mask=None, balance_coef=1.0, z_coef=0.0, loss=None
     ws = logits.new_empty((nb + 3) // 4) if nb else None
     _run("fe_moe_balance_loss", fe_moe_balance_loss, dev, lp, ip, mp, T, E, k, balance_coef, z_coef, loss.data_ptr(),
          counts.data_ptr(), n_tokens.data_ptr(), _dptr(ws), nb)
+    if given:
+        _bump()(given)
     return loss, counts, n_tokens
 
 
@@ -666,15 +709,18 @@ def balance_loss_backward(logits, counts, n_tokens, top_k: int, mask=None, dloss
     import torch
     f32, i32, dev = torch.float32, torch.int32, logits.device
     T, E = logits.shape
-    lp = _arg(logits, "logits", f32, (T, E), dev)
+    lp = _first(logits, "logits", f32)
     cp = _arg(counts, "counts", i32, (E,), dev)
     np_ = _arg(n_tokens, "n_tokens", i32, (1,), dev)
     mp = _arg(mask, "mask", torch.uint8, (T,), dev, True)
     dp = _arg(dloss, "dloss", f32, (1,), dev, True)
+    given = _given(dlogits)
     dlogits = _out(dlogits, "dlogits", dtype or (f32 if dlogits is None else dlogits.dtype), (T, E), dev, logits)
     dt = _dtype_of(dlogits, "dlogits")
     _run("fe_moe_balance_loss_backward", fe_moe_balance_loss_backward, dev, lp, cp, np_, mp, dp, T, E, top_k,
          balance_coef, z_coef, dlogits.data_ptr(), dt)
+    if given:
+        _bump()(given)
     return dlogits
 
 
@@ -695,12 +741,15 @@ def linear(x, w, bias=None, act=ACT_NONE, residual=None, y=None, z=None, stream=
     bp = _arg(bias, "bias", bf, (N,), dev, True)
     zp = _arg(z, "z", bf, (M, N), dev, True)
     resp, ldr = (None, 0) if residual is None else _arg_rows(residual, "residual", bf, out, dev)
+    given = _given(y, z)
     if y is None:
         y = x.new_empty(*out)
         yp, ldy = y.data_ptr(), out[1]
     else:
         yp, ldy = _arg_rows(y, "y", bf, out, dev)
     _run("fe_moe_linear", fe_moe_linear, dev, xp, ldx, wp, bp, resp, ldr, M, N, K, act, yp, ldy, zp)
+    if given:
+        _bump()(given)
     return y
 
 

@@ -143,3 +143,34 @@ def test_the_binding_refuses_before_the_library():
         fe.linear(r, torch.zeros(8, 32, dtype=bf))
     with pytest.raises(ValueError):
         fe.linear_backward(r, r, torch.zeros(64, 64, dtype=bf), act=fe.ACT_SILU)
+
+
+def test_the_binding_refuses_to_lose_a_gradient():
+    """No call records a graph: an operand or a given output that requires grad is refused while grad mode is on, and
+    taken without it (here up to the next check, which wants a GPU)."""
+    bf = torch.bfloat16
+    f = lambda *s, dtype=bf: torch.zeros(*s, dtype=dtype)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    r, w, lg = f(4, 64), f(64), f(4, 8, dtype=torch.float32)
+    kw = dict(y=f(4, 64), w_post=w, w_pre=f(64), gate=f(64), gate_kind=fe.GATE_CHANNEL)
+    calls = [
+        (fe.block_norm, dict(r=r, r_out=f(4, 64), u=f(4, 64), **kw)),
+        (fe.block_norm_backward, dict(dr_out=f(4, 64), du=f(4, 64), r=r, **kw)),
+        (fe.balance_loss, dict(logits=lg, loss=f(3, dtype=torch.float32))),
+        (fe.balance_loss_backward, dict(logits=lg, dloss=f(1, dtype=torch.float32), dlogits=f(4, 8))),
+        (fe.linear, dict(x=r, w=f(32, 64), bias=f(32), residual=f(4, 32), y=f(4, 32), z=f(4, 32))),
+        (fe.linear_backward, dict(dy=f(4, 32), x=r, w=f(32, 64), z=f(4, 32))),
+    ]
+    whole = {fe.balance_loss: dict(idx=i32(4, 2)), fe.balance_loss_backward: dict(counts=i32(8), n_tokens=i32(1), top_k=2)}
+    for fn, args in calls:
+        rest = whole.get(fn, {})
+        with pytest.raises(ValueError, match="CUDA tensors"):
+            fn(**args, **rest)
+        for name, t in args.items():
+            if not isinstance(t, torch.Tensor):
+                continue
+            with_grad = {**args, name: t.clone().requires_grad_()}
+            with pytest.raises(ValueError, match=f"{name} requires grad"):
+                fn(**with_grad, **rest)
+            with torch.no_grad(), pytest.raises(ValueError, match="CUDA tensors"):
+                fn(**with_grad, **rest)
