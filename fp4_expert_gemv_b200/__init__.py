@@ -267,7 +267,6 @@ class MoELayer:
             Is = shared[1].shape[1]
             _arg(shared[0], "shared gate_up", bf, (2 * Is, H), dev)
             _arg(shared[1], "shared down", bf, (H, Is), dev)
-        given = _given(r_out, u_out, logits)
         r_out = _out(r_out, "r_out", r.dtype, (T, H), dev, r)
         if w_next_pre is not None:
             u_out = _out(u_out, "u_out", bf, (T, H), dev, r)
@@ -281,8 +280,8 @@ class MoELayer:
         ws = r.new_empty(max(nb, 16), dtype=torch.uint8)
         _run("fe_moe_forward_block", fe_moe_forward_block, dev, self.h, ctypes.byref(b), _dptr(r), dt, _dptr(u_in), T, top_k,
              _dptr(r_out), _dptr(u_out), _dptr(logits), _dptr(ws), ws.numel())
-        if given:
-            _bump()(given)
+        _written(r_out, u_out)
+        _written(logits, None)
         return r_out, u_out, logits
 
     def forward_host(self, x_bf16_host, logits_host, top_k: int, y_bf16_host, stream=None):
@@ -511,10 +510,22 @@ def _refuse_grad(t, name):
 
 
 @functools.cache
+def _types():
+    """torch.bfloat16, float32 and int32."""
+    import torch
+    return torch.bfloat16, torch.float32, torch.int32
+
+
+@functools.cache
 def _bump():
     """Counts a tuple of tensors as changed in place (without the checks on its argument where torch offers that)."""
     import torch
     return getattr(torch._C, "_increment_version", None) or torch.autograd.graph.increment_version
+
+
+def _written(a, b):
+    """Counts a call's outputs, or the one there is, as changed in place; an output of the call's own does not mind."""
+    _bump()((a,) if b is None else (b,) if a is None else (a, b))
 
 
 def _on_stream(stream, dev):
@@ -567,23 +578,20 @@ def _arg_rows(t, name, dtype, shape, dev):
 
 
 def _arg_gate(gate, kind, T, H, dev):
-    import torch
+    if gate is None and kind == GATE_NONE:
+        return None
     k = kind & ~GATE_SIGMOID
     if k not in (GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL) or (gate is None) != (k == GATE_NONE):
         raise ValueError("gate and gate_kind do not go together")
     if gate is None:
         return None
-    return _arg(gate, "gate", torch.bfloat16, (H,) if k == GATE_CHANNEL else (T,) if k == GATE_TOKEN else (T, H), dev)
+    return _arg(gate, "gate", _types()[0], (H,) if k == GATE_CHANNEL else (T,) if k == GATE_TOKEN else (T, H), dev)
 
 
 def _new(like, dtype, *shape):
     """An uninitialised tensor on like's device (by the cheapest of torch's ways: a third of a small call's host time
     goes into its outputs)."""
     return like.new_empty(*shape) if like.dtype is dtype else like.new_empty(*shape, dtype=dtype)
-
-
-def _given(*outs):
-    return tuple([t for t in outs if t is not None])
 
 
 def _out(t, name, dtype, shape, dev, like):
@@ -594,10 +602,10 @@ def _out(t, name, dtype, shape, dev, like):
 
 
 def _dtype_of(t, name):
-    import torch
-    if t.dtype == torch.bfloat16:
+    bf, f32, _ = _types()
+    if t.dtype is bf:
         return DTYPE_BF16
-    if t.dtype == torch.float32:
+    if t.dtype is f32:
         return DTYPE_F32
     raise ValueError(f"{name}: bfloat16 or float32 is needed, got {t.dtype}")
 
@@ -610,8 +618,8 @@ def block_norm(r, y=None, w_post=None, w_pre=None, gate=None, gate_kind=GATE_NON
     if stream is not None:
         with _on_stream(stream, r.device):
             return block_norm(r, y, w_post, w_pre, gate, gate_kind, scale, eps, r_out, u)
-    import torch
-    bf, dev, shape = torch.bfloat16, r.device, r.shape
+    bf, _, _ = _types()
+    dev, shape = r.device, r.shape
     T, H = shape
     dt = _dtype_of(r, "r")
     rp = _first(r, "r", r.dtype)
@@ -619,15 +627,13 @@ def block_norm(r, y=None, w_post=None, w_pre=None, gate=None, gate_kind=GATE_NON
     postp = _arg(w_post, "w_post", bf, (H,), dev, True)
     prep = _arg(w_pre, "w_pre", bf, (H,), dev, True)
     gp = _arg_gate(gate, gate_kind, T, H, dev)
-    given = _given(r_out, u)
     if y is not None:
         r_out = _out(r_out, "r_out", r.dtype, shape, dev, r)
     if w_pre is not None:
         u = _out(u, "u", bf, shape, dev, r)
     _run("fe_moe_block_norm", fe_moe_block_norm, dev, rp, dt, yp, postp, gp, gate_kind, scale, prep, eps, T, H,
          _dptr(r_out), _dptr(u))
-    if given:
-        _bump()(given)
+    _written(r_out, u)
     return r_out, u
 
 
@@ -641,7 +647,8 @@ def block_norm_backward(dr_out, du, r, y=None, w_post=None, w_pre=None, gate=Non
         with _on_stream(stream, r.device):
             return block_norm_backward(dr_out, du, r, y, w_post, w_pre, gate, gate_kind, scale, eps, weight_grads)
     import torch
-    bf, f32, dev, shape = torch.bfloat16, torch.float32, r.device, r.shape
+    bf, f32, _ = _types()
+    dev, shape = r.device, r.shape
     T, H = shape
     dt = _dtype_of(r, "r")
     rp = _first(r, "r", r.dtype)
@@ -686,7 +693,7 @@ def balance_loss(logits, idx, mask=None, balance_coef=1.0, z_coef=0.0, loss=None
     lp = _first(logits, "logits", f32)
     ip = _arg(idx, "idx", i32, (T, k), dev)
     mp = _arg(mask, "mask", torch.uint8, (T,), dev, True)
-    given = _given(loss, counts, n_tokens)
+    given = loss is not None or counts is not None or n_tokens is not None
     loss = _out(loss, "loss", f32, (3,), dev, logits)
     counts = _out(counts, "counts", i32, (E,), dev, idx)
     n_tokens = _out(n_tokens, "n_tokens", i32, (1,), dev, idx)
@@ -695,7 +702,7 @@ def balance_loss(logits, idx, mask=None, balance_coef=1.0, z_coef=0.0, loss=None
     _run("fe_moe_balance_loss", fe_moe_balance_loss, dev, lp, ip, mp, T, E, k, balance_coef, z_coef, loss.data_ptr(),
          counts.data_ptr(), n_tokens.data_ptr(), _dptr(ws), nb)
     if given:
-        _bump()(given)
+        _bump()((loss, counts, n_tokens))
     return loss, counts, n_tokens
 
 
@@ -714,13 +721,11 @@ def balance_loss_backward(logits, counts, n_tokens, top_k: int, mask=None, dloss
     np_ = _arg(n_tokens, "n_tokens", i32, (1,), dev)
     mp = _arg(mask, "mask", torch.uint8, (T,), dev, True)
     dp = _arg(dloss, "dloss", f32, (1,), dev, True)
-    given = _given(dlogits)
     dlogits = _out(dlogits, "dlogits", dtype or (f32 if dlogits is None else dlogits.dtype), (T, E), dev, logits)
     dt = _dtype_of(dlogits, "dlogits")
     _run("fe_moe_balance_loss_backward", fe_moe_balance_loss_backward, dev, lp, cp, np_, mp, dp, T, E, top_k,
          balance_coef, z_coef, dlogits.data_ptr(), dt)
-    if given:
-        _bump()(given)
+    _written(dlogits, None)
     return dlogits
 
 
@@ -731,17 +736,20 @@ def linear(x, w, bias=None, act=ACT_NONE, residual=None, y=None, z=None, stream=
     if stream is not None:
         with _on_stream(stream, x.device):
             return linear(x, w, bias, act, residual, y, z)
-    import torch
-    bf, dev = torch.bfloat16, x.device
+    bf, _, _ = _types()
+    dev = x.device
     M, K = x.shape
     N = w.shape[0]
     out = (M, N // 2 if act == ACT_SWIGLU else N)
-    xp, ldx = _arg_rows(x, "x", bf, (M, K), dev)
+    if x.dtype is bf and not x.requires_grad and x.is_contiguous():
+        xp, ldx = x.data_ptr(), K
+    else:
+        xp, ldx = _arg_rows(x, "x", bf, (M, K), dev)
     wp = _arg(w, "w", bf, (N, K), dev)
     bp = _arg(bias, "bias", bf, (N,), dev, True)
     zp = _arg(z, "z", bf, (M, N), dev, True)
     resp, ldr = (None, 0) if residual is None else _arg_rows(residual, "residual", bf, out, dev)
-    given = _given(y, z)
+    given = y is not None or z is not None
     if y is None:
         y = x.new_empty(*out)
         yp, ldy = y.data_ptr(), out[1]
@@ -749,7 +757,7 @@ def linear(x, w, bias=None, act=ACT_NONE, residual=None, y=None, z=None, stream=
         yp, ldy = _arg_rows(y, "y", bf, out, dev)
     _run("fe_moe_linear", fe_moe_linear, dev, xp, ldx, wp, bp, resp, ldr, M, N, K, act, yp, ldy, zp)
     if given:
-        _bump()(given)
+        _written(y, z)
     return y
 
 
