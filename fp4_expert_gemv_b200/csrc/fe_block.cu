@@ -1065,7 +1065,7 @@ fe_status fe_moe_linear_backward(const void* dy, int64_t lddy, const void* x, in
     const fe_status st = check_linear_shape(M, N, K, act);
     if (st != FE_OK) return st;
     const int cols = out_cols(act, N);
-    if (!dx && !dw && !db) return FE_ERR_INVALID_ARG;
+    if (M > 0 && !dx && !dw && !db) return FE_ERR_INVALID_ARG;   // dx of no rows may have no address
     const size_t nx = span(M, ldx, K), ndx = span(M, lddx, K), nw = 2 * (size_t)N * K, nz = 2 * (size_t)M * N;
     const size_t ndy = span(M, lddy, cols);
     const size_t need = fe_moe_linear_workspace(M, N, K, act);

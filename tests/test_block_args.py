@@ -174,3 +174,10 @@ def test_the_binding_refuses_to_lose_a_gradient():
                 fn(**with_grad, **rest)
             with torch.no_grad(), pytest.raises(ValueError, match="CUDA tensors"):
                 fn(**with_grad, **rest)
+
+
+def test_linear_backward_of_no_rows_may_have_no_dx():
+    """The gradient of an empty x has no address (torch gives an empty tensor none)."""
+    none = dict(M=0, dy=None, x=None, z=None, dx=None, dw=None, db=None, ws=None, nb=0)
+    assert linear_bwd(**none) == OK and linear_bwd(**none, act=0) == OK
+    assert linear_bwd(**{**none, "M": 1}) == INV

@@ -314,3 +314,10 @@ def test_refusals():
         fe.linear(x[:, 4:60], w[:, :56].contiguous())      # rows not on 16 bytes
     with pytest.raises(fe.FeMoeError):
         fe.linear(x, w, y=x[:, :32])
+
+
+def test_no_rows_and_the_gradient_of_x_alone():
+    import fp4_expert_gemv_b200 as fe
+    x, w, _, _, dy = make(0, 32, 64, "none")
+    dx, dw, db = fe.linear_backward(dy, x, w, need_dw=False, need_db=False)
+    assert dx.shape == (0, 64) and dw is None and db is None
