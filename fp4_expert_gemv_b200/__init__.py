@@ -99,6 +99,7 @@ _SIGS = {
     "fe_moe_balance_loss_backward": (_st, [_P, _P, _P, _P, _P, _i64, _i32, _i32, _f32, _f32, _P, _i32, _P]),
     "fe_moe_linear": (_st, [_P, _i64, _P, _P, _P, _i64, _i64, _i32, _i32, _i32, _P, _i64, _P, _P]),
     "fe_moe_linear_workspace": (_sz, [_i64, _i32, _i32, _i32]),
+    "fe_moe_linear_backward_workspace": (_sz, [_i64, _i32, _i32, _i32, _i32, _i32, _i32, _i32]),
     "fe_moe_linear_backward": (_st, [_P, _i64, _P, _i64, _P, _P, _i64, _i32, _i32, _i32, _P, _i64, _P, _P, _P, _sz, _P]),
     "fe_moe_get_op_status": (_st, [ctypes.POINTER(ctypes.c_uint32)]),
     "fe_moe_forward_block_workspace": (_sz, [_P, _i32, _i32]),
@@ -472,9 +473,9 @@ def pack_device(W, codes=None, scales=None, stream=None):
 
 
 # The sizes' answers alone: a model asks for the same few at every step.
-_norm_workspace, _balance_workspace, _linear_workspace = (
+_norm_workspace, _balance_workspace, _linear_backward_workspace = (
     functools.lru_cache(1024)(lambda *sizes, query=query: query(*sizes))
-    for query in (fe_moe_block_norm_workspace, fe_moe_balance_workspace, fe_moe_linear_workspace))
+    for query in (fe_moe_block_norm_workspace, fe_moe_balance_workspace, fe_moe_linear_backward_workspace))
 
 
 @functools.cache
@@ -778,10 +779,10 @@ def linear_backward(dy, x, w, z=None, act=ACT_NONE, need_dx=True, need_dw=True, 
     dx = (torch.empty_like(x) if x.is_contiguous() else x.new_empty(M, K)) if need_dx else None
     dw = torch.empty_like(w) if need_dw else None
     db = _new(x, torch.float32, N) if need_db else None
-    nb = _linear_workspace(M, N, K, act)
-    ws = x.new_empty(max((nb + 1) // 2, 8))
+    nb = _linear_backward_workspace(M, N, K, act, lddy % 8 == 0 and dyp % 16 == 0, need_dx, need_dw, need_db)
+    ws = x.new_empty((nb + 1) // 2) if nb else None
     _run("fe_moe_linear_backward", fe_moe_linear_backward, dev, dyp, lddy, xp, ldx, wp, zp, M, N, K, act, _dptr(dx),
-         K, _dptr(dw), _dptr(db), ws.data_ptr(), nb)
+         K, _dptr(dw), _dptr(db), _dptr(ws), nb)
     return dx, dw, db
 
 

@@ -739,8 +739,12 @@ cudaError_t dz_launch(int act, dim3 grid, const fe::LinDzParams& p, cudaStream_t
     return launch(fe::linear_dz_kernel<VEC, fe::kActNone>, grid, 256, 0, s, p);
 }
 
-// Backward workspace: dz [M][roundup8(N)] bf16, then the column partials.
+// Backward workspace: dz [M][roundup8(N)] bf16 where it is written, then the column partials behind db.
 int dz_chunks(int64_t M) { return (int)std::max<int64_t>(1, std::min<int64_t>(256, (M + 31) / 32)); }
+size_t dz_bytes(int64_t M, int N, bool written) { return written ? align256(2 * (size_t)M * (((size_t)N + 7) / 8 * 8)) : 0; }
+size_t db_bytes(int64_t M, int N, bool db) { return db ? sizeof(float) * (size_t)dz_chunks(M) * N : 0; }
+// dz is dy itself without an activation, when its rows suit TMA; db alone needs none.
+bool dz_written(int act, bool dy_rows16, bool dx, bool dw) { return (dx || dw) && !(act == FE_ACT_NONE && dy_rows16); }
 
 }  // namespace
 
@@ -1054,8 +1058,13 @@ fe_status fe_moe_linear(const void* x, int64_t ldx, const void* w, const void* b
 
 size_t fe_moe_linear_workspace(int64_t M, int N, int K, int act)
 {
+    return fe_moe_linear_backward_workspace(M, N, K, act, 0, 1, 1, 1);
+}
+
+size_t fe_moe_linear_backward_workspace(int64_t M, int N, int K, int act, int dy_rows16, int dx, int dw, int db)
+{
     if (check_linear_shape(M, N, K, act) != FE_OK) return 0;
-    return align256(2 * (size_t)M * (((size_t)N + 7) / 8 * 8)) + sizeof(float) * (size_t)dz_chunks(M) * N;
+    return dz_bytes(M, N, dz_written(act, dy_rows16, dx, dw)) + db_bytes(M, N, db);
 }
 
 fe_status fe_moe_linear_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w, const void* z,
@@ -1068,10 +1077,11 @@ fe_status fe_moe_linear_backward(const void* dy, int64_t lddy, const void* x, in
     if (M > 0 && !dx && !dw && !db) return FE_ERR_INVALID_ARG;   // dx of no rows may have no address
     const size_t nx = span(M, ldx, K), ndx = span(M, lddx, K), nw = 2 * (size_t)N * K, nz = 2 * (size_t)M * N;
     const size_t ndy = span(M, lddy, cols);
-    const size_t need = fe_moe_linear_workspace(M, N, K, act);
+    const bool rows16 = lddy % 8 == 0 && aligned(dy, 16), dz_buf = dz_written(act, rows16, dx, dw);
+    const size_t need = M > 0 ? dz_bytes(M, N, dz_buf) + db_bytes(M, N, db) : 0;
     if (M > 0) {
         if (!dy || lddy < cols || (act != FE_ACT_NONE && !z) || (dx && (!w || lddx < K)) || (dw && (!x || ldx < K)) ||
-            !workspace || !aligned(workspace, 16))
+            (need > 0 && (!workspace || !aligned(workspace, 16))))
             return FE_ERR_INVALID_ARG;
         if (dw && ldx % 8 != 0) return FE_ERR_UNSUPPORTED;
         if (!aligned(dy, 2) || !aligned(z, 2) || (dw && !aligned(x, 16)) || (dx && !aligned(w, 16))) return FE_ERR_INVALID_ARG;
@@ -1080,7 +1090,7 @@ fe_status fe_moe_linear_backward(const void* dy, int64_t lddy, const void* x, in
     if (!aligned(dx, 2) || !aligned(dw, 2) || !aligned(db, 4)) return FE_ERR_INVALID_ARG;
     const void* ins[4] = {dy, dw ? x : nullptr, dx ? w : nullptr, act != FE_ACT_NONE ? z : nullptr};
     const size_t in_n[4] = {ndy, nx, nw, nz};
-    const void* outs[4] = {dx, dw, db, M > 0 ? workspace : nullptr};
+    const void* outs[4] = {dx, dw, db, need > 0 ? workspace : nullptr};
     const size_t out_n[4] = {ndx, nw, 4 * (size_t)N, need};
     for (int i = 0; i < 4; ++i) {
         for (int j = 0; j < 4; ++j)
@@ -1094,20 +1104,18 @@ fe_status fe_moe_linear_backward(const void* dy, int64_t lddy, const void* x, in
         if (db) FE_CUDA_TRY(cudaMemsetAsync(db, 0, 4 * (size_t)N, s));
         return FE_OK;
     }
-    // dZ: dY itself without an activation, when its rows suit TMA
-    const bool direct = act == FE_ACT_NONE && lddy % 8 == 0 && aligned(dy, 16);
+    const bool direct = act == FE_ACT_NONE && rows16;   // dZ is dY itself
     const int64_t lddz = direct ? lddy : ((int64_t)N + 7) / 8 * 8;
     uint16_t* dzbuf = static_cast<uint16_t*>(workspace);
     const void* dz = direct ? dy : dzbuf;
-    float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                           align256(2 * (size_t)M * (((size_t)N + 7) / 8 * 8)));
+    float* part = reinterpret_cast<float*>(static_cast<char*>(workspace) + dz_bytes(M, N, dz_buf));
     int partials = 0;
     if (!direct || db) {
         fe::LinDzParams p{};
         p.dy = static_cast<const uint16_t*>(dy);
         p.lddy = lddy;
         p.z = static_cast<const uint16_t*>(z);
-        p.dz = direct || (!dx && !dw) ? nullptr : dzbuf;
+        p.dz = dz_buf ? dzbuf : nullptr;
         p.lddz = lddz;
         p.part = db ? part : nullptr;
         p.M = M;

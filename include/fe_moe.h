@@ -531,16 +531,22 @@ fe_status fe_moe_balance_loss_backward(const float* logits, const int32_t* count
 fe_status fe_moe_linear(const void* x, int64_t ldx, const void* w, const void* bias, const void* residual, int64_t ldr,
                         int64_t M, int N, int K, int act, void* y, int64_t ldy, void* z, fe_stream_t stream);
 
-/* Bytes of workspace fe_moe_linear_backward needs (0 for sizes it refuses). */
+/* Bytes of workspace that are enough for any fe_moe_linear_backward of these sizes (0
+ * for sizes it refuses). */
 size_t fe_moe_linear_workspace(int64_t M, int N, int K, int act);
+
+/* What a call that asks for these outputs needs (dx, dw, db: 0 or 1): room for dz with
+ * dx or dw, unless there is no activation and dy's base and row stride are multiples of
+ * 16 bytes (dy_rows16), and for partial sums with db. */
+size_t fe_moe_linear_backward_workspace(int64_t M, int N, int K, int act, int dy_rows16, int dx, int dw, int db);
 
 /* Its gradients: dz = dy * act'(z) (0 at a relu's zero), dx = dz w, dw = dz^T x, db =
  * sum over rows of dz; the residual's gradient is dy.  dy bf16 [M][C], row stride
  * lddy; z as the forward call wrote it (NULL without an activation).  dz is rounded
  * to bf16 as an operand of the two products; db sums it unrounded.  Outputs, each optional
  * (at least one): dx bf16 [M][K] (row stride lddx), dw bf16 [N][K], db float [N]; x
- * is needed for dw, w for dx.  workspace 16-byte aligned.  M = 0 writes zeros to dw
- * and db. */
+ * is needed for dw, w for dx.  workspace 16-byte aligned, NULL where none is needed;
+ * too small: FE_ERR_CAPACITY.  M = 0 writes zeros to dw and db. */
 fe_status fe_moe_linear_backward(const void* dy, int64_t lddy, const void* x, int64_t ldx, const void* w, const void* z,
                                  int64_t M, int N, int K, int act, void* dx, int64_t lddx, void* dw, float* db,
                                  void* workspace, size_t workspace_bytes, fe_stream_t stream);

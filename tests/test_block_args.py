@@ -181,3 +181,22 @@ def test_linear_backward_of_no_rows_may_have_no_dx():
     none = dict(M=0, dy=None, x=None, z=None, dx=None, dw=None, db=None, ws=None, nb=0)
     assert linear_bwd(**none) == OK and linear_bwd(**none, act=0) == OK
     assert linear_bwd(**{**none, "M": 1}) == INV
+
+
+def test_linear_backward_asks_for_what_it_writes():
+    """dz [M][N rounded up to 8] in bf16 unless dy itself serves, rounded up to 256 bytes, and partial sums of db."""
+    q = fe.fe_moe_linear_backward_workspace
+    for M, N, K, act in ((16, 32, 64, 0), (100, 33, 64, 0), (100, 32, 64, 4), (2_200_000, 1024, 64, 0)):
+        dz = (2 * M * ((N + 7) // 8 * 8) + 255) // 256 * 256
+        db = 4 * N * max(1, min(256, (M + 31) // 32))
+        for rows16 in (0, 1):
+            for dx, dw, b in ((1, 1, 1), (1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 0, 1)):
+                want = (dz if (dx or dw) and not (act == 0 and rows16) else 0) + (db if b else 0)
+                assert q(M, N, K, act, rows16, dx, dw, b) == want, (M, N, act, rows16, dx, dw, b)
+        assert fe.fe_moe_linear_workspace(M, N, K, act) == dz + db
+    assert q(4, 8, 12, 0, 0, 1, 1, 1) == 0
+    # a byte less, or none where some is needed, is refused
+    for kw in (dict(), dict(act=0, z=None, lddy=33, N=32), dict(dx=None, dw=None)):
+        a = dict(dict(M=16, N=32, K=64, act=4, lddy=16, dx=F, dw=G), **kw)
+        nb = q(a["M"], a["N"], a["K"], a["act"], a["lddy"] % 8 == 0, a["dx"] is not None, a["dw"] is not None, 1)
+        assert nb > 0 and linear_bwd(**kw, nb=nb - 1) == CAP and linear_bwd(**kw, nb=nb, ws=None) == INV

@@ -321,3 +321,41 @@ def test_no_rows_and_the_gradient_of_x_alone():
     x, w, _, _, dy = make(0, 32, 64, "none")
     dx, dw, db = fe.linear_backward(dy, x, w, need_dw=False, need_db=False)
     assert dx.shape == (0, 64) and dw is None and db is None
+
+
+@pytest.mark.parametrize("act, odd", [("none", False), ("none", True), ("gelu", False)])
+@pytest.mark.parametrize("M", [1, 70, 1000])
+def test_the_workspace_asked_for_is_enough(M, act, odd):
+    """Every set of outputs with exactly the bytes of its query (no workspace at all where that says 0), the bytes behind
+    watched, against the call that is given the most."""
+    import fp4_expert_gemv_b200 as fe
+    N, K = 264, 136
+    x, w, bias, _, dy = make(M, N, K, act, seed=M)
+    ld = 267 if odd else N
+    rows = torch.zeros(M, ld, dtype=bf, device="cuda")
+    rows[:, :N] = dy
+    z = torch.empty(M, N, dtype=bf, device="cuda")
+    fe.linear(x, w, bias=bias, act=act_id(fe, act), z=z)
+    stream = torch.cuda.current_stream().cuda_stream
+
+    def call(outs, ws, nb):
+        dx, dw, db = (torch.full(s, 5.0, dtype=t, device="cuda") if o else None
+                      for o, s, t in zip(outs, ((M, K), (N, K), (N,)), (bf, bf, torch.float32)))
+        ptr = lambda t: None if t is None else t.data_ptr()
+        st = fe.fe_moe_linear_backward(rows.data_ptr(), ld, x.data_ptr(), K, w.data_ptr(), z.data_ptr() if act != "none" else None,
+                                       M, N, K, act_id(fe, act), ptr(dx), K, ptr(dw), ptr(db), ptr(ws), nb, stream)
+        assert st == fe.FE_OK
+        return dx, dw, db
+
+    most = fe.fe_moe_linear_workspace(M, N, K, act_id(fe, act))
+    want = call((1, 1, 1), torch.empty(most, dtype=torch.uint8, device="cuda"), most)
+    for outs in ((1, 1, 1), (1, 1, 0), (1, 0, 0), (0, 1, 0), (0, 0, 1)):
+        nb = fe.fe_moe_linear_backward_workspace(M, N, K, act_id(fe, act), not odd, *outs)
+        assert nb > 0 or (act == "none" and not odd and not outs[2])
+        ws = torch.full((nb + 4096,), 85, dtype=torch.uint8, device="cuda") if nb else None
+        got = call(outs, ws, nb)
+        for o, a, b in zip(outs, got, want):
+            assert not o or torch.equal(a, b)
+        assert ws is None or (ws[nb:] == 85).all()
+    torch.cuda.synchronize()
+    assert fe.op_status() == (fe.FE_OK, 0)
