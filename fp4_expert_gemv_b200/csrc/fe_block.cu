@@ -47,8 +47,9 @@ int sm_count()
     return n;
 }
 
-// The workspace sizes must not depend on the device that is current when they are asked for.
-constexpr int kMaxPartials = 512;
+// CTAs that leave partial sums over rows, at most: two on each of 148 SMs.  The workspace sizes must not depend
+// on the device that is current when they are asked for, so a grid keeps to this number instead.
+constexpr int kMaxPartials = 296;
 
 // Every kernel here begins with griddepcontrol.wait, so its launch may overlap the tail of the
 // kernel before it on the stream.
@@ -168,7 +169,7 @@ bool norm_ring_plan(int64_t T, int H, uint32_t stage, int sms, NormRingPlan* b)
         b->smem = (size_t)groups * (b->stages * stage + fe::norm_group_extra(b->tpr, b->stages));
         if (b->smem <= kNormRingSmem) break;
     }
-    b->grid = (int)std::min<int64_t>(sms, (T + groups - 1) / groups);
+    b->grid = (int)std::min<int64_t>(std::min(sms, kMaxPartials), (T + groups - 1) / groups);
     return b->stages >= 2;
 }
 
@@ -213,7 +214,7 @@ cudaError_t norm_bwd_columns(const fe::NormBwdParams& q, int sms, int* partials,
     static std::atomic<bool> ready[64];
     const int H = q.f.H, tpr = std::min(512, norm_threads(H, 1)), groups = 512 / tpr;
     const size_t smem = sizeof(float) * groups * (2 * (size_t)fe::norm_red_floats(tpr) + 2 * (size_t)H);
-    *partials = (int)std::min<int64_t>(2 * sms, (q.f.T + groups - 1) / groups);
+    *partials = (int)std::min<int64_t>(std::min(2 * sms, kMaxPartials), (q.f.T + groups - 1) / groups);
     const auto kernel = fe::block_norm_backward_any_kernel<R32, GATE, ALL>;
     const cudaError_t e = norm_ring_ready(kernel, ready);
     if (e != cudaSuccess) return e;

@@ -200,3 +200,9 @@ def test_linear_backward_asks_for_what_it_writes():
         a = dict(dict(M=16, N=32, K=64, act=4, lddy=16, dx=F, dw=G), **kw)
         nb = q(a["M"], a["N"], a["K"], a["act"], a["lddy"] % 8 == 0, a["dx"] is not None, a["dw"] is not None, 1)
         assert nb > 0 and linear_bwd(**kw, nb=nb - 1) == CAP and linear_bwd(**kw, nb=nb, ws=None) == INV
+
+
+def test_the_norms_workspace_is_what_the_partials_take():
+    """Three sums of H floats from each of up to two CTAs on 148 SMs, a row each at least."""
+    for T, H in ((1, 8), (100, 2048), (296, 64), (4096, 2048), (1 << 30, 16384)):
+        assert fe.fe_moe_block_norm_workspace(T, H) == 12 * H * min(T, 2 * 148)
