@@ -12,12 +12,15 @@
 
 #include "../../include/fe_moe.h"
 #include "balance.cuh"
+#include "block_plan.cuh"
 #include "common.cuh"
 #include "host.h"
 #include "linear.cuh"
 #include "norm.cuh"
 
 using fe_host::record_cuda;
+
+using namespace fe_plan;
 
 namespace {
 
@@ -30,8 +33,6 @@ namespace {
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 using fe_host::overlap;
-
-size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 // SMs of the current device (looked up once per device).
 int sm_count()
@@ -46,10 +47,6 @@ int sm_count()
     }
     return n;
 }
-
-// CTAs that leave partial sums over rows, at most: two on each of 148 SMs.  The workspace sizes must not depend
-// on the device that is current when they are asked for, so a grid keeps to this number instead.
-constexpr int kMaxPartials = 296;
 
 // Every kernel here begins with griddepcontrol.wait, so its launch may overlap the tail of the
 // kernel before it on the stream.
@@ -70,14 +67,6 @@ cudaError_t launch(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
 }
 
 // ---- norms ------------------------------------------------------------------------------
-
-// Threads of a row: 8 elements each, as many as cover the row, from one warp to 1024.
-int norm_threads(int H, int chunk)
-{
-    int tpr = 32;
-    while (tpr < 1024 && tpr * 8 * chunk < H) tpr *= 2;
-    return tpr;
-}
 
 size_t dtype_bytes(int dt) { return dt == FE_DTYPE_F32 ? 4 : 2; }
 
@@ -150,29 +139,6 @@ cudaError_t norm_launch(const fe::NormParams& p, bool r32, int tpr, cudaStream_t
                : launch(fe::block_norm_kernel<1, C, false>, grid, threads, 0, s, p, tpr);
 }
 
-// The streamed kernels' launch: groups of tpr threads with 16 columns each, a CTA of 512 threads per SM, as
-// many stages (to four) as fit.
-struct NormRingPlan {
-    int tpr, threads, stages, grid;
-    size_t smem;
-};
-
-constexpr size_t kNormRingSmem = 220 * 1024;
-
-bool norm_ring_plan(int64_t T, int H, uint32_t stage, int sms, NormRingPlan* b)
-{
-    b->tpr = norm_threads(H, fe::kRingC);
-    if (b->tpr > 512) return false;
-    b->threads = 512;
-    const int groups = b->threads / b->tpr;
-    for (b->stages = 4; b->stages >= 2; --b->stages) {
-        b->smem = (size_t)groups * (b->stages * stage + fe::norm_group_extra(b->tpr, b->stages));
-        if (b->smem <= kNormRingSmem) break;
-    }
-    b->grid = (int)std::min<int64_t>(std::min(sms, kMaxPartials), (T + groups - 1) / groups);
-    return b->stages >= 2;
-}
-
 // Opts a kernel into kNormRingSmem of shared memory, once per device.
 template <typename K>
 cudaError_t norm_ring_ready(K kernel, std::atomic<bool>* ready)
@@ -212,13 +178,12 @@ template <bool R32, int GATE, bool ALL>
 cudaError_t norm_bwd_columns(const fe::NormBwdParams& q, int sms, int* partials, cudaStream_t s)
 {
     static std::atomic<bool> ready[64];
-    const int H = q.f.H, tpr = std::min(512, norm_threads(H, 1)), groups = 512 / tpr;
-    const size_t smem = sizeof(float) * groups * (2 * (size_t)fe::norm_red_floats(tpr) + 2 * (size_t)H);
-    *partials = (int)std::min<int64_t>(std::min(2 * sms, kMaxPartials), (q.f.T + groups - 1) / groups);
+    const NormColumnsPlan b = norm_columns_plan(q.f.T, q.f.H, sms);
+    *partials = b.grid;
     const auto kernel = fe::block_norm_backward_any_kernel<R32, GATE, ALL>;
     const cudaError_t e = norm_ring_ready(kernel, ready);
     if (e != cudaSuccess) return e;
-    return launch(kernel, *partials, 512, smem, s, q, tpr);
+    return launch(kernel, b.grid, b.threads, b.smem, s, q, b.tpr);
 }
 
 // Through the ring when rows are whole aligned chunks and every operand is there, else column by column.
@@ -230,7 +195,7 @@ cudaError_t norm_bwd_any(const fe::NormBwdParams& q, bool vec, int sms, int* par
     NormRingPlan b;
     if (vec && q.f.y && q.du && q.dr_out &&
         norm_ring_plan(q.f.T, H, fe::norm_bwd_stage(H, R32, GATE == fe::kByElement), sms, &b)) {
-        b.smem = std::max(b.smem, sizeof(float) * 3 * H * (b.threads / b.tpr));   // the groups' column sums at the end
+        b.smem = std::max(b.smem, norm_ring_sums(b, H));
         *partials = b.grid;
         const auto kernel = fe::block_norm_backward_ring_kernel<R32, GATE>;
         const cudaError_t e = norm_ring_ready(kernel, ring_ready);
@@ -250,34 +215,6 @@ cudaError_t norm_bwd(const fe::NormBwdParams& q, bool vec, int sms, int* partial
 }
 
 // ---- balance loss -------------------------------------------------------------------------
-
-// Lanes that hold a row of E logits, 16 values each (32 beyond 512).
-int balance_lanes(int E)
-{
-    int l = 1;
-    while (l < 32 && 16 * l < E) l *= 2;
-    return l;
-}
-
-// CTAs of the forward pass: a group of rows per warp, up to kMaxBalanceCtas of them.
-constexpr int kMaxBalanceCtas = 444;
-int balance_ctas(int64_t T, int E)
-{
-    const int rows = fe::kBalWarps * (32 / balance_lanes(E));
-    return (int)std::max<int64_t>(1, std::min<int64_t>(kMaxBalanceCtas, (T + rows - 1) / rows));
-}
-
-// Rows that one cluster takes by itself, two groups per warp: with the rows in registers (64 x 128: 3.9 us),
-// then through the rings, which have more warps but want whole 16-byte pieces (1024 x 128: 7.4 us, 8.1 from
-// registers).  Beyond, two launches are faster: 2048 x 128 takes 8.2 us, 9.2 in one; 4096 8.9, 13.3 in one,
-// as eight SMs take in too little.
-int64_t balance_small(int E) { return (int64_t)2 * fe::kBalCluster * fe::kBalWarps * (32 / balance_lanes(E)); }
-
-bool balance_fused(int64_t T, int E)
-{
-    if (E % 4 != 0) return T <= 2 * balance_small(E);
-    return T <= (int64_t)2 * fe::kBalCluster * fe::bal_ring_warps(E > 512 ? 32 : 16) * (32 / balance_lanes(E));
-}
 
 fe_status check_balance(const float* logits, const uint8_t*, int64_t T, int E, int top_k)
 {
@@ -305,24 +242,12 @@ cudaError_t balance_run(const fe::BalanceParams& p, bool backward, int grid, cud
     return cudaLaunchKernelEx(&cfg, fe::balance_kernel<L, N, VEC>, p);
 }
 
-// Dynamic shared memory of the streamed pass, and the stages of a warp's ring (to eight) that fit, each a
-// group of 32 / L rows.
-constexpr int balance_ring_room(int L, int N)
-{
-    return fe::kBalRingSmem - 4 * L * N - 1024 - 8 * fe::kBalRingStages * fe::bal_ring_warps(N);
-}
-
-int balance_stages(int E, int L, int N)
-{
-    return std::min(fe::kBalRingStages, balance_ring_room(L, N) / (4 * (32 / L) * E * fe::bal_ring_warps(N)));
-}
-
 template <int L, int N>
 cudaError_t balance_ring_run(const fe::BalanceParams& p, cudaStream_t s)
 {
     static std::atomic<bool> ready[64];
     const int W = fe::bal_ring_warps(N), stages = balance_stages(p.E, L, N);
-    const size_t smem = std::max((size_t)stages * W * 4 * (32 / L) * p.E, sizeof(float) * W * L * N);
+    const size_t smem = balance_ring_smem(p.E, L, N);
     const auto kernel = fe::balance_ring_kernel<L, N>;
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -481,38 +406,6 @@ cudaError_t lin_pairs(int* pairs)
     return cudaSuccess;
 }
 
-// Shares out two problems' tiles, the first's (fewer and longer) evenly, the second's so that the pairs
-// end together: the smallest finish time, found by bisection, that has room for all of them.
-void lin_share(fe::LinParams& P, int pairs)
-{
-    const int64_t ca = (P.p[0].K + 63) / 64 + 2, cb = (P.p[1].K + 63) / 64 + 2;   // k steps, and a tile's ends
-    const int na = P.p[0].tiles, nb = P.p[1].tiles;
-    auto load = [&](int c) { return (int64_t)(na / pairs + (c < na % pairs ? 1 : 0)) * ca; };
-    const int64_t la = load(0), lb = load(pairs - 1);
-    const int xa = na % pairs;
-    auto room = [&](int64_t L) {
-        return (L > la ? (L - la) / cb : 0) * xa + (L > lb ? (L - lb) / cb : 0) * (pairs - xa);
-    };
-    int64_t lo = 0, hi = la + cb * ((int64_t)nb + 1);
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) / 2;
-        if (room(mid) >= nb) hi = mid;
-        else lo = mid + 1;
-    }
-    int ta = 0, tb = 0;
-    for (int c = 0; c < pairs; ++c) {
-        P.start[0][c] = ta;
-        P.start[1][c] = tb;
-        ta += na / pairs + (c < xa ? 1 : 0);
-        const int64_t l = load(c);
-        tb += (int)std::min<int64_t>(nb - tb, lo > l ? (lo - l) / cb : 0);
-    }
-    P.start[0][pairs] = na;
-    P.start[1][pairs] = nb;
-}
-
-int lin_tile_cols(const fe::LinProblem& p, int BN) { return p.act == FE_ACT_SWIGLU ? BN / 2 : BN; }
-
 template <int BN, bool PLAIN>
 cudaError_t lin_launch(fe::LinParams& P, const Product* f, int n, cudaStream_t s)
 {
@@ -553,31 +446,10 @@ cudaError_t lin_run(fe::LinParams& P, const Product* f, int n, cudaStream_t s)
         p.vec_res = p.res && tma_rows(p.res, p.M, p.ldr);
         p.vec_z = p.z && tma_rows(p.z, p.M, p.N) && (p.act != FE_ACT_SWIGLU || p.cols % 8 == 0);
     }
-    // The tile width whose busiest pair has least to do.  A k step of 256 columns takes 512 cycles of
-    // products; narrower ones less, but a little more per column (A is read as often).
     int pairs = 0;
     const cudaError_t e = lin_pairs<256, true>(&pairs);
     if (e != cudaSuccess) return e;
-    const int widths[3] = {256, 192, 128};
-    const int64_t cost[3] = {512, 392, 272};
-    int best = 0;
-    int64_t least = INT64_MAX;
-    for (int w = 0; w < 3; ++w) {
-        int64_t total = 0, longest = 0;
-        for (int i = 0; i < n; ++i) {
-            const int tc = lin_tile_cols(P.p[i], widths[w]);
-            const int64_t tiles = (int64_t)((P.p[i].cols + tc - 1) / tc) * ((P.p[i].M + fe::kLinM - 1) / fe::kLinM);
-            const int64_t steps = (P.p[i].K + 63) / 64 + 2;
-            if (n == 1) total = (tiles + pairs - 1) / pairs * steps * pairs;
-            else total += tiles * steps;
-            longest = std::max(longest, steps);
-        }
-        const int64_t c = std::max((total + pairs - 1) / pairs, longest) * cost[w];
-        if (c < least) {
-            least = c;
-            best = w;
-        }
-    }
+    const int best = lin_width(P, n, pairs);
     bool plain = true;   // nothing but the product: the lean epilogue
     for (int i = 0; i < n; ++i) plain &= P.p[i].act == FE_ACT_NONE && !P.p[i].bias && !P.p[i].res && !P.p[i].z;
     if (plain)
@@ -588,8 +460,6 @@ cudaError_t lin_run(fe::LinParams& P, const Product* f, int n, cudaStream_t s)
            : best == 1 ? lin_launch<192, false>(P, f, n, s)
                        : lin_launch<128, false>(P, f, n, s);
 }
-
-constexpr int kSplSmem = 227 * 1024;   // all that a CTA can have
 
 // Products of few tiles, the contraction split over clusters.
 template <bool GLU, int BN, bool VEC>
@@ -621,9 +491,7 @@ cudaError_t split_launch(const fe::LinProblem& q, const Product& f, int splits, 
     p.ldr = q.ldr;
     p.vec_res = q.cols % 8 == 0 && q.ldr % 8 == 0 && aligned(q.res, 16);
     p.res_bytes = q.res ? 128 / splits * w * 2 : 0;
-    const int steps = (f.K + 63) / 64;
-    p.stages = std::min(fe::kSplMaxStages, (steps + splits - 1) / splits);
-    while (fe::spl_smem(BN, p.stages, p.res_bytes) > kSplSmem) --p.stages;
+    p.stages = split_stages(f.K, BN, splits, p.res_bytes);
     p.out = q.out;
     p.ldo = q.ldo;
     p.z = q.z;
@@ -652,17 +520,19 @@ cudaError_t split_run(const fe::LinProblem& q, const Product& f, int BN, int spl
     return vec ? split_launch<GLU, 128, true>(q, f, splits, s) : split_launch<GLU, 128, false>(q, f, splits, s);
 }
 
-// Clusters of 2^lg CTAs, one to an SM, that run at once (looked up once per device): a cluster lies within
-// one of the GPU's groups of SMs, so those of 8 leave some of them over.
-cudaError_t split_room(int lg, int* clusters)
+// Clusters of 2^lg CTAs, one to an SM, that run at once, lg to 3 (looked up once per device): a cluster lies
+// within one of the GPU's groups of SMs, so those of 8 leave some of them over.
+cudaError_t split_room(int (&room)[4])
 {
     static std::atomic<int> known[64][4];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    int n = known[dev][lg].load(std::memory_order_acquire);
-    if (n == 0) {
+    for (int lg = 0; lg <= 3; ++lg) {
+        int& n = room[lg];
+        n = known[dev][lg].load(std::memory_order_acquire);
+        if (n != 0) continue;
         e = cudaFuncSetAttribute(fe::linear_split_kernel<false, 128, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSplSmem);
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg = {};
@@ -680,39 +550,16 @@ cudaError_t split_room(int lg, int* clusters)
         if (n < 1) return cudaErrorLaunchOutOfResources;
         known[dev][lg].store(n, std::memory_order_release);
     }
-    *clusters = n;
     return cudaSuccess;
 }
 
-// CTAs that share a tile's contraction (a power of two, to 8) and the tile's columns: of those whose
-// clusters all run at once, with two k steps or more a CTA, the least that an SM has to take in, which is
-// what bounds these products: its k steps' operands at 72 bytes a clock (measured), and its share of the
-// other CTAs' partial sums, which cross between SMs at a fifth of that.  1024 x 1000, K = 2048: 9.5 us with
-// 128 columns and two CTAs, 10.6 us with 64 and no split; 256 x 2048, K = 768: 5.6 us with 64 columns and
-// two, 7.6 us with 128 and four.  0 if the tiles alone fill the SMs.
+// split_choice for the current device; ways 0 if the tiles alone fill the SMs.
 cudaError_t split_ways(const fe::LinProblem& q, const Product& f, int* ways, int* BN)
 {
-    *ways = 0;
-    int64_t least = INT64_MAX;
-    const int steps = (f.K + 63) / 64;
-    for (const int bn : {64, 128}) {
-        const int w = lin_tile_cols(q, bn);
-        const int64_t tiles = (int64_t)((q.cols + w - 1) / w) * ((f.M + 127) / 128);
-        for (int lg = bn == 64 ? 0 : 1; lg <= 3; ++lg) {   // 128 columns' sums and stages fit with a split only
-            const int n = 1 << lg;
-            int room = 0;
-            const cudaError_t e = split_room(lg, &room);
-            if (e != cudaSuccess) return e;
-            if (tiles > room || (lg > 0 && steps < 2 * n)) break;
-            const int rows = std::min(f.M, 128);
-            const int64_t cost = (int64_t)((steps + n - 1) / n) * 128 * (rows + bn) + 5 * 4 * bn * rows / n * (n - 1);
-            if (cost < least) {
-                least = cost;
-                *ways = n;
-                *BN = bn;
-            }
-        }
-    }
+    int room[4];
+    const cudaError_t e = split_room(room);
+    if (e != cudaSuccess) return e;
+    split_choice(q.act == FE_ACT_SWIGLU, q.cols, f.M, f.K, room, ways, BN);
     return cudaSuccess;
 }
 
@@ -739,13 +586,6 @@ cudaError_t dz_launch(int act, dim3 grid, const fe::LinDzParams& p, cudaStream_t
     }
     return launch(fe::linear_dz_kernel<VEC, fe::kActNone>, grid, 256, 0, s, p);
 }
-
-// Backward workspace: dz [M][roundup8(N)] bf16 where it is written, then the column partials behind db.
-int dz_chunks(int64_t M) { return (int)std::max<int64_t>(1, std::min<int64_t>(256, (M + 31) / 32)); }
-size_t dz_bytes(int64_t M, int N, bool written) { return written ? align256(2 * (size_t)M * (((size_t)N + 7) / 8 * 8)) : 0; }
-size_t db_bytes(int64_t M, int N, bool db) { return db ? sizeof(float) * (size_t)dz_chunks(M) * N : 0; }
-// dz is dy itself without an activation, when its rows suit TMA; db alone needs none.
-bool dz_written(int act, bool dy_rows16, bool dx, bool dw) { return (dx || dw) && !(act == FE_ACT_NONE && dy_rows16); }
 
 }  // namespace
 
@@ -834,7 +674,7 @@ fe_status fe_moe_block_norm(const void* r, int r_dtype, const void* y, const voi
 size_t fe_moe_block_norm_workspace(int64_t T, int H)
 {
     if (T < 0 || H < 1 || H > fe::kNormMaxH) return 0;
-    return sizeof(float) * 3 * (size_t)H * (size_t)std::min<int64_t>(kMaxPartials, std::max<int64_t>(T, 1));
+    return norm_workspace(T, H);
 }
 
 fe_status fe_moe_block_norm_backward(const void* dr_out, const void* du, const void* r, int r_dtype, const void* y,
@@ -902,8 +742,8 @@ fe_status fe_moe_block_norm_backward(const void* dr_out, const void* du, const v
 
 size_t fe_moe_balance_workspace(int64_t T, int E)
 {
-    if (T < 0 || E < 1 || E > fe::kBalMaxE || balance_fused(T, E)) return 0;
-    return 8 * (size_t)balance_ctas(T, E) * ((size_t)E + 1);
+    if (T < 0 || E < 1 || E > fe::kBalMaxE) return 0;
+    return balance_workspace(T, E);
 }
 
 fe_status fe_moe_balance_loss(const float* logits, const int32_t* idx, const uint8_t* mask, int64_t T, int E, int top_k,
@@ -956,12 +796,8 @@ fe_status fe_moe_balance_loss(const float* logits, const int32_t* idx, const uin
     p.ipart = reinterpret_cast<int32_t*>(p.part + (size_t)p.G * (E + 1));
     const int sms = sm_count();
     if (sms < 1) return record_cuda(cudaErrorInvalidDevice, "device");
-    const int64_t groups = (T + 32 / balance_lanes(E) - 1) / (32 / balance_lanes(E));
-    const int W = fe::bal_ring_warps(E > 512 ? 32 : 16);
     if (vec) {
-        // enough CTAs for a group of rows per two warps, a CTA an SM at most, and no more than the workspace has
-        // partials for: the second pass has the fewer to join
-        p.G = (int)std::min<int64_t>(std::min(sms, ctas), (2 * groups + W - 1) / W);
+        p.G = balance_ring_ctas(T, E, sms);
         p.ipart = reinterpret_cast<int32_t*>(p.part + (size_t)p.G * (E + 1));
         FE_CUDA_TRY(balance_ring_dispatch(p, s));
     } else {
@@ -1122,8 +958,7 @@ fe_status fe_moe_linear_backward(const void* dy, int64_t lddy, const void* x, in
         p.M = M;
         p.N = N;
         p.cols = cols;
-        const int chunks = dz_chunks(M);
-        p.rows_per_cta = (M + chunks - 1) / chunks;
+        p.rows_per_cta = dz_rows(M);
         const int used = (int)((M + p.rows_per_cta - 1) / p.rows_per_cta);
         const bool vec = cols % 8 == 0 && lddy % 8 == 0 && aligned(dy, 16) && (act == FE_ACT_NONE || aligned(z, 16));
         const int per = 32 * (vec ? 8 : 1);
