@@ -287,7 +287,8 @@ __global__ void __launch_bounds__(1024) block_norm_kernel(NormParams p, int tpr)
 // (block_norm_backward_ring_kernel), so the sums of all of them travel together and a second walk over
 // the stage writes every output.  Where r' is small next to what cancels in it (sum r'^2 below an
 // eighth of its positive parts, or not finite), the group takes the sums of the rounded r' itself,
-// which costs that row two more exchanges.  With an exchange per norm and one for dm, the group's
+// which costs that row two more exchanges; the backward pass also where a product of y before its norm with a
+// gradient leaves fp32 though the norm's own does not.  With an exchange per norm and one for dm, the group's
 // warps spent 10,000 cycles a row in latencies: 44 us for T = 4096, H = 2048 backward, where memory
 // needs 16.  Now it takes 26.5 us there and 85 us at T = 16384 (4.7 TB/s) without the weights' gradients, 6 us
 // more with them (their last partials and the launch that adds them); forward with fp32 rows 21.2 us (4.75
@@ -443,6 +444,9 @@ enum { kByRow = 0, kByColumn = 1, kByElement = 2 };
 
 // Whether the expanded sum of squares lost too much, given its positive parts (also if it is not finite).
 FE_DEV bool sum_cancelled(float sum, float parts) { return !(sum >= 0.125f * parts) || isinf(sum); }
+
+// Whether a sum of products with y before its norm left fp32 (or met a NaN), though the sum it stands for may not.
+FE_DEV bool sum_overflowed(float sum) { return !(fabsf(sum) <= 3.402823466e38f); }
 
 // Copies of a row's operands: lane k of the group's first warp holds operand k.
 struct RowCopies {
@@ -751,7 +755,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_ring_kernel(NormBwdPa
         const float k1 = g1 * rho_y;   // v's factor of q
         const float parts = sum[1] + k1 * k1 * sum[3];
         float ss = parts + 2.0f * k1 * sum[2], sx = sum[4] + k1 * sum[5];
-        const bool direct = sum_cancelled(ss, parts);   // the same for the whole group
+        const bool direct = sum_cancelled(ss, parts) || sum_overflowed(sx);   // the same for the whole group
         if (direct) {
             float d0[2] = {0, 0}, d1s[2] = {0, 0};
 #pragma unroll 1
@@ -785,9 +789,10 @@ __global__ void __launch_bounds__(512) block_norm_backward_ring_kernel(NormBwdPa
         }
         const float rho = rsqrtf(ss * inv_h + p.eps);
         const float rk = sx * inv_h * rho * rho * rho;   // rho mean(x n) rho
-        float sdm = k1 * (sum[6] + rho * sum[5] - rk * (sum[2] + k1 * sum[3]));   // sum dm m; over d1 / g1: dg of a token
-        float sdg = rho_y * (sum[6] + rho * sum[5] - rk * (sum[2] + k1 * sum[3]));
-        if (direct) {
+        const float dq = sum[6] + rho * sum[5] - rk * (sum[2] + k1 * sum[3]);
+        float sdm = k1 * dq;   // sum dm m; over d1 / g1: dg of a token
+        float sdg = rho_y * dq;
+        if (direct || sum_overflowed(dq)) {
             float d0[2] = {0, 0};
 #pragma unroll 1
             for (int c = 0; c < C; ++c) {
@@ -1048,7 +1053,7 @@ __global__ void __launch_bounds__(512, 2) block_norm_backward_any_kernel(NormBwd
         const float k1 = g1 * rho_y;
         const float parts = sum[1] + k1 * k1 * sum[3];
         float ss = parts + 2.0f * k1 * sum[2], sx = sum[4] + k1 * sum[5];
-        const bool direct = sum_cancelled(ss, parts);
+        const bool direct = sum_cancelled(ss, parts) || sum_overflowed(sx);
         if (direct) {
             float two[2] = {0, 0};
 #pragma unroll 1
@@ -1064,8 +1069,9 @@ __global__ void __launch_bounds__(512, 2) block_norm_backward_any_kernel(NormBwd
         }
         const float rho = has_du ? rsqrtf(ss * inv_h + p.eps) : 0.0f;
         const float rk = has_du ? sx * inv_h * rho * rho * rho : 0.0f;
-        float sdg = rho_y * (sum[6] + rho * sum[5] - rk * (sum[2] + k1 * sum[3]));
-        if (direct) {
+        const float dq = sum[6] + rho * sum[5] - rk * (sum[2] + k1 * sum[3]);
+        float sdg = rho_y * dq;
+        if (direct || sum_overflowed(dq)) {
             float one[1] = {0};
 #pragma unroll 1
             for (int e = t; e < H; e += tpr) {

@@ -273,3 +273,63 @@ def test_refuses_other_layouts():
         fe.block_norm(c["r"], c["y"], c["w_post"], c["w_pre"], eps=0.0)
     with pytest.raises(fe.FeMoeError):
         fe.block_norm(c["r"], c["y"], c["w_post"], c["w_pre"], u=c["y"])
+
+
+def extremes(T, H, rt, gate, seed, finite=False):
+    """make() with extreme rows at the start, in the middle and at the end; which rows are not finite."""
+    c = make(T, H, rt, gate, seed=seed)
+    bad = torch.zeros(T, dtype=torch.bool, device="cuda")
+    for at in (0, T // 2, T - 9):
+        c["r"][at] = 0                     # nothing at all: 1 / rms is eps^-1/2
+        c["y"][at] = 0
+        c["y"][at + 1] = 0
+        c["r"][at + 2] *= 1e15
+        c["y"][at + 3] *= 1e-15
+        c["y"][at + 4] *= 1e17             # s a w_post y squared is beyond fp32, the norm of y and r' are not
+        c["dr_out"][at + 5] *= 1e12        # a large gradient
+        c["du"][at + 5] *= 1e12
+        c["y"][at + 6] *= 1e15             # the same where dr' y and du y are beyond fp32 too, but no square
+        c["dr_out"][at + 6] *= 1e22
+        c["du"][at + 6] *= 1e22
+        if not finite:
+            c["y"][at + 7, H // 3] = float("nan")
+            c["r"][at + 8, 1] = float("inf")
+            bad[at + 7:at + 9] = True
+    return c, bad
+
+
+EXTREME = [(36, 256, torch.float32), (15001, 64, torch.float32), (4000, 1024, torch.bfloat16), (37, 255, torch.float32),
+           (3001, 255, torch.bfloat16), (700, 2048, torch.float32), (1501, 4096, torch.bfloat16)]
+
+
+@pytest.mark.parametrize("gate", ["none", "token", "channel", "full"])
+@pytest.mark.parametrize("T, H, rt", EXTREME)
+def test_extreme_rows_of_every_kernel(T, H, rt, gate):
+    """Zero, huge, tiny, NaN and infinite rows stay in their rows forward and backward, whichever rows share a
+    ring, a reduction or a block with them, and the finite ones keep the bounds of the others.  s = 512: products of
+    y without its norm reach beyond fp32 where the outputs do not."""
+    import fp4_expert_gemv_b200 as fe
+    s = 512.0
+    c, bad = extremes(T, H, rt, gate, seed=T)
+    ok = ~bad
+    kw = dict(gate=c["g"], gate_kind=kind_of(fe, gate, False), scale=s, eps=EPS)
+    r2, u = fe.block_norm(c["r"], c["y"], c["w_post"], c["w_pre"], **kw)
+    want = ref.norm_forward(c["r"], c["y"], c["w_post"], c["w_pre"], c["g"], gate, False, s, EPS)
+    ref.close(r2[ok], want["r_out"][0][ok], ref.FWD * want["r_out"][1][ok], "r_out")
+    ref.close(u[ok], want["u"][0][ok], ref.FWD * want["u"][1][ok], "u")
+    nan, inf = bad.nonzero()[::2, 0], bad.nonzero()[1::2, 0]
+    assert torch.isnan(u[nan]).all() and torch.isnan(r2[nan]).all()
+    assert torch.isnan(u[inf, 1]).all() and (u[inf, 2:] == 0).all()   # 1 / rms is 0
+    got = fe.block_norm_backward(c["dr_out"], c["du"], c["r"], c["y"], c["w_post"], c["w_pre"], weight_grads=False, **kw)
+    want = ref.norm_backward(c["dr_out"], c["du"], c["r"], c["y"], c["w_post"], c["w_pre"], c["g"], gate, False, s, EPS)
+    for name, t in zip(("dr", "dy", "dgate"), got):
+        if t is not None:
+            ref.close(t[ok], want[name][0][ok], ref.BWD * want[name][1][ok], name)
+    assert fe.op_status() == (fe.FE_OK, 0)
+
+
+@pytest.mark.parametrize("T, H, rt", EXTREME)
+def test_sums_over_extreme_rows(T, H, rt):
+    import fp4_expert_gemv_b200 as fe
+    c, _ = extremes(T, H, rt, "channel", seed=T + 1, finite=True)
+    check_backward(fe, c, "channel", False, s=512.0)
