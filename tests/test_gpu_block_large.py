@@ -74,3 +74,54 @@ def test_linear(M, N, K):
         same_ends(dx)
         assert torch.isfinite(db).all()
     assert fe.op_status() == (fe.FE_OK, 0)
+
+
+def near(got, want, err):
+    """Within half a step of bf16 and err, element by element, and not all zero."""
+    want = want.double()
+    assert ((got.double() - want).abs() <= 2.0 ** -8 * want.abs() + err).all() and (want != 0).any()
+
+
+def test_the_last_rows_gradients():
+    """The last period's gradients against the 64-bit definition (the other tests compare it with the first)."""
+    import block_ref as ref
+    import fp4_expert_gemv_b200 as fe
+    T, H = 1_100_000, 2048
+    (r, big_r), (y, big_y) = rows(T, H, bf, 1), rows(T, H, bf, 2)
+    (dr, big_dr), (du, big_du) = rows(T, H, bf, 3), rows(T, H, bf, 4)
+    w = torch.linspace(0.5, 1.5, H, device="cuda").to(bf)
+    got = fe.block_norm_backward(big_dr, big_du, big_r, big_y, w, w, weight_grads=False)
+    want = ref.norm_backward(dr, du, r, y, w, w, None, "none", False, 1.0, 1e-6)
+    for name, t in zip(("dr", "dy"), got):
+        for part in (t[:PERIOD], t[-PERIOD:]):
+            near(part, want[name][0], ref.BWD * want[name][1])
+    del got, big_r, big_y, big_dr, big_du
+    M, N, K = 2_200_000, 1024, 64
+    (x, big_x), (dy, big_dy) = rows(M, K, bf, 4), rows(M, N, bf, 5)
+    w = (torch.randn(N, K, generator=torch.Generator(device="cuda").manual_seed(6), device="cuda") * K ** -0.5).to(bf)
+    z = torch.empty(M, N, dtype=bf, device="cuda")
+    fe.linear(big_x, w, act=fe.ACT_SILU, z=z)
+    dx, _, _ = fe.linear_backward(big_dy, big_x, w, z=z, act=fe.ACT_SILU, need_dw=False)
+    dz, mag = ref.linear_dz(dy, z[-PERIOD:], "silu")
+    edz = 2.0 ** -8 * dz.abs() + ref.FWD * mag
+    W = w.double()
+    err = edz @ W.abs() + (N / 16 + 4) * 2.0 ** -22 * ((dz.abs() + edz) @ W.abs())
+    near(dx[-PERIOD:], dz @ W, err)
+    assert fe.op_status() == (fe.FE_OK, 0)
+
+
+@pytest.mark.parametrize("M, N, K", [(2_200_000, 64, 1024), (2_200_000, 1024, 64)])
+def test_the_weights_gradient_over_more_rows(M, N, K):
+    """Values in {-1, 0, 1}: every sum is a whole number below 2^24 and exact in fp32 whatever the order, so dw and dx are the
+    exact sums rounded once, and db is exact."""
+    import fp4_expert_gemv_b200 as fe
+    g = torch.Generator(device="cuda").manual_seed(8)
+    tri = lambda *s: (torch.randint(-1, 2, s, generator=g, device="cuda")).to(bf)
+    x, dy, w = tri(PERIOD, K), tri(PERIOD, N), tri(N, K)
+    dx, dw, db = fe.linear_backward(dy.repeat(M // PERIOD, 1), x.repeat(M // PERIOD, 1), w)
+    n = M // PERIOD
+    assert torch.equal(dw, (n * (dy.double().t() @ x.double())).to(bf))
+    assert torch.equal(db.double(), n * dy.double().sum(0))
+    want = (dy.double() @ w.double()).to(bf)
+    assert torch.equal(dx[:PERIOD], want) and torch.equal(dx[-PERIOD:], want) and (want != 0).any()
+    assert fe.op_status() == (fe.FE_OK, 0)
