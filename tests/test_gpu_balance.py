@@ -231,3 +231,26 @@ def test_refusals():
         fe.balance_loss(l[:, ::2], idx)
     with pytest.raises(fe.FeMoeError):
         fe.balance_loss(torch.zeros(2, 1025, device="cuda"), idx[:2].contiguous())
+
+
+@pytest.mark.parametrize("T, E, k", [(50, 64, 4), (700, 128, 8), (3000, 128, 8), (9000, 512, 10), (33, 250, 6), (5000, 1024, 8)])
+def test_logits_spread_to_underflow(T, E, k):
+    """Every p from 1 down to below the smallest normal number: the exponential's argument d log2 e is rounded three times
+    (the difference, the constant and the product), 2^-24 of itself each, so p is off by 3 |d| 2^-24 of
+    itself besides what the other tests allow; below 2^-126 it is 0."""
+    import fp4_expert_gemv_b200 as fe
+    l, idx, mask = make(T, E, k, True, seed=E)
+    l = l * 0.1 - torch.rand(T, E, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda") * 100
+    a, b = 1.0, 0.1
+    loss, counts, n = fe.balance_loss(l, idx, mask=mask, balance_coef=a, z_coef=b)
+    dl = fe.balance_loss_backward(l, counts, n, k, mask=mask, balance_coef=a, z_coef=b)
+    wl, wc, wn, wd, ml, md = ref.balance(l, idx, mask, a, b)
+    assert torch.equal(counts.long(), wc) and int(n) == wn
+    depth = T / 4096 + 64
+    # the loss holds sums of p: a small p's own error is small beside them
+    ref.close(loss, wl, (ref.FWD + depth * 2.0 ** -24) * ml, "loss")
+    d = (l.double().max(1, keepdim=True).values - l.double()).clamp(max=100)
+    lse = torch.logsumexp(l.double(), 1).abs()[:, None]
+    flushed = 2.0 ** -126 * (a * E * 2 + 2 * b * (lse + 1)) / max(wn, 1)
+    ref.close(dl, wd, (ref.FWD + 3 * d * 2.0 ** -24) * md + flushed, "dlogits")
+    assert (wd.abs() > 0).float().mean() > 0.3

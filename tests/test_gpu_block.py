@@ -209,3 +209,63 @@ def test_training_the_router_on_the_balance_loss():
     ref.close(dr, want["dr"][0], ref.BWD * want["dr"][1], "dr")
     ref.close(dw_pre, want["dw_pre"][0], ref.BWD * want["dw_pre"][1], "dw_pre")
     gl.layer.close()
+
+
+# from 200 to 9100 rows: through the layer's streaming and its tensor-core path (4096 pairs and more), the products by
+# split tiles of several row tiles and by CTA pairs, the norms row by row and streamed
+@pytest.mark.parametrize("T, H, I, Is, k, rt", [(200, 2048, 256, 768, 2, bf), (600, 1024, 128, 1000, 4, torch.float32),
+                                                (2100, 2048, 256, 768, 2, bf), (5000, 512, 128, 264, 3, bf),
+                                                (9100, 1024, 128, 512, 2, torch.float32)])
+def test_block_of_a_prefill(T, H, I, Is, k, rt):
+    """The composed call is its parts bit by bit at prefill sizes, repeats, and is close to the definition at rows from
+    the start, the middle and the end (the bounds of the test of small blocks)."""
+    import fp4_expert_gemv_b200 as fe
+    E, seed = 8, 3
+    gl = harness.GpuLayer(E, H, I, seed, max_T=T, max_k=4)
+    p = params(H, Is, E, T)
+    r = (torch.randn(T, H, generator=torch.Generator(device="cuda").manual_seed(T), device="cuda") * 2).to(rt)
+    kind = fe.GATE_CHANNEL | fe.GATE_SIGMOID
+    kw = dict(shared=p["shared"], w_post=p["w_post"], gate=p["gate"], gate_kind=kind, scale=0.5, w_next_pre=p["w_next_pre"])
+    r2, u2, logits = gl.layer.forward_block(r, k, p["w_router"], w_pre=p["w_pre"], **kw)
+    h2, hu2, hl, u = by_hand(fe, gl.layer, r, p, k, kind, 0.5)
+    assert torch.equal(r2, h2) and torch.equal(u2, hu2) and torch.equal(logits, hl)
+    again = gl.layer.forward_block(r, k, p["w_router"], u_in=u, **kw)
+    assert torch.equal(again[0], r2) and torch.equal(again[1], u2) and torch.equal(again[2], logits)
+    assert gl.layer.status() == (fe.FE_OK, 0) and fe.op_status() == (fe.FE_OK, 0)
+    at = torch.tensor([0, 1, 2, 127, 128, 129, T // 2, T // 2 + 1, T - 3, T - 2, T - 1], device="cuda")
+    side = harness.OracleSide(E, H, I, seed)
+    y64, _ = side.forward(u[at].contiguous().view(torch.int16).cpu().numpy().view(np.uint16), logits[at].cpu().numpy(), k)
+    a = ref.linear(u[at], p["shared"][0], None, "swiglu", None)[0]
+    y64 = torch.from_numpy(y64).cuda() + a @ p["shared"][1].double().t()
+    want = ref.norm_forward(r[at], y64, p["w_post"], p["w_next_pre"], p["gate"], "channel", True, 0.5, 1e-6)
+    add = want["r_out"][0] - r[at].double()
+    tol = (harness.MAX_REL_TOL + 3 * 2.0 ** -8) * float(add.abs().max())
+    ref.close(r2[at], want["r_out"][0], torch.full_like(add, tol), "r_out")
+    rho = float((want["r_out"][0] ** 2).mean(1).min() ** -0.5)
+    ref.close(u2[at], want["u"][0], torch.full_like(add, 2 * tol * rho * float(p["w_next_pre"].abs().max())), "u_out")
+    gl.layer.close()
+
+
+def test_blocks_of_a_prefill_in_a_graph_and_on_a_stream():
+    import fp4_expert_gemv_b200 as fe
+    E, H, T, k = 8, 1024, 2100, 2
+    gl = harness.GpuLayer(E, H, 128, 1, max_T=T, max_k=2)
+    p = params(H, 512, E, 2)
+    r = torch.randn(T, H, device="cuda", generator=torch.Generator(device="cuda").manual_seed(6)).to(bf)
+    call = lambda **kw: gl.layer.forward_block(r, k, p["w_router"], w_pre=p["w_pre"], shared=p["shared"], w_post=p["w_post"],
+                                               w_next_pre=p["w_next_pre"], **kw)
+    want = call()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = call(stream=side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = call()
+    r.mul_(-0.75)
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(out, call())) and not torch.equal(out[0], want[0])
+    assert gl.layer.status() == (fe.FE_OK, 0) and fe.op_status() == (fe.FE_OK, 0)
+    gl.layer.close()
