@@ -153,6 +153,8 @@ class MoELayer:
         h = _P()
         check(fe_moe_create(E, H, I, group, ctypes.byref(h)), "fe_moe_create")
         self.h = h
+        import torch
+        self.device = torch.cuda.current_device()   # the one it was made on
         self.E, self.H, self.I = E, H, I
         self.max_T, self.max_top_k = max_T, max_top_k
         try:
@@ -257,6 +259,8 @@ class MoELayer:
         bf, dev = torch.bfloat16, r.device
         T, H = r.shape
         dt = _dtype_of(r, "r")
+        if dev.type == "cuda" and dev.index != self.device:
+            raise ValueError(f"the tensors are on {dev}, the layer on cuda:{self.device}")
         _arg(r, "r", r.dtype, (T, self.H), dev)
         _arg(w_router, "w_router", bf, (self.E, H), dev)
         for name, t in (("w_pre", w_pre), ("w_post", w_post), ("w_next_pre", w_next_pre)):

@@ -269,3 +269,16 @@ def test_blocks_of_a_prefill_in_a_graph_and_on_a_stream():
     assert all(torch.equal(a, b) for a, b in zip(out, call())) and not torch.equal(out[0], want[0])
     assert gl.layer.status() == (fe.FE_OK, 0) and fe.op_status() == (fe.FE_OK, 0)
     gl.layer.close()
+
+
+def test_tensors_of_another_device_are_refused():
+    """The layer runs on the device that it was made on; its kernels must not be given another one's memory (here the
+    layer is made to believe that it lies elsewhere: nothing is launched)."""
+    gl = harness.GpuLayer(8, 256, 128, 0, max_T=4, max_k=2)
+    p = params(256, 64, 8, 1)
+    r = torch.zeros(4, 256, device="cuda")
+    gl.layer.forward_block(r, 2, p["w_router"], w_pre=p["w_pre"])
+    gl.layer.device += 1
+    with pytest.raises(ValueError, match="layer on cuda"):
+        gl.layer.forward_block(r, 2, p["w_router"], w_pre=p["w_pre"])
+    gl.layer.close()
