@@ -287,8 +287,9 @@ __global__ void __launch_bounds__(32 * bal_ring_warps(N)) balance_ring_kernel(Ba
     griddep_wait();
     griddep_launch();
     const int64_t step = (int64_t)gridDim.x * W * R;
+    bool dead = false;   // a wait ran out: no more copies
     auto fill = [&](int64_t t0, int s) {
-        if (lane != 0 || t0 >= p.T) return;
+        if (lane != 0 || t0 >= p.T || dead) return;
         const uint32_t bytes = 4u * p.E * (uint32_t)min((int64_t)R, p.T - t0);
         mbar_expect_tx(bar + 8 * s, bytes);
         bulk_g2s(ring + s * stage, p.logits + (size_t)t0 * p.E, bytes, bar + 8 * s);
@@ -301,7 +302,6 @@ __global__ void __launch_bounds__(32 * bal_ring_warps(N)) balance_ring_kernel(Ba
     float z = 0.0f;
     int n = 0, s = 0;
     uint32_t parity = 0;
-    bool dead = false;
     // the next group's mask byte and chosen id are fetched a group ahead
     uint32_t keep_next = 0;
     int id_next = -1;
@@ -319,7 +319,10 @@ __global__ void __launch_bounds__(32 * bal_ring_warps(N)) balance_ring_kernel(Ba
         const bool on = keep_next != 0;
         const int id = on ? id_next : -1;
         ahead(t + step);
-        if (!dead && !mbar_wait(bar + 8 * s, parity, kNormTimeoutNs)) dead = true;
+        if (!dead && !mbar_wait(bar + 8 * s, parity, kNormTimeoutNs)) {
+            dead = true;
+            if (lane == 0) ring_drain(bar, s, parity, stages, (p.T - t0 + step - 1) / step);
+        }
         float l[N], inv, lse;
         const uint32_t row = ring + s * stage + 4u * sub * p.E;
 #pragma unroll

@@ -633,7 +633,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                         }
                         if (has_res) {
                             const uint32_t turn = nres - 1;   // this block's fetch
-                            if (tma_res && !lin_wait_warp(resfull(ew, turn & 1), (turn >> 1) & 1)) *abort = 1;
+                            if (tma_res && !lin_wait_warp(resfull(ew, turn & 1), (turn >> 1) & 1)) {
+                                *abort = 1;
+                                lin_wait_warp(resfull(ew, turn & 1), (turn >> 1) & 1);   // it must not outlive the slot
+                            }
                             st.add(slot, lane, v);
                             // the next block's residual goes to the other slot, whose store has been read by then
                             if (c + 2 < chunks) {

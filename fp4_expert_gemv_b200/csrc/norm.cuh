@@ -439,6 +439,19 @@ FE_DEV void vdot(float (&s)[2], const float (&a)[8], const float (&b)[8])
     }
 }
 
+// After a wait that ran out: the copies under way, of up to n rows from stage s on, get the same time again, each, so
+// that none outlives the CTA's shared memory.
+FE_DEV void ring_drain(uint32_t bar, int s, uint32_t parity, int stages, int64_t n)
+{
+    for (int j = 0; j < stages && j < n; ++j) {
+        mbar_wait(bar + 8 * s, parity, kNormTimeoutNs);
+        if (++s == stages) {
+            s = 0;
+            parity ^= 1;
+        }
+    }
+}
+
 // How the gate enters a row: one factor, a factor per column, or one per element.
 enum { kByRow = 0, kByColumn = 1, kByElement = 2 };
 
@@ -464,10 +477,10 @@ struct RowCopies {
         }
         ++n;
     }
-    // Row `row` into the stage at dst; by the group's first warp, converged.
-    FE_DEV void fill(int t, int64_t row, int64_t rows, uint32_t dst, uint32_t stage, uint32_t bar) const
+    // Row `row` into the stage at dst; by the group's first warp, converged.  Nothing more once a wait of its has run out.
+    FE_DEV void fill(int t, int64_t row, int64_t rows, uint32_t dst, uint32_t stage, uint32_t bar, bool dead = false) const
     {
-        if (t >= 32 || row >= rows) return;
+        if (t >= 32 || row >= rows || __any_sync(0xffffffffu, dead)) return;
         if (t == 0) mbar_expect_tx(bar, stage);
         __syncwarp();
         if (t < n) bulk_g2s(dst + off, src + (size_t)row * bytes, bytes, bar);
@@ -526,7 +539,10 @@ __global__ void __launch_bounds__(512) block_norm_ring_kernel(NormParams p, int 
     uint16_t graw = token && first < p.T ? p.gate[first] : 0;   // the coming row's gate
     const float inv_h = 1.0f / (float)H;
     for (int64_t row = first; row < p.T; row += step) {
-        if (!dead && !mbar_wait(bar + 8 * s, parity, kNormTimeoutNs)) dead = true;
+        if (!dead && !mbar_wait(bar + 8 * s, parity, kNormTimeoutNs)) {
+            dead = true;
+            if (t < 32) ring_drain(bar, s, parity, stages, (p.T - row + step - 1) / step);
+        }
         const uint32_t src = base_a + s * stage;
         float k = 1.0f;
         if (token) {
@@ -568,7 +584,7 @@ __global__ void __launch_bounds__(512) block_norm_ring_kernel(NormParams p, int 
             if (p.w_post) k *= rsqrtf(sum[1] * inv_h + p.eps);
             const float parts = sum[0] + k * k * sum[3];
             ss = parts + 2.0f * k * sum[2];
-            rc.fill(t, row + stages * step, p.T, src, stage, bar + 8 * s);
+            rc.fill(t, row + stages * step, p.T, src, stage, bar + 8 * s, dead);
             if (has_u && sum_cancelled(ss, parts)) {   // the same for the whole group
                 float d[2] = {0, 0}, v[8];
 #pragma unroll
@@ -586,7 +602,7 @@ __global__ void __launch_bounds__(512) block_norm_ring_kernel(NormParams p, int 
             float one[1] = {srr[0] + srr[1]};
             ring_sum<1>(one, group, tpr, red + half * norm_red_floats(tpr));
             half ^= 1;
-            rc.fill(t, row + stages * step, p.T, src, stage, bar + 8 * s);
+            rc.fill(t, row + stages * step, p.T, src, stage, bar + 8 * s, dead);
             ss = one[0];
         }
         const float rho = has_u ? rsqrtf(ss * inv_h + p.eps) : 0.0f;
@@ -689,7 +705,11 @@ __global__ void __launch_bounds__(512) block_norm_backward_ring_kernel(NormBwdPa
     uint16_t graw = token && first < p.T ? p.gate[first] : 0;   // the coming row's gate
     const float inv_h = 1.0f / (float)H;
     for (int64_t row = first; row < p.T; row += step) {
-        if (!dead && !mbar_wait(bar + 8 * s, parity, kNormTimeoutNs)) dead = true;
+        if (!dead && !mbar_wait(bar + 8 * s, parity, kNormTimeoutNs)) {
+            dead = true;
+            // the row before has not been replaced yet
+            if (t < 32) ring_drain(bar, s, parity, stages, min((p.T - row + step - 1) / step, (int64_t)stages - (row != first)));
+        }
         const uint32_t src = base_a + s * stage;
         const size_t at = (size_t)row * H;
         // chunk c of an operand of the row, for chunks inside it
@@ -749,7 +769,7 @@ __global__ void __launch_bounds__(512) block_norm_backward_ring_kernel(NormBwdPa
         // everyone is past the row before: its stage takes the row that follows the ones under way
         if (row != first) {
             const int sp = s == 0 ? stages - 1 : s - 1;
-            rc.fill(t, row + (stages - 1) * step, p.T, base_a + sp * stage, stage, bar + 8 * sp);
+            rc.fill(t, row + (stages - 1) * step, p.T, base_a + sp * stage, stage, bar + 8 * sp, dead);
         }
         const float rho_y = w_post ? rsqrtf(sum[0] * inv_h + p.eps) : 1.0f;
         const float k1 = g1 * rho_y;   // v's factor of q
