@@ -373,8 +373,9 @@ struct LinStage {
         return reinterpret_cast<uint16_t*>(base + slot * kLinSlotBytes + lin_slot_chunk(r, col >> 3)) + (col & 7);
     }
 
-    // Block (row0, col0) of a matrix with row stride ld from a slot; columns from `limit` on are not the
-    // block's (the matrix ends there, where TMA stops by itself, or a swiglu z's other half begins).
+    // Block (row0, col0) of a matrix with row stride ld from a slot; columns from `limit` on are not the block's: a
+    // swiglu z's other half begins there, or the matrix ends (`ends`: after whole 16-byte pieces, where TMA
+    // stops by itself; within a piece it would write the rest of the piece too).
     FE_DEV void flush(int slot, int lane, const CUtensorMap* map, bool vec, bool ends, uint16_t* m, int64_t ld, int row0,
                       int rows, int col0, int limit) const
     {
@@ -387,6 +388,8 @@ struct LinStage {
             if (col0 + lane < limit)
                 for (int r = 0; r < 32 && row0 + r < rows; ++r) m[(size_t)(row0 + r) * ld + col0 + lane] = *at(slot, r, lane);
             __syncwarp();
+            // a group for this block as well: settle() counts blocks
+            if (vec && lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
         }
     }
 
@@ -561,7 +564,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
             uint16_t *out = p.out, *zo = p.z;
             const int64_t ldr = p.ldr, ldo = p.ldo;
             const CUtensorMap *to = &p.to, *tr = &p.tr, *tz = &p.tz;
-            const bool glu = !PLAIN && act == kActSwiglu;
+            const bool glu = !PLAIN && act == kActSwiglu, ends = cols % 8 == 0;
             const int tile_cols = glu ? BN / 2 : BN;
             st.settle<0>();   // the problem before may have used the slots another way
             for (LinRange g(P, i, pair, pairs); g.t < g.end; g.t += g.step, ++done) {
@@ -643,7 +646,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                                 const int ahead = fetch(c + 2);
                                 if (live && !stop) {
                                     st.put(slot, lane, v);
-                                    st.flush(slot, lane, to, vec_out, true, out, ldo, row0, M, c0, cols);
+                                    st.flush(slot, lane, to, vec_out, ends, out, ldo, row0, M, c0, cols);
                                 }
                                 slot = ahead;
                                 continue;
@@ -662,7 +665,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                             }
                         }
                         st.put(slot, lane, v);
-                        st.flush(slot, lane, to, vec_out, true, out, ldo, row0, M, c0, cols);
+                        st.flush(slot, lane, to, vec_out, ends, out, ldo, row0, M, c0, cols);
                     }
                 }
                 // the accumulator is read: the products after the next may begin

@@ -398,3 +398,30 @@ def test_backward_of_many_tiles(act):
     z = torch.empty(M, N, dtype=bf, device="cuda")
     fe.linear(x, w, bias=bias, act=act_id(fe, act), z=z)
     check_backward(fe, dy, x, w, z, act)
+
+
+@pytest.mark.parametrize("act", ["none", "gelu", "swiglu"])
+@pytest.mark.parametrize("cols", [33, 34, 36, 39, 250, 1537])
+@pytest.mark.parametrize("M", [5, 70, 300, 20011])
+def test_nothing_is_written_behind_a_row(M, cols, act):
+    """Rows of whole 16-byte pieces apart whose last piece is not all theirs, in a buffer that ends with the last row's last
+    column: what lies between the rows and behind them stays."""
+    import fp4_expert_gemv_b200 as fe
+    N = 2 * cols if act == "swiglu" else cols
+    x, w, bias, res, _ = make(M, N, 72, act, seed=cols)
+    want = fe.linear(x, w, bias=bias, act=act_id(fe, act), residual=res)
+    plain = fe.linear(x, w, act=act_id(fe, act))
+    ld = (cols + 7) // 8 * 8 + 8
+    n = (M - 1) * ld + cols
+    buf = torch.empty(n + 64, dtype=bf, device="cuda")
+    y = buf[:n].as_strided((M, cols), (ld, 1))
+    for kw, ref_y in ((dict(bias=bias, residual=res), want), (dict(), plain), (dict(bias=bias, residual=y), want),
+                      (dict(bias=bias, residual=res, z=torch.empty(M, N, dtype=bf, device="cuda")), want)):
+        buf.fill_(7.0)
+        if kw.get("residual") is y:
+            y.copy_(res)
+        fe.linear(x, w, act=act_id(fe, act), y=y, **kw)
+        assert torch.equal(y, ref_y)
+        y.fill_(7.0)
+        assert (buf == 7).all()
+    assert fe.op_status() == (fe.FE_OK, 0)
