@@ -33,6 +33,7 @@ namespace {
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 using fe_host::overlap;
+using fe_host::overlap_rows;
 
 // SMs of the current device (looked up once per device).
 int sm_count()
@@ -630,11 +631,13 @@ fe_status check_linear(const void* x, int64_t ldx, const void* w, const void* bi
         return FE_ERR_INVALID_ARG;
     const size_t ny = span(M, ldy, cols), nz = 2 * (size_t)M * N, nx = span(M, ldx, K), nw = 2 * (size_t)N * K;
     const size_t nres = span(M, ldr, cols), nbias = 2 * (size_t)N;
-    if (overlap(y, ny, x, nx) || overlap(y, ny, w, nw) || overlap(y, ny, bias, nbias) || overlap(y, ny, z, nz) ||
+    if (overlap_rows(y, ny, 2 * (size_t)ldy, 2 * (size_t)cols, x, nx, 2 * (size_t)ldx, 2 * (size_t)K) || overlap(y, ny, w, nw) || overlap(y, ny, bias, nbias) || overlap(y, ny, z, nz) ||
         overlap(z, nz, x, nx) || overlap(z, nz, w, nw) || overlap(z, nz, bias, nbias) || overlap(z, nz, residual, nres))
         return FE_ERR_INVALID_ARG;
-    // y may be the residual itself (the sum in place), not a shifted view of it
-    if (overlap(y, ny, residual, nres) && (y != residual || ldy != ldr)) return FE_ERR_INVALID_ARG;
+    // y may be the residual itself (the sum in place) or lie beside it, not be a shifted view of it
+    if (overlap_rows(y, ny, 2 * (size_t)ldy, 2 * (size_t)cols, residual, nres, 2 * (size_t)ldr, 2 * (size_t)cols) &&
+        (y != residual || ldy != ldr))
+        return FE_ERR_INVALID_ARG;
     return FE_OK;
 }
 
@@ -929,9 +932,12 @@ fe_status fe_moe_linear_backward(const void* dy, int64_t lddy, const void* x, in
     const size_t in_n[4] = {ndy, nx, nw, nz};
     const void* outs[4] = {dx, dw, db, need > 0 ? workspace : nullptr};
     const size_t out_n[4] = {ndx, nw, 4 * (size_t)N, need};
+    const size_t ld[2] = {2 * (size_t)lddy, 2 * (size_t)ldx}, width[2] = {2 * (size_t)cols, 2 * (size_t)K};
     for (int i = 0; i < 4; ++i) {
-        for (int j = 0; j < 4; ++j)
-            if (overlap(outs[i], out_n[i], ins[j], in_n[j])) return FE_ERR_INVALID_ARG;
+        for (int j = 0; j < 4; ++j)   // dx may lie beside dy or x
+            if (i == 0 && j < 2 ? overlap_rows(dx, ndx, 2 * (size_t)lddx, 2 * (size_t)K, ins[j], in_n[j], ld[j], width[j])
+                                : overlap(outs[i], out_n[i], ins[j], in_n[j]))
+                return FE_ERR_INVALID_ARG;
         for (int j = 0; j < i; ++j)
             if (overlap(outs[i], out_n[i], outs[j], out_n[j])) return FE_ERR_INVALID_ARG;
     }

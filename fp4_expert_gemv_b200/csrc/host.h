@@ -18,6 +18,17 @@ inline bool overlap(const void* a, size_t na, const void* b, size_t nb)
     return x < y + nb && y < x + na;
 }
 
+// The same for the first ca (cb) of every la (lb) bytes over ranges of na and nb bytes: rows of the same stride lie
+// beside each other where their columns do.
+inline bool overlap_rows(const void* a, size_t na, size_t la, size_t ca, const void* b, size_t nb, size_t lb, size_t cb)
+{
+    if (!overlap(a, na, b, nb)) return false;
+    if (la != lb || ca > la || cb > lb || la == 0) return true;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    const size_t d = y >= x ? (y - x) % la : (la - (x - y) % la) % la;   // from a row's start to the other's next one
+    return d < ca || d + cb > la;
+}
+
 // Keeps the text of a CUDA failure for fe_moe_last_error and maps it to a status.
 fe_status record_cuda(cudaError_t e, const char* where);
 

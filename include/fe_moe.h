@@ -438,7 +438,8 @@ void fe_moe_stack_destroy(fe_moe_stack_t s);
  * (capturable).  Arrays are dense and row-major unless a row stride (ld, in
  * elements) is given; addresses need their type's alignment, 16-byte aligned rows
  * are faster.  Outputs must not overlap operands, workspace or each other except
- * where said (FE_ERR_INVALID_ARG).  Sums, statistics and epilogues are fp32, each
+ * where said (FE_ERR_INVALID_ARG); columns beside each other in the rows of one buffer
+ * (the same stride) do not.  Sums, statistics and epilogues are fp32, each
  * output is rounded once, and every result is the same from run to run.  */
 #define FE_DTYPE_BF16 0
 #define FE_DTYPE_F32 1

@@ -206,3 +206,15 @@ def test_the_norms_workspace_is_what_the_partials_take():
     """Three sums of H floats from each of up to two CTAs on 148 SMs, a row each at least."""
     for T, H in ((1, 8), (100, 2048), (296, 64), (4096, 2048), (1 << 30, 16384)):
         assert fe.fe_moe_block_norm_workspace(T, H) == 12 * H * min(T, 2 * 148)
+
+
+def test_rows_beside_each_other_do_not_overlap():
+    """Columns of one buffer serve as operand and output where they are apart; a column in common is refused.  (What is
+    not refused here is refused afterwards for z, so that nothing is enqueued.)"""
+    # x in columns 0..63, y in 64..95, the residual in 96..127 of rows of 128, z over the weights
+    ok = dict(x=A, ldx=128, y=A + 128, ldy=128, res=A + 192, ldr=128, w=B, z=B)
+    assert linear(**ok) == INV                                      # z alone
+    assert linear(**{**ok, "z": None, "y": A + 126}) == INV         # y over x's last column
+    assert linear(**{**ok, "z": None, "y": A + 130}) == INV         # y over the residual's first
+    assert linear(**{**ok, "z": None, "y": A + 2 * 100, "res": None}) == INV   # y runs into the next row's x
+    assert linear(**{**ok, "z": None, "ldy": 130}) == INV           # strides that drift apart

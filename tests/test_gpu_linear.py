@@ -425,3 +425,32 @@ def test_nothing_is_written_behind_a_row(M, cols, act):
         y.fill_(7.0)
         assert (buf == 7).all()
     assert fe.op_status() == (fe.FE_OK, 0)
+
+
+@pytest.mark.parametrize("M", [2, 12, 200, 3000])
+def test_columns_of_one_buffer_as_operand_and_output(M):
+    """x, the residual and y (dy, x and dx) side by side in the rows of one buffer."""
+    import fp4_expert_gemv_b200 as fe
+    N, K = 96, 128
+    x, w, bias, res, dy = make(M, N, K, "gelu", seed=M)
+    want = fe.linear(x, w, bias=bias, act=fe.ACT_GELU, residual=res)
+    buf = torch.full((M, K + 2 * N + 8), 7.0, dtype=bf, device="cuda")
+    bx, by, br = buf[:, :K], buf[:, K:K + N], buf[:, K + N:K + 2 * N]
+    for order in ((bx, by, br), (bx, br, by)):
+        bx.copy_(x), order[2].copy_(res)
+        fe.linear(bx, w, bias=bias, act=fe.ACT_GELU, residual=order[2], y=order[1])
+        assert torch.equal(order[1], want) and torch.equal(bx, x) and torch.equal(order[2], res) and (buf[:, K + 2 * N:] == 7).all()
+    z = torch.empty(M, N, dtype=bf, device="cuda")
+    fe.linear(x, w, act=fe.ACT_GELU, z=z)
+    dx, dw, db = fe.linear_backward(dy, x, w, z=z, act=fe.ACT_GELU)
+    wide = torch.full((M, 2 * K + N), 7.0, dtype=bf, device="cuda")
+    vdy, vx, vdx = wide[:, K:K + N], wide[:, K + N:], wide[:, :K]
+    vdy.copy_(dy), vx.copy_(x)
+    dw2 = torch.empty_like(w)
+    nb = fe.fe_moe_linear_workspace(M, N, K, fe.ACT_GELU)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    st = fe.fe_moe_linear_backward(vdy.data_ptr(), wide.stride(0), vx.data_ptr(), wide.stride(0), w.data_ptr(), z.data_ptr(), M, N, K,
+                                   fe.ACT_GELU, vdx.data_ptr(), wide.stride(0), dw2.data_ptr(), None, ws.data_ptr(), nb,
+                                   torch.cuda.current_stream().cuda_stream)
+    assert st == fe.FE_OK
+    assert torch.equal(vdx, dx) and torch.equal(dw2, dw) and torch.equal(vdy, dy) and torch.equal(vx, x)
