@@ -75,7 +75,8 @@ FE_DEV float bal_row_sum(float v)
 }
 
 // l -> softmax numerators exp(l - max), returns 1 / sum and the logsumexp; 0 and 0 for a row of
-// -inf.  NaN or +inf anywhere makes both NaN, as the formula does.
+// -inf.  NaN or +inf anywhere makes both NaN, as the formula does.  A numerator far below the largest is off by up
+// to |l - max| 2^-22 of itself (ex2_ftz's argument is rounded), one below 2^-126 is 0.
 template <int L, int N>
 FE_DEV void bal_softmax(float (&l)[N], float& inv, float& lse)
 {

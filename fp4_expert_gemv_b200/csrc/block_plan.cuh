@@ -205,8 +205,8 @@ constexpr int kSplSmem = 227 * 1024;   // all that a CTA can have
 // CTAs that share a tile's contraction (a power of two, to 8) and the tile's columns: of those whose
 // clusters all run at once (room[lg]: clusters of 2^lg), with two k steps or more a CTA, the least that an SM has
 // to take in, which is what bounds these products: its k steps' operands at 72 bytes a clock (measured), and its
-// share of the other CTAs' partial sums, which cross between SMs at a fifth of that.  1024 x 1000, K = 2048: 9.5 us
-// with 128 columns and two CTAs, 10.6 us with 64 and no split; 256 x 2048, K = 768: 5.6 us with 64 columns and
+// share of the other CTAs' partial sums, which cross between SMs at a fifth of that.  1024 x 1000, K = 2048: 9.0 us
+// with 128 columns and two CTAs (9.5 when both were measured), 10.6 us with 64 and no split; 256 x 2048, K = 768: 5.6 us with 64 columns and
 // two, 7.6 us with 128 and four.  ways 0 if the tiles alone fill the SMs.
 inline void split_choice(bool glu, int cols, int M, int K, const int (&room)[4], int* ways, int* BN)
 {

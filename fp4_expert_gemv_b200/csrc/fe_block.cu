@@ -217,7 +217,7 @@ cudaError_t norm_bwd(const fe::NormBwdParams& q, bool vec, int sms, int* partial
 
 // ---- balance loss -------------------------------------------------------------------------
 
-fe_status check_balance(const float* logits, const uint8_t*, int64_t T, int E, int top_k)
+fe_status check_balance(const float* logits, int64_t T, int E, int top_k)
 {
     if (T < 0 || E < 1 || top_k < 1 || top_k > E || (T > 0 && !logits) || !aligned(logits, 4)) return FE_ERR_INVALID_ARG;
     if (E > fe::kBalMaxE || T > INT32_MAX / top_k) return FE_ERR_UNSUPPORTED;
@@ -658,9 +658,13 @@ fe_status fe_moe_block_norm(const void* r, int r_dtype, const void* y, const voi
     p.u = static_cast<uint16_t*>(u);
     const bool r32 = r_dtype == FE_DTYPE_F32;
     const cudaStream_t s = (cudaStream_t)stream;
-    // The streamed kernel pays from a few rows per group: at H = 2048 (four groups on each of 148 SMs) bf16 rows
-    // take 3.5 us with it and 3.4 without at T = 512, 8.7 and 10.3 at 2048, 24.6 and 38.5 at 8192; fp32
-    // rows 14.0 and 12.0 at 2048, 20.8 and 20.9 at 4096, 35.0 and 38.2 at 8192.
+    // The streamed kernel pays from a few rows per group.  With it and without, us:
+    //   H = 2048 (four groups on each of 148 SMs), bf16 rows: 3.5, 3.6 at one row per group, 5.0, 5.5 at two, 10.4, 13.5 at
+    //   four, 38.8, 64.0 at 24; fp32 rows: 15.3, 13.3 at four, 18.7, 18.5 at six, 30.7, 33.5 at twelve, 60, 63 at 24;
+    //   H = 512 (16 groups), bf16: 3.4, 3.6 at one, 4.6, 5.2 at two, 19.6, 30.9 at twelve; fp32: 13.7, 12.0 at four, 17.2,
+    //   16.8 at six, 30.4, 30.4 at twelve, 63.8, 57.5 at 24;  H = 4096 (two groups), bf16: 4.0, 3.4 at one, 6.0, 6.0 at two,
+    //   27, 42 at twelve; fp32: 21.8, 22.9 at six, 37, 42 at twelve.
+    // The rule does not look at H: narrow fp32 rows in large batches lose up to a tenth by it.
     NormRingPlan ring;
     const int sms = sm_count();
     if (sms < 1) return record_cuda(cudaErrorInvalidDevice, "device");
@@ -753,7 +757,7 @@ fe_status fe_moe_balance_loss(const float* logits, const int32_t* idx, const uin
                               float balance_coef, float z_coef, float* loss, int32_t* counts, int32_t* n_tokens,
                               void* workspace, size_t workspace_bytes, fe_stream_t stream)
 {
-    const fe_status st = check_balance(logits, mask, T, E, top_k);
+    const fe_status st = check_balance(logits, T, E, top_k);
     if (st != FE_OK) return st;
     if ((T > 0 && !idx) || !loss || !counts || !n_tokens || !aligned(idx, 4) || !aligned(loss, 4) ||
         !aligned(counts, 4) || !aligned(n_tokens, 4) || !aligned(workspace, 4))
@@ -815,7 +819,7 @@ fe_status fe_moe_balance_loss_backward(const float* logits, const int32_t* count
                                        float balance_coef, float z_coef, void* dlogits, int dlogits_dtype,
                                        fe_stream_t stream)
 {
-    const fe_status st = check_balance(logits, mask, T, E, top_k);
+    const fe_status st = check_balance(logits, T, E, top_k);
     if (st != FE_OK) return st;
     if (dlogits_dtype != FE_DTYPE_F32 && dlogits_dtype != FE_DTYPE_BF16) return FE_ERR_INVALID_ARG;
     if (T == 0) return FE_OK;
@@ -973,7 +977,9 @@ fe_status fe_moe_linear_backward(const void* dy, int64_t lddy, const void* x, in
         partials = used;
     }
     if (dx || dw) {
-        // dW [N][K] = dZ^T X (longest tiles first), dX [M][K] = dZ W: one launch
+        // dW [N][K] = dZ^T X (longest tiles first), dX [M][K] = dZ W: one launch of whole tiles.  Neither
+        // contraction is split: where there are fewer tiles than CTA pairs, a pair walks a tile's rows alone (dW of
+        // 16384 rows, N = K = 64: one tile, 48 us; N = 128, K = 2048: 50 us).
         fe::LinParams P{};
         Product prod[2];
         int n = 0;

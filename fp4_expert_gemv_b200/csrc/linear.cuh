@@ -9,11 +9,12 @@
 //     products of the next.  Either operand may lie along the contraction (rows of K) or across it
 //     (the gradients' transposed operands): only the boxes' order and two descriptor bits differ,
 //     nothing is transposed in memory.  One launch takes up to two products (dX = dZ W and dW = dZ^T X).
-//     16384 x 1536 at K = 2048 with swiglu: 70 us, 1470 TFLOP/s; dX and dW of 4096 rows 43 us.
+//     16384 x 1536 at K = 2048 with swiglu: 70 to 72 us, 1450 TFLOP/s; dX and dW of 4096 rows 39 us.  (All figures
+//     here: launches of one kind in a captured graph, operands in turn.)
 //   * linear_split_kernel, fewer tiles than SMs, bound by what an SM takes in: 128 x 64 or 128 x 128 tiles,
-//     the contraction split over a cluster.  64 x 2048 at K = 768: 4.1 us; 1024 x 1000 at K = 2048: 8.9 us.
+//     the contraction split over a cluster.  64 x 2048 at K = 768: 4.2 us; 1024 x 1000 at K = 2048: 9.0 us.
 //   * linear_skinny_kernel, 2 to 16 rows, and linear_rows_kernel, one row: bound by one pass over the
-//     weights.  1536 x 2048 with swiglu: 3.9 us for 16 rows, 2.8 us (2.2 TB/s) for one.
+//     weights.  1536 x 2048 with swiglu: 4.0 us for 16 rows, 2.8 us (2.2 TB/s) for one.
 //   * linear_dz_kernel, memory: dZ = dY act'(Z) and the column sums behind db.  4096 x 1536 with swiglu:
 //     7.2 us with the sums' launch.
 #pragma once
@@ -1023,7 +1024,11 @@ __global__ void __launch_bounds__(32 * kLinRowsWarps) linear_rows_kernel(LinRows
 
 // ---- a small batch ---------------------------------------------------------------------
 
-constexpr int kSkinnyMaxM = 16;   // N = 1536, K = 2048: 3.9 us at 16 rows (tiles 5.3), 8.8 at 32 (tiles 5.4): every CTA reads all of x
+// Rows to which the kernel below is taken.  Every CTA reads all of x, so that more rows are faster in tiles: N = 1536,
+// K = 2048 takes 4.0 us at 16 rows (tiles 5.0), 8.8 at 32 (tiles 5.4); N = 4096, K = 1024 4.0 at 16 (tiles 6.0), 3.0 at 2
+// (6.2).  A warp walks the contraction 512 of k at a time, so a long one is faster in tiles as well, which split it: N =
+// 512, K = 4096 takes 6.1 us at 16 rows (tiles 4.3) and 5.0 at 2 (tiles 4.1); the rule does not look at K.
+constexpr int kSkinnyMaxM = 16;
 
 FE_DEV void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {

@@ -50,7 +50,10 @@ struct NormBwdParams {
     float* part;              // [grid][3][H] column sums (dw_post, dw_pre, dgate per channel), or null
 };
 
-// 2^x and 1 / x to 2 ulp, one instruction each: no scaling around results below 2^-126, which are zero.
+// 2^x and 1 / x to 2 ulp, one instruction each: no scaling around results below 2^-126, which are zero.  exp(x) as
+// 2^(x log2 e) with one rounded product is off by |x| 2^-23 of itself besides (2^-16 at x = -87, the last one that
+// is not zero): a sigmoid far from 0 and a softmax's small p are rounded so by choice, what they are added to is
+// larger by as much, and a product in two parts would cost two more instructions an element.
 FE_DEV float ex2_ftz(float x)
 {
     float v;
@@ -645,8 +648,9 @@ __global__ void __launch_bounds__(512) block_norm_ring_kernel(NormParams p, int 
 // With e = D m, dw_post and a channel gate's gradient are column factors times the same sum of e over
 // rows.  The sums over rows stay in the registers of the thread that owns the column; one partial per
 // CTA, added in a fixed order by column_sum_kernel.
-// RING: rows of whole aligned 16-byte chunks and every operand there, through the ring; otherwise any width,
-// alignment and set of operands, straight from memory (the second walk finds them in L1), columns strided by the group's threads.
+// Two kernels: block_norm_backward_ring_kernel for rows of whole aligned 16-byte chunks with y, du and dr' there, up
+// to the width whose stages fit; block_norm_backward_any_kernel for any other width, alignment and set of
+// operands, straight from memory.
 template <bool R32, int GATE>
 __global__ void __launch_bounds__(512) block_norm_backward_ring_kernel(NormBwdParams q, int tpr, int stages)
 {
@@ -936,13 +940,13 @@ __global__ void __launch_bounds__(512) block_norm_backward_ring_kernel(NormBwdPa
     }
 }
 
-// A row's columns one at a time, t, t + tpr, ...: any width, alignment and set of operands.  The same sums and
-// the same two walks, over memory, four columns of a thread at a time; the second walk goes backwards, so
-// that the four it begins with are still held in registers (a whole row of up to 2048 columns), and the
-// rest of the row is found in L1.  The next row is asked for into L2 while this one is summed.  What bounds
-// it is issuing instructions, two bytes a load: a warp's columns lie 32 apart, so that one address serves
-// four of them (columns a row's threads apart took a third more time), and a batch within the row checks no
-// ends.  16384 x 1999 with a full gate takes 229 us, 1.7 TB/s; 1237 x 1999 29.9 us.  The sums over rows lie in
+// Any width, alignment and set of operands: the same sums and the same two walks, over memory.  A thread has four
+// columns 32 apart at a time (a warp 128 beside each other), the group's next batch lies 4 tpr columns further; the
+// second walk goes backwards, so that the four it begins with are still held in registers (a whole row of
+// up to 2048 columns), and the rest of the row is found in L1.  The next row is asked for into L2 while this
+// one is summed.  What bounds it is issuing instructions, two bytes a load: one address serves a thread's four
+// columns (columns a row's threads apart took a third more time), and a batch within the row checks no
+// ends.  16384 x 1999 with a full gate takes 224 us, 2.3 TB/s; 1237 x 1999 29.2 us.  The sums over rows lie in
 // shared memory, where each column has one thread per group.
 template <typename OT>
 FE_DEV float any_get(const OT* p, size_t i)
