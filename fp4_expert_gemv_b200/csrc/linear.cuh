@@ -206,7 +206,7 @@ FE_DEV void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read %0;" 
 
 // Bounded wait for phase `parity` of an mbarrier by a thread that suspends meanwhile: the products run
 // at the power limit, where polling warps cost clocks.
-FE_DEV bool lin_wait(uint32_t bar, uint32_t parity)
+FE_DEV bool lin_wait(uint32_t bar, uint32_t parity, unsigned long long limit_ns = kLinTimeoutNs)
 {
     unsigned long long t0 = 0;
     for (int it = 0;; ++it) {
@@ -218,12 +218,15 @@ FE_DEV bool lin_wait(uint32_t bar, uint32_t parity)
             : "memory");
         if (ok) return true;
         if (it == 0) t0 = globaltimer_ns();
-        else if (globaltimer_ns() - t0 > kLinTimeoutNs) return false;
+        else if (globaltimer_ns() - t0 > limit_ns) return false;
     }
 }
 
 // The same by every lane of a warp, with one answer.
-FE_DEV bool lin_wait_warp(uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, lin_wait(bar, parity)); }
+FE_DEV bool lin_wait_warp(uint32_t bar, uint32_t parity, unsigned long long limit_ns = kLinTimeoutNs)
+{
+    return __all_sync(0xffffffffu, lin_wait(bar, parity, limit_ns));
+}
 
 // One lane of a converged warp.  The producer and MMA warps run their loops with every lane and pick
 // the issuing one only around the instruction, so that addresses and descriptors stay warp-uniform: a
@@ -593,7 +596,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kLinThreads, 1)
                 };
                 int slot = 0;
                 if (has_res && half < chunks) slot = fetch(half);
-                if (!lin_wait_warp(accfull(acc), (done / 2) & 1)) *abort = 1;
+                // a whole tile's products: a dW's run over every row, some 200 ns per k step
+                if (!lin_wait_warp(accfull(acc), (done / 2) & 1, kLinTimeoutNs + 1000ull * ((p.K + 63) / 64))) *abort = 1;
                 stop = __any_sync(0xffffffffu, *abort != 0);
                 tc_fence_after();
                 const uint32_t t0 = tmem + ((uint32_t)(32 * quarter) << 16) + kAccCol * acc;

@@ -125,3 +125,21 @@ def test_the_weights_gradient_over_more_rows(M, N, K):
     want = (dy.double() @ w.double()).to(bf)
     assert torch.equal(dx[:PERIOD], want) and torch.equal(dx[-PERIOD:], want) and (want != 0).any()
     assert fe.op_status() == (fe.FE_OK, 0)
+
+
+def test_one_tile_over_a_billion_rows():
+    """dW of one tile whose k steps take a single pair of CTAs seconds: the epilogue's wait lasts as long.  All rows are
+    zero but a few, so that every sum is exact."""
+    import fp4_expert_gemv_b200 as fe
+    M, N, K = 1_200_000_000, 8, 8
+    x = torch.zeros(M, K, dtype=bf, device="cuda")
+    dy = torch.zeros(M, N, dtype=bf, device="cuda")
+    w = torch.ones(N, K, dtype=bf, device="cuda")
+    at = torch.tensor([0, 1, 63, 64, 12345, M // 2, M - 2, M - 1], device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x[at] = torch.randint(-3, 4, (8, K), generator=g, device="cuda").to(bf)
+    dy[at] = torch.randint(-3, 4, (8, N), generator=g, device="cuda").to(bf)
+    _, dw, db = fe.linear_backward(dy, x, w, need_dx=False)
+    assert torch.equal(dw.double(), dy[at].double().t() @ x[at].double())
+    assert torch.equal(db.double(), dy[at].double().sum(0))
+    assert fe.op_status() == (fe.FE_OK, 0)
